@@ -70,10 +70,10 @@ enum { WSL_W_BF16 = 0, WSL_W_NF4 = 1 };
 /* Output formats. */
 enum { WSL_OUT_F32 = 0, WSL_OUT_BF16 = 1 };
 
-/* Bits OR-ed into nf4_pack's optional device status word. */
-#define WSL_STATUS_NONFINITE 1u   /* a group held a NaN or an infinity */
+/* Bits OR-ed into a call's optional device status word. */
+#define WSL_STATUS_NONFINITE 1u   /* a group (or cache row) held a NaN or an infinity; verify_drafts: no weights to sample */
 #define WSL_STATUS_OVERFLOW  2u   /* a group's absmax rounds to +inf in fp16 (>= 65520) */
-#define WSL_STATUS_INDEX     4u   /* nf4_embed_rows: a requested row index was outside the matrix */
+#define WSL_STATUS_INDEX     4u   /* a row index, cache slot, page, length or draft was out of range */
 #define WSL_STATUS_SWEEP_TIMEOUT 8u   /* linear_gemv_sweep: a stage barrier waited past its bound */
 #define WSL_STATUS_DESCRIPTOR    16u  /* linear_gemv_sweep: a device stage descriptor was invalid (skipped) */
 
@@ -347,6 +347,134 @@ int linear_gemm_streamed(int wfmt, int64_t count, const void *const *h_w, const 
                          const void *const *d_x, int64_t m, int64_t ldx, void *const *d_y, int ofmt, int64_t ldy,
                          void *d_ws, size_t ws_bytes, void *const *d_slot, size_t slot_bytes,
                          void *copy_stream, void *compute_stream, void *const *events, int flags);
+
+/* Formats of a key-value cache. */
+enum { WSL_KV_BF16 = 0, WSL_KV_E4M3 = 1 };
+
+/*
+ * A paged key-value cache of one layer, described by the caller (host struct, read before a
+ * call returns).  Keys and values are [n_pages][n_kv][page_size][head_dim] each, with the
+ * strides given here (the same for both): a token's slot is page * page_size + its place in
+ * the page.  A sequence's tokens lie in the pages its row of a block table names, in order.
+ *   (deep-fold README, "Метод" table: a decode step reads only the valid prefix of the cache;
+ *   IPE page, "What is built": a decode step indexes preallocated buffers.)
+ * fmt        WSL_KV_BF16, or WSL_KV_E4M3: 8-bit codes (1 sign, 4 exponent, 3 fraction bits, no
+ *            infinities) with one power of two per token and kv head: with a = max|x| over the
+ *            head_dim elements, e is the least integer >= -110 with a <= 448 * 2^e, a code is
+ *            the e4m3 number nearest to x * 2^-e (ties to even), its value code * 2^e, and the
+ *            scale byte e + 127.  A row that holds a NaN or an infinity is kept as NaN codes
+ *            with scale byte 127.
+ * k, v       device, 16-byte aligned.
+ * k_exp, v_exp   device uint8 [n_pages][n_kv][page_size], contiguous (E4M3; else ignored).
+ * n_pages    1 .. 2^31 - 1.   page_size 1 .. 2^30, any number.   n_kv 1 .. 2^20.
+ * head_dim   16 .. 256, a multiple of 16.
+ * page_stride, head_stride, token_stride   in elements, >= head_dim, multiples of 16 bytes.
+ */
+typedef struct wsl_kv_cache {
+    void *k, *v;
+    uint8_t *k_exp, *v_exp;
+    int64_t fmt;
+    int64_t n_pages, n_kv, page_size, head_dim;
+    int64_t page_stride, head_stride, token_stride;
+} wsl_kv_cache;
+
+/*
+ * kv_cache_write -- put the keys and values of count tokens into their slots, rounded to bf16
+ * (to nearest even) or quantised as above.
+ * d_k, d_v   device [count][ld_k] / [count][ld_v] of xfmt (WSL_OUT_F32 as linear_gemv gives
+ *            them, or WSL_OUT_BF16): n_kv * head_dim elements a token, heads in order; 16-byte
+ *            aligned, ld_k, ld_v >= n_kv * head_dim and multiples of 16 bytes (so views of a
+ *            fused projection's output serve).
+ * count      >= 0 (0 launches nothing); count * n_kv <= 2^26.
+ * d_slots    device int64 [count]; -1: the token is not kept.  Two tokens of one call must not
+ *            name the same slot.
+ * d_status   device uint32 or NULL: WSL_STATUS_INDEX is ORed in if a slot is outside the cache
+ *            (nothing is written for it), WSL_STATUS_NONFINITE if an E4M3 row held a NaN or an
+ *            infinity.
+ */
+int kv_cache_write(const wsl_kv_cache *h_cache, const void *d_k, const void *d_v, int xfmt, int64_t count,
+                   int64_t ld_k, int64_t ld_v, const int64_t *d_slots, uint32_t *d_status, void *stream);
+
+/*
+ * kv_cache_read -- the keys and values held in count slots (repeats allowed), as bf16 or fp32:
+ * exact in both (a row whose largest element rounded up to 2^128 holds an infinity there, as its
+ * bf16 rounding would).  Arguments as for kv_cache_write, d_k and d_v written in ofmt.  Slot -1 gives
+ * zeros; a slot outside the cache gives zeros and WSL_STATUS_INDEX.
+ */
+int kv_cache_read(const wsl_kv_cache *h_cache, const int64_t *d_slots, int64_t count, void *d_k, void *d_v, int ofmt,
+                  int64_t ld_k, int64_t ld_v, uint32_t *d_status, void *stream);
+
+/*
+ * attn_decode -- attention of the q_len newest tokens of each of n_seq sequences over the
+ * sequence's cached keys and values (its own included: write them first).
+ *   (TCPP README, "Quickstart": a line of drafted tokens is scored in one sweep; deep-fold
+ *   README, "Метод" table: decode reads the valid prefix of the cache.)
+ * For sequence b with L = d_kv_lens[b] tokens, query i stands at position p = L - q_len + i and
+ * sees the tokens t <= p (with window > 0 only t > p - window):
+ *   out = sum_t exp(s_t - max s) V_t / sum_t exp(s_t - max s),   s_t = scale * <q, K_t>,
+ * head h reading kv head h / (n_heads / n_kv).  A query that sees nothing (p < 0) gives zeros.
+ * Tokens a query does not see have no part in it, whatever their slots hold.
+ * d_q        device [n_seq * q_len][ld_q] of qfmt (WSL_OUT_F32 or WSL_OUT_BF16), n_heads *
+ *            head_dim elements a token; 16-byte aligned, ld_q a multiple of 16 bytes.
+ * n_seq      0 .. 65535 (0 launches nothing).  q_len 1 .. 256.  n_heads a multiple of n_kv.
+ *            q_len * n_heads / n_kv <= 2^16, q_len * n_heads <= 2^24.
+ * d_block_table   device int32 [n_seq][ld_table]: page of token t of a sequence at [t / page_size];
+ *            pages_per_seq (1 .. ld_table) entries of a row may be read.
+ * d_kv_lens  device int32 [n_seq]: read by the kernels only, so a captured call goes on with
+ *            lengths that grow.  One outside [0, pages_per_seq * page_size] is clamped to it
+ *            and reported; so is, as if it were not seen, a token whose page is outside [0, n_pages).
+ * scale      the factor of the scores.  window >= 0 (0: none).
+ * d_out      device [n_seq * q_len][ld_out] of ofmt, 16-byte aligned, ld_out a multiple of 16 bytes.
+ * d_lse      device fp32 [n_seq][q_len][n_heads] or NULL: log sum_t exp(s_t), -infinity where
+ *            nothing is seen (for joining with attention over tokens kept elsewhere).
+ * d_ws       device workspace, 16-byte aligned, of attn_decode_workspace_bytes (else WSL_E_RANGE):
+ *            the length is split over the chip by the actual lengths, and parts of one head are
+ *            joined by a second launch.  Its contents on entry do not matter.  Calls that share
+ *            a workspace must not overlap.
+ * d_status   device uint32 or NULL: WSL_STATUS_INDEX as above.
+ * Scores, maxima, sums and products with V are held in fp32; the weights enter the matrix
+ * instructions as two bf16 numbers (16 bits), fp32 queries as three (24 bits).  Deterministic.
+ */
+size_t attn_decode_workspace_bytes(int qfmt, int64_t n_seq, int64_t q_len, int64_t n_heads, int64_t n_kv,
+                                   int64_t head_dim, int64_t pages_per_seq, int64_t page_size);
+int attn_decode(const wsl_kv_cache *h_cache, const void *d_q, int qfmt, int64_t n_seq, int64_t q_len, int64_t n_heads,
+                int64_t ld_q, const int32_t *d_block_table, int64_t ld_table, int64_t pages_per_seq,
+                const int32_t *d_kv_lens, float scale, int64_t window, void *d_out, int ofmt, int64_t ld_out,
+                float *d_lse, void *d_ws, size_t ws_bytes, uint32_t *d_status, void *stream);
+
+/*
+ * verify_drafts -- which drafted tokens the target's probabilities let stand, and the token that
+ * follows them, from given random numbers.
+ *   (TCPP README, "Quickstart": batch verification scores every position in one sweep; Tarfa 2,
+ *   "Speculative decoding".)
+ * For each of n_seq sequences with n drafts x_0 .. x_{n-1}, rows p_0 .. p_n of the target, rows
+ * q_0 .. q_{n-1} of the drafter and numbers u_0 .. u_width:
+ *   draft i stands iff all before it do and u_i * q_i(x_i) < p_i(x_i); r = how many stand;
+ *   w_j = max(p_r(j) - q_r(j), 0) if r < n, else max(p_n(j), 0); if they sum to 0, max(p_r(j), 0);
+ *   the next token is the least j with w_0 + .. + w_j > u_width * sum w.
+ * With u uniform in [0, 1) and x_i drawn from q_i, every token has the target's distribution.
+ * All of it in 64 bits.  NaN and negative weights count as zero; where no sum passes (u >= 1 or
+ * NaN) the last entry with a weight is taken.
+ * d_p        device [n_seq][width + 1][ld_p] of pfmt (WSL_OUT_F32 or WSL_OUT_BF16), the first
+ *            vocab of each row used; aligned to its element.
+ * d_q        device [n_seq][width][ld_q] of pfmt, or NULL: the drafter was certain (q_i = 1 at x_i).
+ * n_seq      0 .. 65535 (0 launches nothing).  width 0 .. 64 (0: p_0 is sampled).
+ * vocab      1 .. 2^30.
+ * d_drafts   device int32 [n_seq][width].  A draft outside [0, vocab) falls (WSL_STATUS_INDEX).
+ * d_n_drafts device int32 [n_seq] or NULL (width for all): n, clamped to [0, width].
+ * d_u        device fp32 [n_seq][width + 1].
+ * d_accepted device int32 [n_seq]: r.   d_tokens device int32 [n_seq][width + 1]: the r drafts
+ *            that stand, the next token, then -1.  If the weights do not sum to a positive finite
+ *            number the next token is -1 (WSL_STATUS_NONFINITE).
+ * d_ws       device workspace, 8-byte aligned, of verify_drafts_workspace_bytes (else WSL_E_RANGE).
+ *            Its contents on entry do not matter.  Calls that share a workspace must not overlap.
+ */
+#define WSL_VERIFY_MAX_DRAFTS 64
+size_t verify_drafts_workspace_bytes(int64_t n_seq, int64_t vocab);
+int verify_drafts(const void *d_p, const void *d_q, int pfmt, int64_t n_seq, int64_t width, int64_t vocab,
+                  int64_t ld_p, int64_t ld_q, const int32_t *d_drafts, const int32_t *d_n_drafts, const float *d_u,
+                  int32_t *d_accepted, int32_t *d_tokens, void *d_ws, size_t ws_bytes, uint32_t *d_status,
+                  void *stream);
 
 /*
  * wsl_stream_read -- measurement aid, not part of the linear path: a read-only

@@ -12,6 +12,8 @@ Entry points (same names as the C ABI):
   linear_gemv, linear_gemm, linear_gemm_workspace_bytes, nf4_embed_rows, wsl_strerror;
   linear_gemm_noalloc; linear_gemv_multi; GemvSweep (linear_gemv_sweep,
   linear_gemv_sweep_workspace_bytes);
+  KVCache (wsl_kv_cache) with kv_cache_write, kv_cache_read, attn_decode and
+  attn_decode_workspace_bytes; verify_drafts and verify_drafts_workspace_bytes;
   stream_read (wsl_stream_read); CopyRing.gemv / CopyRing.gemm (linear_gemv_streamed /
   linear_gemm_streamed, weights streamed from page-locked host memory, see to_pinned).
 """
@@ -27,14 +29,19 @@ WSL_W_BF16 = 0
 WSL_W_NF4 = 1
 WSL_OUT_F32 = 0
 WSL_OUT_BF16 = 1
+WSL_KV_BF16 = 0
+WSL_KV_E4M3 = 1
 WSL_STATUS_NONFINITE = 1
 WSL_STATUS_OVERFLOW = 2
+WSL_STATUS_INDEX = 4
 
 EXPORTED = [
     "nf4_packed_bytes", "nf4_codebook", "nf4_pack", "nf4_dequant_tile", "linear_gemv",
     "linear_gemm_workspace_bytes", "linear_gemm", "nf4_embed_rows", "linear_gemv_streamed",
     "linear_gemm_streamed", "wsl_stream_read", "wsl_strerror", "linear_gemm_noalloc",
     "linear_gemv_sweep_workspace_bytes", "linear_gemv_sweep", "linear_gemv_multi",
+    "kv_cache_write", "kv_cache_read", "attn_decode_workspace_bytes", "attn_decode",
+    "verify_drafts_workspace_bytes", "verify_drafts",
 ]
 WSL_STATUS_SWEEP_TIMEOUT = 8
 WSL_STATUS_DESCRIPTOR = 16
@@ -93,6 +100,20 @@ def lib():
     L.linear_gemm_streamed.argtypes = [ctypes.c_int, i64, vp, vp, vp, vp, i64, i64, vp, ctypes.c_int, i64, vp, sz, vp,
                                        sz, vp, vp, vp, ctypes.c_int]
     L.linear_gemm_streamed.restype = ctypes.c_int
+    ci = ctypes.c_int
+    L.kv_cache_write.argtypes = [vp, vp, vp, ci, i64, i64, i64, vp, vp, vp]
+    L.kv_cache_write.restype = ci
+    L.kv_cache_read.argtypes = [vp, vp, i64, vp, vp, ci, i64, i64, vp, vp]
+    L.kv_cache_read.restype = ci
+    L.attn_decode_workspace_bytes.argtypes = [ci] + [i64] * 7
+    L.attn_decode_workspace_bytes.restype = sz
+    L.attn_decode.argtypes = [vp, vp, ci, i64, i64, i64, i64, vp, i64, i64, vp, ctypes.c_float, i64, vp, ci, i64, vp,
+                              vp, sz, vp, vp]
+    L.attn_decode.restype = ci
+    L.verify_drafts_workspace_bytes.argtypes = [i64, i64]
+    L.verify_drafts_workspace_bytes.restype = sz
+    L.verify_drafts.argtypes = [vp, vp, ci, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp, sz, vp, vp]
+    L.verify_drafts.restype = ci
     L.wsl_stream_read.argtypes = [vp, sz, vp, vp]
     L.wsl_stream_read.restype = ctypes.c_int
     L.wsl_strerror.argtypes = [ctypes.c_int]
@@ -371,6 +392,282 @@ def linear_gemv_multi(mats, stream=None):
     rc = lib().linear_gemv_multi(WSL_W_BF16, len(mats), ctypes.byref(h), _stream(stream))
     _check(rc, "linear_gemv_multi")
     return ys
+
+
+# ---------------------------------------------------------------- key-value cache, attention, drafts
+class WslKvCache(ctypes.Structure):
+    """struct wsl_kv_cache of the C ABI."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_exp", ctypes.c_void_p),
+                ("v_exp", ctypes.c_void_p), ("fmt", ctypes.c_int64), ("n_pages", ctypes.c_int64),
+                ("n_kv", ctypes.c_int64), ("page_size", ctypes.c_int64), ("head_dim", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64)]
+
+
+class KVCache:
+    """The handle of one layer's paged key-value cache (wsl_kv_cache), over tensors that the caller owns.
+
+    k, v: [n_pages][n_kv][page_size][head_dim] of bfloat16, or of float8_e4m3fn with k_exp and
+    v_exp, uint8 [n_pages][n_kv][page_size] (see include/wsl.h for the 8-bit form).  k and v may
+    be views with other orders of pages, heads and tokens (a transposed [page][token][head] pool,
+    the halves of one tensor), both with the same strides and head_dim contiguous.  The handle
+    keeps the tensors alive."""
+
+    def __init__(self, k, v, k_exp=None, v_exp=None):
+        import torch
+        e4m3 = k.dtype == torch.float8_e4m3fn
+        dtype = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+        _require(k, "k", (dtype,), ndim=4)
+        _require(v, "v", (dtype,), device=k.device, ndim=4)
+        if v.shape != k.shape or v.stride() != k.stride():
+            raise ValueError(f"k and v differ: {tuple(k.shape)} {k.stride()}, {tuple(v.shape)} {v.stride()}")
+        if e4m3:
+            if k_exp is None or v_exp is None:
+                raise ValueError("an e4m3 cache needs k_exp and v_exp")
+            for t, name in ((k_exp, "k_exp"), (v_exp, "v_exp")):
+                _require(t, name, (torch.uint8,), device=k.device, contiguous=True)
+                if t.shape != k.shape[:3]:
+                    raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(k.shape[:3])}")
+        elif k_exp is not None or v_exp is not None:
+            raise ValueError("a bf16 cache has no scale bytes")
+        n_pages, n_kv, page_size, dim = k.shape
+        # a dimension of one entry is never stepped over: any stride serves
+        strides = [s if n > 1 else -(-dim // 16) * 16 for s, n in zip(k.stride()[:3], k.shape[:3])]
+        self.tensors = (k, v, k_exp, v_exp)
+        self.device = k.device
+        self.fmt = WSL_KV_E4M3 if e4m3 else WSL_KV_BF16
+        self.n_pages, self.n_kv, self.page_size, self.head_dim = n_pages, n_kv, page_size, dim
+        self.desc = WslKvCache(k.data_ptr(), v.data_ptr(), k_exp.data_ptr() if e4m3 else None,
+                               v_exp.data_ptr() if e4m3 else None, self.fmt, n_pages, n_kv, page_size, dim, *strides)
+        self.ref = ctypes.byref(self.desc)
+
+    @classmethod
+    def empty(cls, n_pages, n_kv, page_size, head_dim, fmt=WSL_KV_BF16, device="cuda"):
+        """A cache over new tensors (uninitialised: a slot is read only once it has been written)."""
+        import torch
+        shape = (int(n_pages), int(n_kv), int(page_size), int(head_dim))
+        if fmt not in (WSL_KV_BF16, WSL_KV_E4M3):
+            raise ValueError(f"unknown cache format {fmt}")
+        dtype = torch.float8_e4m3fn if fmt == WSL_KV_E4M3 else torch.bfloat16
+        k, v = (torch.empty(shape, dtype=dtype, device=device) for _ in range(2))
+        if fmt == WSL_KV_BF16:
+            return cls(k, v)
+        return cls(k, v, *(torch.empty(shape[:3], dtype=torch.uint8, device=device) for _ in range(2)))
+
+
+def _float_format(t, name):
+    """WSL_OUT_F32 or WSL_OUT_BF16 of a tensor."""
+    import torch
+    if t.dtype == torch.bfloat16:
+        return WSL_OUT_BF16
+    if t.dtype == torch.float32:
+        return WSL_OUT_F32
+    raise ValueError(f"{name}: dtype {t.dtype} is neither float32 nor bfloat16")
+
+
+def _float_dtype(fmt):
+    import torch
+    if fmt not in (WSL_OUT_F32, WSL_OUT_BF16):
+        raise ValueError(f"unknown element format {fmt}")
+    return torch.float32 if fmt == WSL_OUT_F32 else torch.bfloat16
+
+
+def _new(shape, dtype, device, stream):
+    """A new tensor whose memory belongs to the stream that the call runs on."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _status(status, device):
+    import torch
+    if status is not None:
+        _require(status, "status", (torch.int32, torch.uint32), device=device)
+        if status.numel() < 1:
+            raise ValueError("status: empty")
+
+
+def _head_rows(t, name, device, shape):
+    """Check a [..., heads, head_dim] tensor whose leading dimensions step as one (a view of a wider
+    row of tokens serves); returns the elements from token to token."""
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    st = t.stride()
+    heads, dim = shape[-2:]
+    if (dim > 1 and st[-1] != 1) or (heads > 1 and st[-2] != dim):
+        raise ValueError(f"{name}: heads and their elements must be contiguous (strides {st})")
+    if len(shape) == 4:
+        if shape[1] == 1:
+            return st[0] if shape[0] > 1 else heads * dim
+        if shape[0] > 1 and st[0] != shape[1] * st[1]:
+            raise ValueError(f"{name}: the first two dimensions must step as one (strides {st})")
+        return st[1]
+    return st[0] if shape[0] > 1 else heads * dim
+
+
+def _slots(cache, slots):
+    import torch
+    _require(slots, "slots", (torch.int64,), device=cache.device, contiguous=True, ndim=1)
+    return int(slots.numel())
+
+
+def kv_cache_write(cache, k, v, slots, status=None, stream=None):
+    """Put k, v [count][n_kv][head_dim] (fp32 or bf16; views of a fused projection serve) into the
+    slots (int64 [count]: page * page_size + place, -1 for none) of a KVCache."""
+    count = _slots(cache, slots)
+    shape = (count, cache.n_kv, cache.head_dim)
+    xfmt = _float_format(k, "k")
+    if v.dtype != k.dtype:
+        raise ValueError(f"v: dtype {v.dtype}, k has {k.dtype}")
+    ld_k, ld_v = _head_rows(k, "k", cache.device, shape), _head_rows(v, "v", cache.device, shape)
+    _status(status, cache.device)
+    rc = lib().kv_cache_write(cache.ref, k.data_ptr(), v.data_ptr(), xfmt, count, ld_k, ld_v, slots.data_ptr(),
+                              _ptr(status), _stream(stream))
+    _check(rc, "kv_cache_write")
+
+
+def kv_cache_read(cache, slots, k=None, v=None, ofmt=WSL_OUT_BF16, status=None, stream=None):
+    """The keys and values held in slots, [count][n_kv][head_dim] each of ofmt's type."""
+    count = _slots(cache, slots)
+    shape, dtype = (count, cache.n_kv, cache.head_dim), _float_dtype(ofmt)
+    if k is None:
+        k = _new(shape, dtype, cache.device, stream)
+    if v is None:
+        v = _new(shape, dtype, cache.device, stream)
+    if k.dtype != dtype or v.dtype != dtype:
+        raise ValueError(f"k, v: dtypes {k.dtype}, {v.dtype}, expected {dtype}")
+    ld_k, ld_v = _head_rows(k, "k", cache.device, shape), _head_rows(v, "v", cache.device, shape)
+    _status(status, cache.device)
+    rc = lib().kv_cache_read(cache.ref, slots.data_ptr(), count, k.data_ptr(), v.data_ptr(), int(ofmt), ld_k, ld_v,
+                             _ptr(status), _stream(stream))
+    _check(rc, "kv_cache_read")
+    return k, v
+
+
+def attn_decode_workspace_bytes(qfmt, n_seq, q_len, n_heads, n_kv, head_dim, pages_per_seq, page_size):
+    return int(lib().attn_decode_workspace_bytes(int(qfmt), int(n_seq), int(q_len), int(n_heads), int(n_kv),
+                                                 int(head_dim), int(pages_per_seq), int(page_size)))
+
+
+def attn_decode(cache, q, block_table, kv_lens, scale=None, window=0, out=None, ofmt=None, lse=None, workspace=None,
+                status=None, stream=None):
+    """Attention of each sequence's q_len newest tokens over its cached tokens (their own included).
+
+    q: [n_seq][q_len][n_heads][head_dim], fp32 or bf16; block_table: int32 [n_seq][pages];
+    kv_lens: int32 [n_seq]; scale: 1 / sqrt(head_dim) unless given; window: the last positions a
+    query sees, 0 for all; ofmt: q's type unless given; lse: fp32 [n_seq][q_len][n_heads] to be
+    written; workspace: a device tensor of attn_decode_workspace_bytes (allocated unless given)."""
+    import torch
+    if q.dim() != 4:
+        raise ValueError(f"q: expected 4 dimensions, got shape {tuple(q.shape)}")
+    n_seq, q_len, n_heads, dim = shape = tuple(q.shape)
+    dev = cache.device
+    qfmt = _float_format(q, "q")
+    ld_q = _head_rows(q, "q", dev, (n_seq, q_len, n_heads, cache.head_dim))
+    _require(block_table, "block_table", (torch.int32,), device=dev, ndim=2)
+    _require(kv_lens, "kv_lens", (torch.int32,), device=dev, contiguous=True, ndim=1)
+    pages = block_table.shape[1]
+    if block_table.shape[0] != n_seq or kv_lens.shape[0] != n_seq:
+        raise ValueError(f"{n_seq} sequences, block_table {tuple(block_table.shape)}, kv_lens {tuple(kv_lens.shape)}")
+    ofmt = (qfmt if out is None else _float_format(out, "out")) if ofmt is None else int(ofmt)
+    if out is None:
+        out = _new(shape, _float_dtype(ofmt), dev, stream)
+    elif out.dtype != _float_dtype(ofmt):
+        raise ValueError(f"out: dtype {out.dtype}, expected {_float_dtype(ofmt)}")
+    ld_out = _head_rows(out, "out", dev, shape)
+    if lse is not None:
+        _require(lse, "lse", (torch.float32,), device=dev, contiguous=True)
+        if tuple(lse.shape) != shape[:3]:
+            raise ValueError(f"lse: shape {tuple(lse.shape)}, expected {shape[:3]}")
+    _status(status, dev)
+    L = lib()
+    if workspace is None:
+        need = L.attn_decode_workspace_bytes(qfmt, n_seq, q_len, n_heads, cache.n_kv, dim, pages, cache.page_size)
+        ws_bytes = need
+        if need:
+            workspace = _new(need, torch.uint8, dev, stream)
+    else:
+        _require(workspace, "workspace", (workspace.dtype,), device=dev, contiguous=True)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    rc = L.attn_decode(cache.ref, q.data_ptr(), qfmt, n_seq, q_len, n_heads, ld_q, block_table.data_ptr(),
+                       block_table.stride(0) if n_seq > 1 else pages, pages, kv_lens.data_ptr(),
+                       dim ** -0.5 if scale is None else float(scale), int(window), out.data_ptr(), ofmt, ld_out,
+                       _ptr(lse), _ptr(workspace), ws_bytes, _ptr(status), _stream(stream))
+    _check(rc, "attn_decode")
+    return out
+
+
+def verify_drafts_workspace_bytes(n_seq, vocab):
+    return int(lib().verify_drafts_workspace_bytes(int(n_seq), int(vocab)))
+
+
+def _prob_rows(t, name, lead, vocab):
+    """Check probability rows [n_seq][rows][vocab]; returns the elements from row to row."""
+    if t.dim() != 3 or tuple(t.shape) != (*lead, vocab):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(*lead, vocab)}")
+    st = t.stride()
+    if vocab > 1 and st[2] != 1:
+        raise ValueError(f"{name}: last dimension must have stride 1 (got strides {st})")
+    ld = st[1] if lead[1] > 1 else (st[0] if lead[0] > 1 else vocab)
+    if lead[0] > 1 and st[0] != lead[1] * ld:
+        raise ValueError(f"{name}: the first two dimensions must step as one (strides {st})")
+    return ld
+
+
+def verify_drafts(p, q, drafts, u, n_drafts=None, accepted=None, tokens=None, workspace=None, status=None,
+                  stream=None):
+    """Which drafts stand, and the token after them, from given random numbers.
+
+    p: [n_seq][width + 1][vocab] target probabilities, q: [n_seq][width][vocab] the drafter's, or
+    None where each draft was certain (fp32 or bf16, the same); drafts: int32 [n_seq][width]; u:
+    fp32 [n_seq][width + 1] in [0, 1); n_drafts: int32 [n_seq], width unless given.  Returns
+    (accepted int32 [n_seq], tokens int32 [n_seq][width + 1]: the drafts that stand, the next
+    token, -1s)."""
+    import torch
+    if p.dim() != 3 or not p.is_cuda:
+        raise ValueError(f"p: expected a GPU tensor of 3 dimensions, got shape {tuple(p.shape)} on {p.device}")
+    dev = p.device
+    n_seq, rows, vocab = p.shape
+    width = rows - 1
+    if width < 0:
+        raise ValueError("p: no rows")
+    pfmt = _float_format(p, "p")
+    ld_p, ld_q = _prob_rows(p, "p", (n_seq, rows), vocab), 0
+    if q is not None and width:
+        _require(q, "q", (p.dtype,), device=dev)
+        ld_q = _prob_rows(q, "q", (n_seq, width), vocab)
+    for t, name, dtype, shape in ((drafts, "drafts", torch.int32, (n_seq, width)), (u, "u", torch.float32, (n_seq, rows)),
+                                  (n_drafts, "n_drafts", torch.int32, (n_seq,)),
+                                  (accepted, "accepted", torch.int32, (n_seq,)),
+                                  (tokens, "tokens", torch.int32, (n_seq, rows))):
+        if t is None:
+            if name in ("drafts", "u"):
+                raise ValueError(f"{name}: missing")
+            continue
+        _require(t, name, (dtype,), device=dev, contiguous=True)
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    _status(status, dev)
+    if accepted is None:
+        accepted = _new((n_seq,), torch.int32, dev, stream)
+    if tokens is None:
+        tokens = _new((n_seq, rows), torch.int32, dev, stream)
+    L = lib()
+    if workspace is None:
+        ws_bytes = L.verify_drafts_workspace_bytes(n_seq, vocab)
+        if ws_bytes:
+            workspace = _new(ws_bytes, torch.uint8, dev, stream)
+    else:
+        _require(workspace, "workspace", (workspace.dtype,), device=dev, contiguous=True)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    rc = L.verify_drafts(p.data_ptr(), q.data_ptr() if ld_q else None, pfmt, n_seq, width, vocab, ld_p, ld_q,
+                         drafts.data_ptr(), _ptr(n_drafts), u.data_ptr(), accepted.data_ptr(), tokens.data_ptr(),
+                         _ptr(workspace), ws_bytes, _ptr(status), _stream(stream))
+    _check(rc, "verify_drafts")
+    return accepted, tokens
 
 
 def stream_read(buf, sink, stream=None):

@@ -14,7 +14,8 @@ CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libwsl.so")
 
-HIP_SOURCES = ["api.hip", "pack.hip", "gemv.hip", "gemm.hip", "embed.hip", "ring.hip", "probe.hip"]
+HIP_SOURCES = ["api.hip", "pack.hip", "gemv.hip", "gemm.hip", "embed.hip", "ring.hip", "probe.hip", "kvcache.hip",
+               "attn.hip", "attn_bf16.hip", "attn_e4m3.hip", "verify.hip"]
 CXX_SOURCES = ["validate.cpp"]
 
 HIP_FLAGS = [

@@ -22,6 +22,19 @@ int launch_gemm_nf4(const void *w, int64_t n_out, int64_t k, const void *x, int6
 size_t gemm_ws_bytes(int wfmt, int64_t n_out, int64_t k, int64_t m);
 int launch_gemm_noalloc(int wfmt, const void *w, int64_t n_out, int64_t k, const void *x, int64_t m, int64_t ldx,
                         void *y, int ofmt, int64_t ldy, hipStream_t s);
+int launch_kv_write(const wsl_kv_cache *c, const void *k, const void *v, int xfmt, int64_t count, int64_t ld_k,
+                    int64_t ld_v, const int64_t *slots, uint32_t *status, hipStream_t s);
+int launch_kv_read(const wsl_kv_cache *c, const int64_t *slots, int64_t count, void *k, void *v, int ofmt,
+                   int64_t ld_k, int64_t ld_v, uint32_t *status, hipStream_t s);
+size_t attn_ws_bytes(int qfmt, int64_t n_seq, int64_t rows, int64_t n_kv, int64_t head_dim, int64_t capacity);
+int launch_attn(const wsl_kv_cache *c, const void *q, int qfmt, int64_t n_seq, int64_t q_len, int64_t n_heads,
+                int64_t ld_q, const int32_t *table, int64_t ld_table, int64_t pages_per_seq, const int32_t *lens,
+                float scale, int64_t window, void *out, int ofmt, int64_t ld_out, float *lse, void *ws,
+                uint32_t *status, hipStream_t s);
+size_t verify_ws_bytes(int64_t n_seq, int64_t vocab);
+int launch_verify(const void *p, const void *q, int pfmt, int64_t n_seq, int64_t width, int64_t vocab, int64_t ld_p,
+                  int64_t ld_q, const int32_t *drafts, const int32_t *n_drafts, const float *u, int32_t *accepted,
+                  int32_t *tokens, void *ws, uint32_t *status, hipStream_t s);
 int check_pinned(int64_t count, const void *const *h_w);
 int ring_gemv(int wfmt, int64_t count, const void *const *h_w, const int64_t *n_out, const int64_t *k,
               const void *const *x, float *const *y, void *const *slot, hipStream_t copy, hipStream_t compute,
@@ -178,6 +191,66 @@ int linear_gemm_streamed(int wfmt, int64_t count, const void *const *h_w, const 
     if ((rc = wsl::check_pinned(count, h_w)) != WSL_OK) return rc;
     return wsl::ring_gemm(wfmt, count, h_w, n_out, k, d_x, m, ldx, d_y, ofmt, ldy, d_ws, ws_bytes, d_slot,
                           wsl::as_stream(copy_stream), wsl::as_stream(compute_stream), events, flags);
+}
+
+int kv_cache_write(const wsl_kv_cache *h_cache, const void *d_k, const void *d_v, int xfmt, int64_t count,
+                   int64_t ld_k, int64_t ld_v, const int64_t *d_slots, uint32_t *d_status, void *stream) {
+    int rc = wsl::check_kv_rows(h_cache, d_k, d_v, xfmt, count, ld_k, ld_v, d_slots);
+    if (rc != WSL_OK || count == 0) return rc;
+    if ((rc = wsl::device_ok()) != WSL_OK) return rc;
+    return wsl::after_launch(wsl::launch_kv_write(h_cache, d_k, d_v, xfmt, count, ld_k, ld_v, d_slots, d_status,
+                                                  wsl::as_stream(stream)));
+}
+
+int kv_cache_read(const wsl_kv_cache *h_cache, const int64_t *d_slots, int64_t count, void *d_k, void *d_v, int ofmt,
+                  int64_t ld_k, int64_t ld_v, uint32_t *d_status, void *stream) {
+    int rc = wsl::check_kv_rows(h_cache, d_k, d_v, ofmt, count, ld_k, ld_v, d_slots);
+    if (rc != WSL_OK || count == 0) return rc;
+    if ((rc = wsl::device_ok()) != WSL_OK) return rc;
+    return wsl::after_launch(wsl::launch_kv_read(h_cache, d_slots, count, d_k, d_v, ofmt, ld_k, ld_v, d_status,
+                                                 wsl::as_stream(stream)));
+}
+
+size_t attn_decode_workspace_bytes(int qfmt, int64_t n_seq, int64_t q_len, int64_t n_heads, int64_t n_kv,
+                                   int64_t head_dim, int64_t pages_per_seq, int64_t page_size) {
+    if (wsl::check_attn_shape(qfmt, n_seq, q_len, n_heads, n_kv, head_dim, pages_per_seq, page_size) != WSL_OK ||
+        n_seq == 0)
+        return 0;
+    return wsl::attn_ws_bytes(qfmt, n_seq, n_heads / n_kv * q_len, n_kv, head_dim, pages_per_seq * page_size);
+}
+
+int attn_decode(const wsl_kv_cache *h_cache, const void *d_q, int qfmt, int64_t n_seq, int64_t q_len, int64_t n_heads,
+                int64_t ld_q, const int32_t *d_block_table, int64_t ld_table, int64_t pages_per_seq,
+                const int32_t *d_kv_lens, float scale, int64_t window, void *d_out, int ofmt, int64_t ld_out,
+                float *d_lse, void *d_ws, size_t ws_bytes, uint32_t *d_status, void *stream) {
+    int rc = wsl::check_attn(h_cache, d_q, qfmt, n_seq, q_len, n_heads, ld_q, d_block_table, ld_table, pages_per_seq,
+                             d_kv_lens, scale, window, d_out, ofmt, ld_out, d_lse);
+    if (rc != WSL_OK || n_seq == 0) return rc;
+    const size_t need = wsl::attn_ws_bytes(qfmt, n_seq, n_heads / h_cache->n_kv * q_len, h_cache->n_kv,
+                                           h_cache->head_dim, pages_per_seq * h_cache->page_size);
+    if ((rc = wsl::check_workspace(d_ws, ws_bytes, need, 16)) != WSL_OK) return rc;
+    if ((rc = wsl::device_ok()) != WSL_OK) return rc;
+    return wsl::after_launch(wsl::launch_attn(h_cache, d_q, qfmt, n_seq, q_len, n_heads, ld_q, d_block_table, ld_table,
+                                              pages_per_seq, d_kv_lens, scale, window, d_out, ofmt, ld_out, d_lse, d_ws,
+                                              d_status, wsl::as_stream(stream)));
+}
+
+size_t verify_drafts_workspace_bytes(int64_t n_seq, int64_t vocab) {
+    if (n_seq <= 0 || n_seq > 65535 || vocab <= 0 || vocab > wsl::kMaxDim) return 0;
+    return wsl::verify_ws_bytes(n_seq, vocab);
+}
+
+int verify_drafts(const void *d_p, const void *d_q, int pfmt, int64_t n_seq, int64_t width, int64_t vocab,
+                  int64_t ld_p, int64_t ld_q, const int32_t *d_drafts, const int32_t *d_n_drafts, const float *d_u,
+                  int32_t *d_accepted, int32_t *d_tokens, void *d_ws, size_t ws_bytes, uint32_t *d_status,
+                  void *stream) {
+    int rc = wsl::check_verify(d_p, d_q, pfmt, n_seq, width, vocab, ld_p, ld_q, d_drafts, d_n_drafts, d_u, d_accepted,
+                               d_tokens);
+    if (rc != WSL_OK || n_seq == 0) return rc;
+    if ((rc = wsl::check_workspace(d_ws, ws_bytes, wsl::verify_ws_bytes(n_seq, vocab), 8)) != WSL_OK) return rc;
+    if ((rc = wsl::device_ok()) != WSL_OK) return rc;
+    return wsl::after_launch(wsl::launch_verify(d_p, d_q, pfmt, n_seq, width, vocab, ld_p, ld_q, d_drafts, d_n_drafts,
+                                                d_u, d_accepted, d_tokens, d_ws, d_status, wsl::as_stream(stream)));
 }
 
 int wsl_stream_read(const void *d_buf, size_t bytes, uint32_t *d_sink, void *stream) {

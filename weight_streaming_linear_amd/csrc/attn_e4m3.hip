@@ -1,0 +1,6 @@
+// attn_decode over an e4m3 cache.
+#include "attn_kernel.h"
+
+namespace wsl {
+template int launch_attn_fmt<WSL_KV_E4M3>(const AttnArgs &, int, hipStream_t);
+}  // namespace wsl

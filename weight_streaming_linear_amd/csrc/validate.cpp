@@ -157,4 +157,117 @@ int check_sweep(int wfmt, int64_t count, const void *h_stages, const void *d_sta
     return WSL_OK;
 }
 
+int check_kv_cache(const void *h_cache) {
+    if (!h_cache) return WSL_E_NULL;
+    const wsl_kv_cache &c = *static_cast<const wsl_kv_cache *>(h_cache);
+    if (c.fmt != WSL_KV_BF16 && c.fmt != WSL_KV_E4M3) return WSL_E_FORMAT;
+    if (!c.k || !c.v) return WSL_E_NULL;
+    if (c.fmt == WSL_KV_E4M3 && (!c.k_exp || !c.v_exp)) return WSL_E_NULL;
+    if (c.n_pages <= 0 || c.n_pages > 0x7fffffff || c.page_size <= 0 || c.page_size > kMaxDim) return WSL_E_SHAPE;
+    if (c.n_kv <= 0 || c.n_kv > (int64_t(1) << 20)) return WSL_E_SHAPE;
+    if (c.head_dim < 16 || c.head_dim > 256 || c.head_dim % 16 != 0) return WSL_E_SHAPE;
+    const int64_t elem = c.fmt == WSL_KV_BF16 ? 2 : 1, step = 16 / elem;
+    const int64_t stride[3] = {c.page_stride, c.head_stride, c.token_stride};
+    const int64_t count[3] = {c.n_pages, c.n_kv, c.page_size};
+    int64_t reach = c.head_dim, cells = 1;
+    for (int i = 0; i < 3; ++i) {
+        if (stride[i] < c.head_dim) return WSL_E_SHAPE;
+        if (stride[i] % step != 0) return WSL_E_ALIGN;
+        int64_t far = 0;
+        if (!mul_ok(stride[i], count[i], &far) || far > INT64_MAX / 8 - reach) return WSL_E_SHAPE;
+        reach += far;
+        if (!mul_ok(cells, count[i], &cells)) return WSL_E_SHAPE;
+    }
+    if (!aligned(c.k, 16) || !aligned(c.v, 16)) return WSL_E_ALIGN;
+    return WSL_OK;
+}
+
+namespace {
+
+// Token rows [count][ld] of `width` elements outside the cache.
+int check_token_rows(int fmt, int64_t count, int64_t width, int64_t ld) {
+    const int64_t step = fmt == WSL_OUT_F32 ? 4 : 8;
+    if (ld < width) return WSL_E_SHAPE;
+    int64_t all = 0;
+    if (!mul_ok(count, ld, &all) || all > INT64_MAX / 8) return WSL_E_SHAPE;
+    return ld % step == 0 ? WSL_OK : WSL_E_ALIGN;
+}
+
+}  // namespace
+
+int check_kv_rows(const void *h_cache, const void *k, const void *v, int fmt, int64_t count, int64_t ld_k, int64_t ld_v,
+                  const void *slots) {
+    int rc = check_kv_cache(h_cache);
+    if (rc != WSL_OK) return rc;
+    if (fmt != WSL_OUT_F32 && fmt != WSL_OUT_BF16) return WSL_E_FORMAT;
+    if (count < 0) return WSL_E_SHAPE;
+    if (count == 0) return WSL_OK;
+    if (!k || !v || !slots) return WSL_E_NULL;
+    const wsl_kv_cache &c = *static_cast<const wsl_kv_cache *>(h_cache);
+    if (count > (int64_t(1) << 26) / c.n_kv) return WSL_E_SHAPE;
+    if ((rc = check_token_rows(fmt, count, c.n_kv * c.head_dim, ld_k)) != WSL_OK) return rc;
+    if ((rc = check_token_rows(fmt, count, c.n_kv * c.head_dim, ld_v)) != WSL_OK) return rc;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 8)) return WSL_E_ALIGN;
+    return WSL_OK;
+}
+
+int check_attn_shape(int qfmt, int64_t n_seq, int64_t q_len, int64_t n_heads, int64_t n_kv, int64_t head_dim,
+                     int64_t pages_per_seq, int64_t page_size) {
+    if (qfmt != WSL_OUT_F32 && qfmt != WSL_OUT_BF16) return WSL_E_FORMAT;
+    if (n_seq < 0 || n_seq > 65535 || q_len < 1 || q_len > 256) return WSL_E_SHAPE;
+    if (n_kv <= 0 || n_kv > (int64_t(1) << 20) || n_heads <= 0 || n_heads > kMaxDim || n_heads % n_kv != 0)
+        return WSL_E_SHAPE;
+    if (n_heads / n_kv * q_len > 65536 || n_heads * q_len > (int64_t(1) << 24)) return WSL_E_SHAPE;
+    if (head_dim < 16 || head_dim > 256 || head_dim % 16 != 0) return WSL_E_SHAPE;
+    if (pages_per_seq < 1 || pages_per_seq > 0x7fffffff || page_size < 1 || page_size > kMaxDim) return WSL_E_SHAPE;
+    return WSL_OK;
+}
+
+int check_attn(const void *h_cache, const void *q, int qfmt, int64_t n_seq, int64_t q_len, int64_t n_heads,
+               int64_t ld_q, const void *table, int64_t ld_table, int64_t pages_per_seq, const void *lens, float scale,
+               int64_t window, const void *out, int ofmt, int64_t ld_out, const void *lse) {
+    int rc = check_kv_cache(h_cache);
+    if (rc != WSL_OK) return rc;
+    const wsl_kv_cache &c = *static_cast<const wsl_kv_cache *>(h_cache);
+    if (ofmt != WSL_OUT_F32 && ofmt != WSL_OUT_BF16) return WSL_E_FORMAT;
+    rc = check_attn_shape(qfmt, n_seq, q_len, n_heads, c.n_kv, c.head_dim, pages_per_seq, c.page_size);
+    if (rc != WSL_OK) return rc;
+    if (n_seq == 0) return WSL_OK;
+    if (!q || !table || !lens || !out) return WSL_E_NULL;
+    if (ld_table < pages_per_seq || window < 0 || !(scale - scale == 0.f)) return WSL_E_SHAPE;
+    int64_t entries = 0;
+    if (!mul_ok(n_seq, ld_table, &entries) || entries > INT64_MAX / 8) return WSL_E_SHAPE;
+    if ((rc = check_token_rows(qfmt, n_seq * q_len, n_heads * c.head_dim, ld_q)) != WSL_OK) return rc;
+    if ((rc = check_token_rows(ofmt, n_seq * q_len, n_heads * c.head_dim, ld_out)) != WSL_OK) return rc;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(lse, 4))
+        return WSL_E_ALIGN;
+    return WSL_OK;
+}
+
+int check_verify(const void *p, const void *q, int pfmt, int64_t n_seq, int64_t width, int64_t vocab, int64_t ld_p,
+                 int64_t ld_q, const void *drafts, const void *n_drafts, const void *u, const void *accepted,
+                 const void *tokens) {
+    if (pfmt != WSL_OUT_F32 && pfmt != WSL_OUT_BF16) return WSL_E_FORMAT;
+    if (n_seq < 0 || n_seq > 65535 || width < 0 || width > WSL_VERIFY_MAX_DRAFTS) return WSL_E_SHAPE;
+    if (vocab <= 0 || vocab > kMaxDim) return WSL_E_SHAPE;
+    if (n_seq == 0) return WSL_OK;
+    if (!p || !u || !accepted || !tokens || (width > 0 && !drafts)) return WSL_E_NULL;
+    int64_t all = 0;
+    if (ld_p < vocab || (q && ld_q < vocab)) return WSL_E_SHAPE;
+    if (!mul_ok(n_seq * (width + 1), ld_p, &all) || all > INT64_MAX / 8) return WSL_E_SHAPE;
+    if (q && (!mul_ok(n_seq * (width + 1), ld_q, &all) || all > INT64_MAX / 8)) return WSL_E_SHAPE;
+    const uintptr_t elem = pfmt == WSL_OUT_F32 ? 4 : 2;
+    if (!aligned(p, elem) || !aligned(q, elem) || !aligned(drafts, 4) || !aligned(n_drafts, 4) || !aligned(u, 4) ||
+        !aligned(accepted, 4) || !aligned(tokens, 4))
+        return WSL_E_ALIGN;
+    return WSL_OK;
+}
+
+int check_workspace(const void *ws, size_t ws_bytes, size_t need, size_t alignment) {
+    if (need == 0) return WSL_OK;
+    if (!ws) return WSL_E_NULL;
+    if (ws_bytes < need) return WSL_E_RANGE;
+    return aligned(ws, alignment) ? WSL_OK : WSL_E_ALIGN;
+}
+
 }  // namespace wsl

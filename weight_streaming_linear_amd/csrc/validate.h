@@ -40,6 +40,21 @@ int check_multi(int wfmt, int64_t count, const void *h_stages);
 int check_embed(const void *packed, int64_t n_rows, int64_t k, const void *ids, int64_t count, const void *out,
                 int ofmt, int64_t ld_out);
 
+// A wsl_kv_cache, then kv_cache_write / kv_cache_read: rows outside the cache of type fmt.
+int check_kv_cache(const void *h_cache);
+int check_kv_rows(const void *h_cache, const void *k, const void *v, int fmt, int64_t count, int64_t ld_k, int64_t ld_v,
+                  const void *slots);
+int check_attn_shape(int qfmt, int64_t n_seq, int64_t q_len, int64_t n_heads, int64_t n_kv, int64_t head_dim,
+                     int64_t pages_per_seq, int64_t page_size);
+int check_attn(const void *h_cache, const void *q, int qfmt, int64_t n_seq, int64_t q_len, int64_t n_heads,
+               int64_t ld_q, const void *table, int64_t ld_table, int64_t pages_per_seq, const void *lens, float scale,
+               int64_t window, const void *out, int ofmt, int64_t ld_out, const void *lse);
+int check_verify(const void *p, const void *q, int pfmt, int64_t n_seq, int64_t width, int64_t vocab, int64_t ld_p,
+                 int64_t ld_q, const void *drafts, const void *n_drafts, const void *u, const void *accepted,
+                 const void *tokens);
+// A workspace of ws_bytes at ws where need bytes are needed.
+int check_workspace(const void *ws, size_t ws_bytes, size_t need, size_t alignment);
+
 // Upper bound on any single dimension accepted by the library (keeps every
 // derived index within int64 and every per-row byte offset within int32).
 constexpr int64_t kMaxDim = int64_t(1) << 30;
