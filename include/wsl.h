@@ -412,12 +412,14 @@ int kv_cache_read(const wsl_kv_cache *h_cache, const int64_t *d_slots, int64_t c
  * For sequence b with L = d_kv_lens[b] tokens, query i stands at position p = L - q_len + i and
  * sees the tokens t <= p (with window > 0 only t > p - window):
  *   out = sum_t exp(s_t - max s) V_t / sum_t exp(s_t - max s),   s_t = scale * <q, K_t>,
- * head h reading kv head h / (n_heads / n_kv).  A query that sees nothing (p < 0) gives zeros.
+ * head h reading kv head h / (n_heads / n_kv).  A query that sees nothing (p < 0), or only scores of
+ * -infinity, gives zeros.
  * Tokens a query does not see have no part in it, whatever their slots hold.
  * d_q        device [n_seq * q_len][ld_q] of qfmt (WSL_OUT_F32 or WSL_OUT_BF16), n_heads *
  *            head_dim elements a token; 16-byte aligned, ld_q a multiple of 16 bytes.
  * n_seq      0 .. 65535 (0 launches nothing).  q_len 1 .. 256.  n_heads a multiple of n_kv.
- *            q_len * n_heads / n_kv <= 2^16, q_len * n_heads <= 2^24.
+ *            q_len * n_heads / n_kv <= 2^16, q_len * n_heads <= 2^24, and n_seq * n_kv *
+ *            ceil(pages_per_seq * page_size / 128) <= 2^30.
  * d_block_table   device int32 [n_seq][ld_table]: page of token t of a sequence at [t / page_size];
  *            pages_per_seq (1 .. ld_table) entries of a row may be read.
  * d_kv_lens  device int32 [n_seq]: read by the kernels only, so a captured call goes on with
@@ -426,14 +428,15 @@ int kv_cache_read(const wsl_kv_cache *h_cache, const int64_t *d_slots, int64_t c
  * scale      the factor of the scores.  window >= 0 (0: none).
  * d_out      device [n_seq * q_len][ld_out] of ofmt, 16-byte aligned, ld_out a multiple of 16 bytes.
  * d_lse      device fp32 [n_seq][q_len][n_heads] or NULL: log sum_t exp(s_t), -infinity where
- *            nothing is seen (for joining with attention over tokens kept elsewhere).
+ *            the sum is zero (for joining with attention over tokens kept elsewhere).
  * d_ws       device workspace, 16-byte aligned, of attn_decode_workspace_bytes (else WSL_E_RANGE):
  *            the length is split over the chip by the actual lengths, and parts of one head are
  *            joined by a second launch.  Its contents on entry do not matter.  Calls that share
  *            a workspace must not overlap.
  * d_status   device uint32 or NULL: WSL_STATUS_INDEX as above.
- * Scores, maxima, sums and products with V are held in fp32; the weights enter the matrix
- * instructions as two bf16 numbers (16 bits), fp32 queries as three (24 bits).  Deterministic.
+ * Scores, maxima, sums and products with V are held in fp32.  The matrix instructions take bf16:
+ * the weights enter them as two bf16 numbers (16 bits) beside bf16 queries; fp32 queries and the
+ * weights beside them as three (24 bits).  Deterministic.
  */
 size_t attn_decode_workspace_bytes(int qfmt, int64_t n_seq, int64_t q_len, int64_t n_heads, int64_t n_kv,
                                    int64_t head_dim, int64_t pages_per_seq, int64_t page_size);

@@ -1,5 +1,4 @@
-// What the host side of attn_decode tells its kernels, and the split of the work that the
-// attention kernel and the joining kernel both derive from it.
+// What the host side of attn_decode tells its kernels, and the split of the work among workgroups.
 #pragma once
 
 #include "device_common.h"
@@ -10,6 +9,15 @@ constexpr int kAttnWaves = 4;                      // waves of a workgroup
 constexpr int kAttnSub = 32;                       // tokens a wave takes at a time
 constexpr int kAttnTile = kAttnWaves * kAttnSub;   // tokens a workgroup takes at a time
 constexpr int kAttnThreads = kAttnWaves * 64;
+constexpr int kAttnCus = 256;
+constexpr int kAttnMaxWaves = 4;                   // of a SIMD, over all variants
+constexpr int64_t kAttnMaxTokens = 0x7fffffff - 4 * kAttnTile;   // positions stay in 32 bits some rounds past the end
+constexpr int kAttnJoinRows = 4;                   // rows a workgroup of the joining kernel takes
+
+// An item that a workgroup began and others go on with: its sequence, kv head and workgroups.
+struct AttnOpen {
+    int32_t seq, head, parts, pad;
+};
 
 struct AttnArgs {
     const char *k, *v;
@@ -17,14 +25,16 @@ struct AttnArgs {
     const void *q;
     void *out;
     float *lse;
-    float *part_o;        // [2 * workers][tile_rows][head_dim]: unnormalised sums
-    float2 *part_ml;      // [2 * workers][tile_rows]: running maximum (log2 domain) and sum
+    float *part_o;        // [row_tiles][2 * workers][tile_rows][head_dim]: unnormalised sums
+    float2 *part_ml;      // [row_tiles][2 * workers][tile_rows]: running maximum (log2 domain) and sum
+    AttnOpen *open;       // [workers]; null where nothing can be split
     const int32_t *table, *lens;
     uint32_t *status;
     int64_t page_stride, head_stride, token_stride;   // bytes
     int64_t ld_q, ld_out, ld_table;                   // elements
-    int64_t window, capacity;                         // capacity: tokens a table row can name
+    int64_t window;
     float scale_log2;
+    int32_t capacity;     // tokens a table row can name
     int32_t n_seq, q_len, n_kv, group, rows, head_dim, page_size, n_pages;
     int32_t row_tiles, tile_rows, workers, qfmt, ofmt;
 };
@@ -40,7 +50,7 @@ __device__ __forceinline__ AttnSpan attn_span(const AttnArgs &a, int32_t seq) {
     AttnSpan s;
     const int32_t raw = a.lens[seq];
     s.bad = raw < 0 || raw > a.capacity;
-    s.len = raw < 0 ? 0 : (raw > a.capacity ? static_cast<int32_t>(a.capacity) : raw);
+    s.len = raw < 0 ? 0 : (raw > a.capacity ? a.capacity : raw);
     s.first = 0;
     if (a.window > 0) {
         const int64_t lo = static_cast<int64_t>(s.len) - a.q_len - a.window + 1;
@@ -51,74 +61,89 @@ __device__ __forceinline__ AttnSpan attn_span(const AttnArgs &a, int32_t seq) {
     return s;
 }
 
-// Token tiles of all sequences in order.  Every workgroup adds them up for itself (the lengths
-// are on the device): thread i takes `each` successive sequences.  lds: 4 int64.
+// The tiles of all (sequence, kv head) in order: the tiles of a sequence's first head, then of its
+// next, then the next sequence's.  Worker w takes `each` successive ones from w * each on, with the
+// least `each` for which the workers suffice.  The lengths are on the device, so every wave works
+// this out for itself: without LDS or barriers, each lane adds up the tiles of `per` successive
+// sequences, a scan over the lanes finds the lane whose sequences hold the wanted tile, and its
+// sequences are divided among the lanes again until one is left.
 struct AttnPlan {
-    int64_t before, mine, total;   // tiles before this thread's sequences, in them, in all
-    int32_t each;
+    int32_t total, each;      // tiles in all; of a worker
+    int32_t seq, before;      // the worker's first sequence and the tiles (of one head) before it
 };
 
-__device__ __forceinline__ AttnPlan attn_plan(const AttnArgs &a, int64_t *lds) {
-    AttnPlan p;
-    const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6;
-    p.each = (a.n_seq + kAttnThreads - 1) / kAttnThreads;
-    p.mine = 0;
-    for (int32_t i = 0; i < p.each; ++i) {
-        const int64_t b = static_cast<int64_t>(tid) * p.each + i;
-        if (b < a.n_seq) p.mine += attn_span(a, static_cast<int32_t>(b)).tiles;
+__device__ __forceinline__ int32_t attn_lane_tiles(const AttnArgs &a, int32_t first, int32_t count, int32_t per,
+                                                   int32_t &mine) {
+    const int lane = static_cast<int>(threadIdx.x & 63);
+    mine = 0;
+    for (int32_t i = 0; i < per; ++i) {
+        const int32_t b = lane * per + i;
+        if (b < count) mine += attn_span(a, first + b).tiles;
     }
-    int64_t run = p.mine;
+    int32_t run = mine;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
-        const int64_t o = __shfl_up(run, off, 64);
+        const int32_t o = __shfl_up(run, off, 64);
         if (lane >= off) run += o;
     }
-    if (lane == 63) lds[wave] = run;
-    __syncthreads();
-    p.before = run - p.mine;
-    p.total = 0;
-    for (int i = 0; i < kAttnWaves; ++i) {
-        if (i < wave) p.before += lds[i];
-        p.total += lds[i];
+    return run;
+}
+
+__device__ __forceinline__ AttnPlan attn_plan(const AttnArgs &a, uint32_t w) {
+    AttnPlan p;
+    p.seq = p.before = 0;
+    const uint32_t heads = static_cast<uint32_t>(a.n_kv), workers = static_cast<uint32_t>(a.workers);
+    if (a.n_seq == 1) {
+        const uint32_t total = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(attn_span(a, 0).tiles)) * heads;
+        p.total = static_cast<int32_t>(total);
+        p.each = static_cast<int32_t>((total + workers - 1) / workers);
+        return p;
     }
-    __syncthreads();
-    return p;
+    int32_t count = a.n_seq, mine;
+    int32_t per = (count + 63) / 64, run = attn_lane_tiles(a, 0, count, per, mine);
+    const uint32_t total = static_cast<uint32_t>(__builtin_amdgcn_readlane(run, 63)) * heads;
+    p.total = static_cast<int32_t>(total);
+    p.each = static_cast<int32_t>((total + workers - 1) / workers);
+    const uint32_t x = w * static_cast<uint32_t>(p.each);
+    if (x >= total) return p;
+    const int32_t y = static_cast<int32_t>(x / heads);
+    for (;;) {
+        // (the bound holds by itself unless the lengths change while they are read: then the rows are
+        // wrong, but nothing outside the tables is touched)
+        const int past = __builtin_popcountll(__ballot(p.before + run <= y)), lastj = (count - 1) / per;
+        const int j = past < lastj ? past : lastj;
+        p.before += __builtin_amdgcn_readlane(run - mine, j);
+        p.seq += j * per;
+        if (per == 1) return p;
+        count = count - j * per < per ? count - j * per : per;
+        per = (count + 63) / 64;
+        run = attn_lane_tiles(a, p.seq, count, per, mine);
+    }
 }
 
-// Worker w takes the global tiles [total * w / workers, total * (w + 1) / workers), with no more
-// workers than tiles, so that none is empty.
-__device__ __forceinline__ int64_t attn_workers(const AttnArgs &a, int64_t total) {
-    return total < a.workers ? total : a.workers;
-}
-__device__ __forceinline__ int64_t attn_start(int64_t total, int64_t w, int64_t workers) { return total * w / workers; }
-__device__ __forceinline__ int64_t attn_worker(int64_t total, int64_t x, int64_t workers) {
-    return ((x + 1) * workers - 1) / total;
-}
-
-__device__ __forceinline__ void attn_store(const AttnArgs &a, int64_t at, float4 o) {
+__device__ __forceinline__ void attn_store(const AttnArgs &a, int64_t at, f32x4 o) {
     if (a.ofmt == WSL_OUT_F32)
-        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = o;
+        *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + at) = o;
     else
         *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) =
             make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
 }
 
-// Row `row` (query position row / group, head h * group + row % group) of a sequence is done:
-// o and l are its sums, m the maximum they are relative to.
-__device__ __forceinline__ void attn_finish(const AttnArgs &a, int32_t seq, int32_t len, int32_t h, int32_t row,
-                                            int32_t d, float4 o, float m, float l) {
+// Elements d .. d + 3 of row `row` (query position row / group, head h * group + row % group) of a
+// sequence are done: o and l are its sums, m the maximum they are relative to.  l is zero where
+// nothing was seen, and at least one otherwise (the maximum's own term).
+__device__ __forceinline__ void attn_finish(const AttnArgs &a, int32_t seq, int32_t h, int32_t row, int32_t d, f32x4 o,
+                                            float m, float l) {
     const int32_t i = row / a.group, head = h * a.group + row - i * a.group;
     const int64_t tok = static_cast<int64_t>(seq) * a.q_len + i;
-    const bool seen = len - a.q_len + i >= 0;       // else no token is visible: zeros, not 0 / 0
-    const float r = 1.f / l;
-    o.x = seen ? o.x * r : 0.f, o.y = seen ? o.y * r : 0.f, o.z = seen ? o.z * r : 0.f, o.w = seen ? o.w * r : 0.f;
-    attn_store(a, tok * a.ld_out + static_cast<int64_t>(head) * a.head_dim + d, o);
+    const float r = l == 0.f ? 0.f : 1.f / l;
+    attn_store(a, tok * a.ld_out + static_cast<int64_t>(head) * a.head_dim + d, o * r);
     if (a.lse != nullptr && d == 0)
         a.lse[tok * (a.n_kv * a.group) + head] =
-            seen ? (m + __builtin_amdgcn_logf(l)) * 0.69314718055994530942f : -__builtin_huge_valf();
+            l == 0.f ? -__builtin_huge_valf() : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994530942f;
 }
 
 template <int FMT>
-int launch_attn_fmt(const AttnArgs &a, int tiles_m, hipStream_t s);
+int launch_attn_fmt(AttnArgs &a, int tiles_m, hipStream_t s);
 
 }  // namespace wsl

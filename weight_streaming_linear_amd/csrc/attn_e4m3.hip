@@ -2,5 +2,5 @@
 #include "attn_kernel.h"
 
 namespace wsl {
-template int launch_attn_fmt<WSL_KV_E4M3>(const AttnArgs &, int, hipStream_t);
+template int launch_attn_fmt<WSL_KV_E4M3>(AttnArgs &, int, hipStream_t);
 }  // namespace wsl

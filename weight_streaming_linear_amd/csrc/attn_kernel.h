@@ -14,110 +14,91 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(b), c, 0, 0, 0);
 }
 
-__device__ __forceinline__ float scale_of(uint32_t byte) { return __builtin_bit_cast(float, byte << 23); }
-
-__device__ __forceinline__ uint32_t fp8_pair(uint32_t w, float s, bool hi) {
-    return hi ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, true))
-              : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, false));
+// Two bf16 numbers of two e4m3 codes (exact).
+__device__ __forceinline__ uint32_t fp8_pair(uint32_t w, bool hi) {
+    return hi ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.f, true))
+              : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.f, false));
 }
 
-// 32 keys or values of one head as loaded: bf16 elements, or e4m3 codes with a scale per token.
+// 32 keys or values of one head as loaded: bf16 elements or e4m3 codes.
 template <int FMT, int DP>
 struct Keys {
     static constexpr int kLoads = FMT == WSL_KV_BF16 ? DP / 32 : DP / 64;   // 16 bytes each
     u32x4 x[2][kLoads];
-    uint32_t e[2];
 };
 template <int FMT, int DP>
 struct Values {
-    static constexpr int kVec = DP >= 128 ? 8 : DP / 16;                    // elements of a load
+    static constexpr int kVec = DP % 128 == 0 ? 8 : 4;                      // elements of a load
     static constexpr int kLoads = DP / (16 * kVec);
     static constexpr int kWords = FMT == WSL_KV_BF16 ? kVec / 2 : kVec / 4;
     uint32_t x[8][kLoads][kWords];
-    uint32_t e[8];
 };
 
-// Where a wave's 32 tokens lie.  UNI: a page holds whole groups of 16 tokens, so the two
-// groups' addresses are the same for all lanes; otherwise each lane keeps its own tokens'.
-template <bool UNI>
-struct Place;
-template <>
-struct Place<true> {
-    int64_t off[2];      // byte offset of the group's first token
-    int64_t cell[2];     // its index among the scale bytes
-    bool ok[2];
-};
-template <>
-struct Place<false> {
-    int64_t koff[2], voff[8];
-    int64_t kcell[2], vcell[8];
-    uint32_t kok, vok;   // bit i: token i of the lane is there
+// One wave's part of LDS: where its 32 tokens lie, and their scales.
+struct WaveLds {
+    int64_t off[kAttnSub];
+    float ks[kAttnSub], vs[kAttnSub];
 };
 
-// Token t of the sequence: its byte offset and scale index; false (and a safe offset) where the
-// sequence ends before it or its page is none of the cache's.
-__device__ __forceinline__ bool find_token(const AttnArgs &a, const int32_t *table, int32_t h, int32_t len, int32_t t,
-                                           int64_t &off, int64_t &cell, bool &bad) {
-    int32_t page = 0, at = 0;
-    bool ok = t < len;
-    if (ok) {
-        const int32_t i = static_cast<uint32_t>(t) / static_cast<uint32_t>(a.page_size);
-        at = t - i * a.page_size;
-        page = table[i];
-        if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.n_pages)) {
-            ok = false;
-            bad = true;
-            page = at = 0;
-        }
-    }
-    off = page * a.page_stride + h * a.head_stride + at * a.token_stride;
-    cell = (static_cast<int64_t>(page) * a.n_kv + h) * a.page_size + at;
-    return ok;
+// Orders one wave's LDS accesses across its lanes (they are carried out in order: no instruction).
+__device__ __forceinline__ void wave_lds_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 }
 
-template <bool UNI>
-__device__ __forceinline__ Place<UNI> find_tokens(const AttnArgs &a, const int32_t *table, int32_t h, int32_t len,
-                                                  int32_t base, bool &bad) {
-    Place<UNI> p;
-    const int lane = static_cast<int>(threadIdx.x & 63);
-    if constexpr (UNI) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) p.ok[i] = find_token(a, table, h, len, base + 16 * i, p.off[i], p.cell[i], bad);
-    } else {
-        p.kok = p.vok = 0;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            p.kok |= find_token(a, table, h, len, base + 16 * i + (lane & 15), p.koff[i], p.kcell[i], bad) ? 1u << i : 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int32_t t = base + 16 * (i >> 2) + 4 * (lane >> 4) + (i & 3);
-            p.vok |= find_token(a, table, h, len, t, p.voff[i], p.vcell[i], bad) ? 1u << i : 0;
-        }
+// Lane l's token (l % 32) of 32 successive ones: its place in its page, and its page as the table
+// names it.  The table is read two rounds before the tokens are, so that nobody waits for it.
+struct Look {
+    int32_t at, page;
+};
+
+__device__ __forceinline__ Look look_up(const AttnArgs &a, const int32_t *table, int32_t len, int32_t t) {
+    t += static_cast<int32_t>(threadIdx.x & 31);
+    Look p = {0, 0};
+    if (t < len) {
+        const uint32_t i = static_cast<uint32_t>(t) / static_cast<uint32_t>(a.page_size);
+        p.at = t - static_cast<int32_t>(i * static_cast<uint32_t>(a.page_size));
+        p.page = table[i];
     }
     return p;
 }
 
+// The byte offsets of the 32 tokens from t on go into LDS (their scale bytes are fetched); returns
+// which of the tokens are there at all: before the sequence's end, on a page that the cache has.
+// A token that is not there gets a safe offset and the scale 1.
+template <int FMT>
+__device__ __forceinline__ uint32_t find_tokens(const AttnArgs &a, WaveLds &w, const Look &p, int32_t h, int32_t len,
+                                                int32_t t, uint32_t &kb, uint32_t &vb, bool &bad) {
+    const int32_t lane = static_cast<int32_t>(threadIdx.x & 31);
+    const bool in = t + lane < len, ok = in && static_cast<uint32_t>(p.page) < static_cast<uint32_t>(a.n_pages);
+    bad |= in && !ok;
+    const int64_t page = ok ? p.page : 0, at = ok ? p.at : 0;
+    wave_lds_fence();
+    w.off[lane] = page * a.page_stride + h * a.head_stride + at * a.token_stride;
+    if constexpr (FMT == WSL_KV_E4M3) {
+        kb = vb = 127;
+        if (ok) {
+            const int64_t cell = (page * a.n_kv + h) * a.page_size + at;
+            kb = a.ke[cell], vb = a.ve[cell];
+        }
+    }
+    wave_lds_fence();
+    return static_cast<uint32_t>(__ballot(ok));
+}
+
 // Keys as the A operand of S^T = K Q^T: lane l holds key l % 16 and, of its head_dim, the
 // 8 consecutive elements per matrix instruction that lane group l / 16 owns.
-template <int FMT, int DP, bool UNI>
-__device__ __forceinline__ void load_keys(const AttnArgs &a, const Place<UNI> &p, Keys<FMT, DP> &k) {
+template <int FMT, int DP>
+__device__ __forceinline__ void load_keys(const AttnArgs &a, const WaveLds &w, Keys<FMT, DP> &k) {
     const int lane = static_cast<int>(threadIdx.x & 63);
     constexpr int kElem = FMT == WSL_KV_BF16 ? 2 : 1, kPer = 16 / kElem;    // elements of a 16-byte load
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const char *row;
-        if constexpr (UNI) row = a.k + p.off[i] + static_cast<uint32_t>((lane & 15) * static_cast<int32_t>(a.token_stride));
-        else row = a.k + p.koff[i];
+        const char *row = a.k + w.off[16 * i + (lane & 15)];
 #pragma unroll
         for (int c = 0; c < Keys<FMT, DP>::kLoads; ++c) {
             const int d = c * 4 * kPer + (lane >> 4) * kPer;
-            const bool in = d < a.head_dim;
-            k.x[i][c] = *reinterpret_cast<const u32x4 *>(row + (in ? d : 0) * kElem);
-            if (a.head_dim != DP && !in) k.x[i][c] = u32x4{0, 0, 0, 0};
-        }
-        if constexpr (FMT == WSL_KV_E4M3) {
-            if constexpr (UNI) k.e[i] = a.ke[p.cell[i] + (lane & 15)];
-            else k.e[i] = a.ke[p.kcell[i]];
+            k.x[i][c] = *reinterpret_cast<const u32x4 *>(row + (d < a.head_dim ? d : 0) * kElem);
         }
     }
 }
@@ -125,60 +106,44 @@ __device__ __forceinline__ void load_keys(const AttnArgs &a, const Place<UNI> &p
 // Values for the A operand of O^T = V^T P: lane l takes its group's 8 tokens (those whose scores
 // S^T leaves in this lane) and, of each, the kVec elements that start at (l % 16) * kVec: whole
 // rows are read in order, and the 8 x kVec block is transposed inside the lane.
-template <int FMT, int DP, bool UNI>
-__device__ __forceinline__ void load_values(const AttnArgs &a, const Place<UNI> &p, Values<FMT, DP> &v) {
+template <int FMT, int DP>
+__device__ __forceinline__ void load_values(const AttnArgs &a, const WaveLds &w, Values<FMT, DP> &v) {
     typedef Values<FMT, DP> V;
     const int lane = static_cast<int>(threadIdx.x & 63);
     constexpr int kElem = FMT == WSL_KV_BF16 ? 2 : 1;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const char *row;
-        if constexpr (UNI)
-            row = a.v + p.off[i >> 2] +
-                  static_cast<uint32_t>((4 * (lane >> 4) + (i & 3)) * static_cast<int32_t>(a.token_stride));
-        else row = a.v + p.voff[i];
+        const char *row = a.v + w.off[16 * (i >> 2) + 4 * (lane >> 4) + (i & 3)];
 #pragma unroll
         for (int n = 0; n < V::kLoads; ++n) {
             int d = n * 16 * V::kVec + (lane & 15) * V::kVec;
             d = d < a.head_dim ? d : 0;              // columns past head_dim: computed, never written
             const uint32_t *src = reinterpret_cast<const uint32_t *>(row + d * kElem);
             if constexpr (V::kWords == 4) {
-                const u32x4 w = *reinterpret_cast<const u32x4 *>(src);
-                v.x[i][n][0] = w.x, v.x[i][n][1] = w.y, v.x[i][n][2] = w.z, v.x[i][n][3] = w.w;
+                const u32x4 x = *reinterpret_cast<const u32x4 *>(src);
+                v.x[i][n][0] = x.x, v.x[i][n][1] = x.y, v.x[i][n][2] = x.z, v.x[i][n][3] = x.w;
             } else if constexpr (V::kWords == 2) {
-                const u32x2 w = *reinterpret_cast<const u32x2 *>(src);
-                v.x[i][n][0] = w.x, v.x[i][n][1] = w.y;
+                const u32x2 x = *reinterpret_cast<const u32x2 *>(src);
+                v.x[i][n][0] = x.x, v.x[i][n][1] = x.y;
             } else {
                 v.x[i][n][0] = src[0];
             }
         }
-        if constexpr (FMT == WSL_KV_E4M3) {
-            if constexpr (UNI) v.e[i] = a.ve[p.cell[i >> 2] + 4 * (lane >> 4) + (i & 3)];
-            else v.e[i] = a.ve[p.vcell[i]];
-        }
     }
 }
 
-// Token pair (2t, 2t + 1) of element word w (two bf16 elements) of load n.
+// Element word w (two bf16 elements) of load n of token t.  Codes are converted as they are: their
+// powers of two go into the scores and the weights, which is exact.
 template <int FMT, int DP>
 __device__ __forceinline__ uint32_t value_word(const Values<FMT, DP> &v, int t, int n, int w) {
     if constexpr (FMT == WSL_KV_BF16) return v.x[t][n][w];
-    else return fp8_pair(v.x[t][n][w >> 1], scale_of(v.e[t]), (w & 1) != 0);
+    else return fp8_pair(v.x[t][n][w >> 1], (w & 1) != 0);
 }
 
-// A pair of bf16 numbers with its NaNs and infinities replaced by zero.
-__device__ __forceinline__ uint32_t finite_pair(uint32_t x) {
-    x = (x & 0x7f80u) == 0x7f80u ? x & 0xffff0000u : x;
-    return (x & 0x7f800000u) == 0x7f800000u ? x & 0xffffu : x;
-}
-
-// O^T += V^T (hi + lo) for MT blocks of 16 rows.
-// CAREFUL: only over the values whose bit of `keep` is set and only into the rows that `rows` picks
-// (bit m: the lane's row of block m), with lo (which may be zero or negative) times the finite
-// values alone, so that an infinity gives the infinity that the weight itself would.
-template <int FMT, int DP, int MT, bool CAREFUL>
-__device__ __forceinline__ void add_values(const Values<FMT, DP> &v, const u32x4 (&hi)[MT], const u32x4 (&lo)[MT],
-                                           f32x4 (&acc)[MT][DP / 16], uint32_t keep, uint32_t rows) {
+// O^T += V^T P for MT blocks of 16 rows, P as a sum of PT bf16 numbers.
+template <int FMT, int DP, int MT, int PT>
+__device__ __forceinline__ void add_values(const Values<FMT, DP> &v, const u32x4 (&p)[MT][PT],
+                                           f32x4 (&acc)[MT][DP / 16]) {
     typedef Values<FMT, DP> V;
 #pragma unroll
     for (int n = 0; n < V::kLoads; ++n)
@@ -186,29 +151,18 @@ __device__ __forceinline__ void add_values(const Values<FMT, DP> &v, const u32x4
         for (int w = 0; w < V::kVec / 2; ++w) {
             uint32_t x[8];
 #pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                x[t] = value_word<FMT, DP>(v, t, n, w);
-                if constexpr (CAREFUL) x[t] = (keep >> t) & 1 ? x[t] : 0;
-            }
+            for (int t = 0; t < 8; ++t) x[t] = value_word<FMT, DP>(v, t, n, w);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int j = n * V::kVec + 2 * w + e;
-                u32x4 both, fine;
+                u32x4 col;
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    both[t] = __builtin_amdgcn_perm(x[2 * t + 1], x[2 * t], e ? 0x07060302u : 0x05040100u);
-                    fine[t] = CAREFUL ? finite_pair(both[t]) : both[t];
-                }
+                for (int t = 0; t < 4; ++t)
+                    col[t] = __builtin_amdgcn_perm(x[2 * t + 1], x[2 * t], e ? 0x07060302u : 0x05040100u);
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    const f32x4 sum = mfma(fine, lo[m], mfma(both, hi[m], acc[m][j]));
-                    if constexpr (CAREFUL) {
+                for (int m = 0; m < MT; ++m)
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) acc[m][j][r] = (rows >> m) & 1 ? sum[r] : acc[m][j][r];
-                    } else {
-                        acc[m][j] = sum;
-                    }
-                }
+                    for (int i = 0; i < PT; ++i) acc[m][j] = mfma(col, p[m][i], acc[m][j]);
             }
         }
 }
@@ -223,7 +177,6 @@ __device__ __forceinline__ void keep_values(Values<FMT, DP> &v, uint32_t keep) {
         for (int n = 0; n < V::kLoads; ++n)
 #pragma unroll
             for (int w = 0; w < V::kWords; ++w) v.x[t][n][w] = on ? v.x[t][n][w] : 0;
-        if constexpr (FMT == WSL_KV_E4M3) v.e[t] = on ? v.e[t] : 127;    // 0 * an unused scale may be NaN
     }
 }
 
@@ -268,6 +221,85 @@ __device__ __forceinline__ void load_queries(const AttnArgs &a, int32_t seq, int
     }
 }
 
+__device__ __forceinline__ AttnSpan wave_span(const AttnArgs &a, int32_t seq) {
+    AttnSpan s = attn_span(a, seq);
+    s.len = __builtin_amdgcn_readfirstlane(s.len);
+    s.first = __builtin_amdgcn_readfirstlane(s.first);
+    s.tiles = __builtin_amdgcn_readfirstlane(s.tiles);
+    return s;
+}
+
+// Element d of a row of keys or values, exactly.
+template <int FMT>
+__device__ __forceinline__ float element(const char *row, int32_t d, float scale) {
+    if constexpr (FMT == WSL_KV_BF16) return bf16_lo(reinterpret_cast<const uint16_t *>(row)[d]);
+    else return bf16_lo(fp8_pair(reinterpret_cast<const uint8_t *>(row)[d], false)) * scale;
+}
+
+// A wave's part of one row block (the lane's row), token by token in fp32: a row's sums take nothing
+// from a token that it does not see.  Only for tokens among which a NaN or an infinity was found.
+template <int FMT, int DP>
+__device__ __forceinline__ void again(const AttnArgs &a, const int32_t *table, int32_t seq, int32_t h, int32_t row,
+                                      int32_t len, int32_t t0, int32_t t1, int32_t hi, f32x4 (&acc)[DP / 16], float &m,
+                                      float &l) {
+    constexpr int kVec = Values<FMT, DP>::kVec;
+    const int g = static_cast<int>(threadIdx.x & 63) >> 4;
+    const int32_t pos = row < a.rows ? row / a.group : 0, head = h * a.group + (row < a.rows ? row - pos * a.group : 0);
+    const int64_t at_q = (static_cast<int64_t>(seq) * a.q_len + pos) * a.ld_q + static_cast<int64_t>(head) * a.head_dim;
+    m = -__builtin_huge_valf();
+    l = 0.f;
+#pragma unroll
+    for (int j = 0; j < DP / 16; ++j) acc[j] = f32x4{0, 0, 0, 0};
+    for (int32_t sub = t0; sub < t1; sub += kAttnTile)
+        for (int32_t t = sub; t < sub + kAttnSub && t < len; ++t) {
+            const uint32_t i = static_cast<uint32_t>(t) / static_cast<uint32_t>(a.page_size);
+            const int64_t page = table[i], at = t - static_cast<int32_t>(i * static_cast<uint32_t>(a.page_size));
+            const bool see = t <= hi && (a.window == 0 || t > hi - a.window);
+            if (page < 0 || page >= a.n_pages || !__any(see)) continue;
+            const int64_t off = page * a.page_stride + h * a.head_stride + at * a.token_stride;
+            float ks = 1.f, vs = 1.f;
+            if constexpr (FMT == WSL_KV_E4M3) {
+                const int64_t cell = (page * a.n_kv + h) * a.page_size + at;
+                ks = __builtin_bit_cast(float, static_cast<uint32_t>(a.ke[cell]) << 23);
+                vs = __builtin_bit_cast(float, static_cast<uint32_t>(a.ve[cell]) << 23);
+            }
+            float s = 0.f;
+            for (int32_t d = g; d < a.head_dim; d += 4) {
+                const float q = a.qfmt == WSL_OUT_F32 ? static_cast<const float *>(a.q)[at_q + d]
+                                                      : bf16_lo(static_cast<const uint16_t *>(a.q)[at_q + d]);
+                s = __builtin_fmaf(q, element<FMT>(a.k + off, d, ks), s);
+            }
+            s += __shfl_xor(s, 16, 64);
+            s += __shfl_xor(s, 32, 64);
+            s = see ? s * a.scale_log2 : -__builtin_huge_valf();
+            const float best = fmaxf(m, s), ref = best == -__builtin_huge_valf() ? 0.f : best;
+            const float f = __builtin_amdgcn_exp2f(m - ref), p = __builtin_amdgcn_exp2f(s - ref);
+            m = best;
+            l = l * f + p;
+#pragma unroll
+            for (int c = 0; c < DP / (16 * kVec); ++c)
+#pragma unroll
+                for (int e = 0; e < kVec; ++e)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int32_t d = c * 16 * kVec + (4 * g + r) * kVec + e;
+                        const float x = d < a.head_dim ? element<FMT>(a.v + off, d, vs) : 0.f;
+                        const float o = acc[c * kVec + e][r] * f;
+                        acc[c * kVec + e][r] = see ? __builtin_fmaf(p, x, o) : o;
+                    }
+        }
+    l = g == 0 ? l : 0.f;       // the lanes of a row add theirs up
+}
+
+// Waves of a SIMD that the registers are shared among (a workgroup is one wave on each): what is in
+// flight has to cover the memory's latency, and a wave has a round's keys and values under way.
+template <int FMT, int DP, int MT, int QT>
+constexpr int attn_waves() {
+    if (DP > 128) return FMT == WSL_KV_BF16 ? 1 : 2;
+    if (FMT == WSL_KV_BF16) return DP == 64 ? 3 : 2;
+    return DP == 64 ? 3 : 2;
+}
+
 // One pass over a range of token tiles with the running maximum and sum of a softmax:
 //     S = scale * Q K^T;  m' = max(m, max S);  P = exp(S - m');
 //     l = l * exp(m - m') + sum P;  O = O * exp(m - m') + P V.
@@ -276,57 +308,53 @@ __device__ __forceinline__ void load_queries(const AttnArgs &a, int32_t seq, int
 // the matrix instruction's 8 reduction slots of a lane group are taken to be those 8 keys: the
 // order of the reduction is free as long as V's lanes use the same.  The rows' maxima and sums
 // then sit in the lanes that hold the rows' outputs.
-// P enters the matrix instruction as the sum of two bf16 numbers (16 bits): one alone would add an
-// error as large as a bf16 result's own rounding.
-template <int FMT, int DP, int MT, int QT, bool UNI>
-__global__ __launch_bounds__(kAttnThreads, MT *DP *(QT == 1 ? 1 : 2) <= 128 ? 2 : 1) void attn_kernel(AttnArgs a) {
-    constexpr int kPad = DP + 4;
+// P enters the matrix instruction as the sum of two bf16 numbers (16 bits) beside bf16 queries, where
+// one alone would add an error as large as a bf16 result's own rounding, and of three (24 bits)
+// beside fp32 queries.
+// Each wave works on 32 tokens of its own in a round, and the four join at an item's end.  In a
+// round it asks for this round's values, then works on the keys that it asked for a round before,
+// asks for the next round's keys and the table's entries for the round after that.
+template <int FMT, int DP, int MT, int QT>
+__global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void attn_kernel(AttnArgs a) {
+    constexpr int kPad = DP + 4, PT = QT == 1 ? 2 : 3;
     __shared__ float lds_o[kAttnWaves][16][kPad];
     __shared__ float lds_m[kAttnWaves][16], lds_l[kAttnWaves][16];
-    __shared__ int64_t lds_plan[4];
-    __shared__ int64_t lds_at[2];
+    __shared__ WaveLds lds_w[kAttnWaves];
 
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int items = a.n_kv * a.row_tiles;
+    WaveLds &mem = lds_w[wave];
 
-    // this workgroup's range of the tiles of all (sequence, head, row tile)
-    const AttnPlan plan = attn_plan(a, lds_plan);
-    const int64_t total = plan.total * items;
-    const int64_t workers = attn_workers(a, total);
-    if (blockIdx.x >= workers) return;
-    const int64_t begin = attn_start(total, blockIdx.x, workers), end = attn_start(total, blockIdx.x + 1, workers);
-    {
-        const int64_t y = begin / items;
-        if (plan.before <= y && y < plan.before + plan.mine) {
-            int64_t before = plan.before;
-            int32_t b = tid * plan.each;
-            for (;; ++b) {
-                const int32_t n = attn_span(a, b).tiles;
-                if (y < before + n) break;
-                before += n;
-            }
-            lds_at[0] = b, lds_at[1] = before;
-        }
-        __syncthreads();
-    }
-    int32_t seq = __builtin_amdgcn_readfirstlane(static_cast<int32_t>(lds_at[0]));
-    AttnSpan span = attn_span(a, seq);
-    const int64_t rest = begin - lds_at[1] * items;
-    int32_t item = __builtin_amdgcn_readfirstlane(static_cast<int32_t>(rest / span.tiles));
-    int32_t tile = __builtin_amdgcn_readfirstlane(static_cast<int32_t>(rest - static_cast<int64_t>(item) * span.tiles));
+    const AttnPlan plan = attn_plan(a, blockIdx.x);
+    const int32_t begin = static_cast<int32_t>(blockIdx.x) * plan.each;
+    const int32_t end = plan.total - begin < plan.each ? plan.total : begin + plan.each;
+    AttnOpen open = {0, 0, 0, 0};
     bool bad = false;
+    int32_t seq = plan.seq, head = 0, tile = 0;
+    AttnSpan span = {};
+    if (begin < end) {
+        span = wave_span(a, seq);
+        const int32_t rest = begin - plan.before * a.n_kv;
+        head = static_cast<int32_t>(static_cast<uint32_t>(rest) / static_cast<uint32_t>(span.tiles));
+        head = head < a.n_kv ? head : a.n_kv - 1;      // (as in attn_plan)
+        tile = rest - head * span.tiles;
+        tile = tile < span.tiles ? tile : span.tiles - 1;
+    }
 
-    for (int64_t x = begin; x < end;) {
+    for (int32_t x = begin; x < end;) {
         const int32_t left = span.tiles - tile;
-        const int32_t n = end - x < left ? static_cast<int32_t>(end - x) : left;
-        const int32_t h = item / a.row_tiles, row0 = (item - h * a.row_tiles) * a.tile_rows;
-        const int32_t len = __builtin_amdgcn_readfirstlane(span.len);
+        const int32_t n = end - x < left ? end - x : left;
+        const int32_t row0 = static_cast<int32_t>(blockIdx.y) * a.tile_rows;
+        const int32_t len = span.len;
         const int32_t *table = a.table + seq * a.ld_table;
         bad |= span.bad;
 
+        const int32_t t0 = (span.first + tile) * kAttnTile + wave * kAttnSub;
+        const int32_t t1 = (span.first + tile + n) * kAttnTile < len ? (span.first + tile + n) * kAttnTile : len;
+        Look here = {0, 0};
+        if (t0 < t1) here = look_up(a, table, len, t0);
         u32x4 q[MT][QT][DP / 32];
-        load_queries<FMT, DP, MT, QT>(a, seq, h, row0, q);
+        load_queries<FMT, DP, MT, QT>(a, seq, head, row0, q);
         f32x4 acc[MT][DP / 16];
         float m[MT], l[MT];
         int32_t hi_t[MT];         // last position that the lane's row sees
@@ -340,12 +368,6 @@ __global__ __launch_bounds__(kAttnThreads, MT *DP *(QT == 1 ? 1 : 2) <= 128 ? 2 
         const int64_t all_lo = a.window > 0 ? static_cast<int64_t>(len) - a.window : 0;
         const int64_t any_lo = a.window > 0 ? static_cast<int64_t>(len) - a.q_len - a.window + 1 : 0;
 
-        const int32_t t0 = (span.first + tile) * kAttnTile + wave * kAttnSub;
-        const int32_t t1 = (span.first + tile + n) * kAttnTile < len ? (span.first + tile + n) * kAttnTile : len;
-        // A NaN or an infinity among the values can reach rows that do not see it (0 * inf) and turn
-        // hi * inf + lo * inf into NaN.  Both end in a NaN sum; a wave that finds one goes over its
-        // tokens once more, carefully.
-        for (bool careful = false;;) {
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
 #pragma unroll
@@ -355,13 +377,28 @@ __global__ __launch_bounds__(kAttnThreads, MT *DP *(QT == 1 ? 1 : 2) <= 128 ? 2 
         }
         Keys<FMT, DP> k;
         Values<FMT, DP> v;
-        Place<UNI> place;
+        uint32_t kb = 127, vb = 127, there_next = 0;
+        Look next = {0, 0};
         if (t0 < t1) {
-            place = find_tokens<UNI>(a, table, h, len, t0, bad);
-            load_keys<FMT, DP, UNI>(a, place, k);
+            there_next = find_tokens<FMT>(a, mem, here, head, len, t0, kb, vb, bad);
+            load_keys<FMT, DP>(a, mem, k);
+            next = look_up(a, table, len, t0 + kAttnTile);
         }
         for (int32_t t = t0; t < t1; t += kAttnTile) {
-            load_values<FMT, DP, UNI>(a, place, v);
+            const uint32_t there = there_next;
+            load_values<FMT, DP>(a, mem, v);
+            f32x4 ks[2], vs[2];
+            if constexpr (FMT == WSL_KV_E4M3) {
+                // (a byte of 255 is none that a write leaves; 254 keeps what it gives finite)
+                mem.ks[lane & 31] = __builtin_bit_cast(float, (kb < 254u ? kb : 254u) << 23);
+                mem.vs[lane & 31] = __builtin_bit_cast(float, (vb < 254u ? vb : 254u) << 23);
+                wave_lds_fence();
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    ks[i] = *reinterpret_cast<const f32x4 *>(&mem.ks[16 * i + 4 * g]);
+                    vs[i] = *reinterpret_cast<const f32x4 *>(&mem.vs[16 * i + 4 * g]);
+                }
+            }
             // scores
             f32x4 s[2][MT];
 #pragma unroll
@@ -371,35 +408,38 @@ __global__ __launch_bounds__(kAttnThreads, MT *DP *(QT == 1 ? 1 : 2) <= 128 ? 2 
 #pragma unroll
                 for (int c = 0; c < DP / 32; ++c) {
                     u32x4 kc;
+                    int d;
                     if constexpr (FMT == WSL_KV_BF16) {
                         kc = k.x[i][c];
+                        d = c * 32 + g * 8;
                     } else {
-                        const float sc = scale_of(k.e[i]);
                         const uint32_t w0 = k.x[i][c >> 1][(c & 1) * 2], w1 = k.x[i][c >> 1][(c & 1) * 2 + 1];
-                        kc = u32x4{fp8_pair(w0, sc, false), fp8_pair(w0, sc, true), fp8_pair(w1, sc, false),
-                                   fp8_pair(w1, sc, true)};
+                        kc = u32x4{fp8_pair(w0, false), fp8_pair(w0, true), fp8_pair(w1, false), fp8_pair(w1, true)};
+                        d = (c >> 1) * 64 + g * 16;
                     }
+                    const bool in = a.head_dim == DP || d < a.head_dim;     // else the load's place was made up
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) kc[e] = in ? kc[e] : 0;
 #pragma unroll
                     for (int j = 0; j < MT; ++j)
 #pragma unroll
                         for (int e = 0; e < QT; ++e) s[i][j] = mfma(kc, q[j][e][c], s[i][j]);
                 }
             }
-            // which of the lane's 8 tokens (values) are there at all
-            uint32_t there;
-            if constexpr (UNI) there = (place.ok[0] ? 0x0fu : 0u) | (place.ok[1] ? 0xf0u : 0u);
-            else there = place.vok;
             // the next keys, in flight under the softmax and the product with V
             if (t + kAttnTile < t1) {
-                place = find_tokens<UNI>(a, table, h, len, t + kAttnTile, bad);
-                load_keys<FMT, DP, UNI>(a, place, k);
+                there_next = find_tokens<FMT>(a, mem, next, head, len, t + kAttnTile, kb, vb, bad);
+                load_keys<FMT, DP>(a, mem, k);
+                if (t + 2 * kAttnTile < t1) next = look_up(a, table, len, t + 2 * kAttnTile);
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int j = 0; j < MT; ++j) s[i][j] *= a.scale_log2;
-            const bool whole = t + kAttnSub - 1 <= all_hi && t >= all_lo && __all(there == 0xffu);
-            bool mixed = false;
+                for (int j = 0; j < MT; ++j) {
+                    if constexpr (FMT == WSL_KV_E4M3) s[i][j] *= ks[i];
+                    s[i][j] *= a.scale_log2;
+                }
+            const bool whole = t + kAttnSub - 1 <= all_hi && t >= all_lo && there == 0xffffffffu;
             if (!whole) {
                 uint32_t keep = 0;
 #pragma unroll
@@ -407,9 +447,8 @@ __global__ __launch_bounds__(kAttnThreads, MT *DP *(QT == 1 ? 1 : 2) <= 128 ? 2 
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const int32_t at = t + 16 * i + 4 * g + r;
-                        const bool ok = ((there >> (4 * i + r)) & 1) && at < len && at >= any_lo;
+                        const bool ok = ((there >> (16 * i + 4 * g + r)) & 1) && at >= any_lo;
                         keep |= ok ? 1u << (4 * i + r) : 0u;
-                        mixed |= ok && (at > all_hi || at < all_lo);
 #pragma unroll
                         for (int j = 0; j < MT; ++j) {
                             const bool see = ok && at <= hi_t[j] && (a.window == 0 || at > hi_t[j] - a.window);
@@ -417,67 +456,62 @@ __global__ __launch_bounds__(kAttnThreads, MT *DP *(QT == 1 ? 1 : 2) <= 128 ? 2 
                         }
                     }
                 keep_values<FMT, DP>(v, keep);     // what no row sees may hold anything
-                mixed = __any(mixed);
             }
-            u32x4 p_hi[MT], p_lo[MT];
+            u32x4 p_t[MT][PT];
 #pragma unroll
             for (int j = 0; j < MT; ++j) {
                 float top = fmaxf(fmaxf(fmaxf(s[0][j][0], s[0][j][1]), fmaxf(s[0][j][2], s[0][j][3])),
                                   fmaxf(fmaxf(s[1][j][0], s[1][j][1]), fmaxf(s[1][j][2], s[1][j][3])));
                 top = fmaxf(top, __shfl_xor(top, 16, 64));
                 top = fmaxf(top, __shfl_xor(top, 32, 64));
-                const float next = fmaxf(m[j], top);
-                const float ref = next == -__builtin_huge_valf() ? 0.f : next;
-                if (__any(next != m[j])) {
+                const float best = fmaxf(m[j], top);
+                const float ref = best == -__builtin_huge_valf() ? 0.f : best;
+                if (__any(best != m[j])) {
                     const float f = __builtin_amdgcn_exp2f(m[j] - ref);
                     l[j] *= f;
 #pragma unroll
                     for (int d = 0; d < DP / 16; ++d) acc[j][d] *= f;
-                    m[j] = next;
+                    m[j] = best;
                 }
                 float p[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) p[i] = __builtin_amdgcn_exp2f(s[i >> 2][j][i & 3] - ref);
                 l[j] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+                if constexpr (FMT == WSL_KV_E4M3) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t b = pack_bf16x2(p[2 * i], p[2 * i + 1]);
-                    p_hi[j][i] = b;
-                    p_lo[j][i] = pack_bf16x2(p[2 * i] - bf16_lo(b), p[2 * i + 1] - bf16_hi(b));
+                    for (int i = 0; i < 8; ++i) p[i] *= vs[i >> 2][i & 3];
                 }
-            }
-            if (careful) {
-                // values that some rows see and others do not: one query position at a time
-                for (int32_t i = 0; i < (mixed ? a.q_len : 1); ++i) {
-                    const int32_t last = all_hi + i;
-                    uint32_t keep = 0, rows = 0;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int32_t at = t + 16 * (e >> 2) + 4 * g + (e & 3);
-                        keep |= !mixed || (at <= last && (a.window == 0 || at > last - a.window)) ? 1u << e : 0u;
+                for (int e = 0; e < PT; ++e)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t b = pack_bf16x2(p[2 * i], p[2 * i + 1]);
+                        p_t[j][e][i] = b;
+                        p[2 * i] -= bf16_lo(b);
+                        p[2 * i + 1] -= bf16_hi(b);
                     }
-#pragma unroll
-                    for (int j = 0; j < MT; ++j) rows |= !mixed || hi_t[j] == last ? 1u << j : 0u;
-                    add_values<FMT, DP, MT, true>(v, p_hi, p_lo, acc, keep, rows);
-                }
-            } else {
-                add_values<FMT, DP, MT, false>(v, p_hi, p_lo, acc, 0, 0);
             }
+            add_values<FMT, DP, MT, PT>(v, p_t, acc);
         }
-        if (careful) break;
+        // A NaN or an infinity among the values can reach rows that do not see it (0 * inf) and turn
+        // the sum of a weight's terms times it into NaN.  Both end in a NaN sum; a wave that finds
+        // one goes over its tokens once more, one by one.
+        bool odd = false;
 #pragma unroll
         for (int j = 0; j < MT; ++j)
 #pragma unroll
             for (int d = 0; d < DP / 16; ++d)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) careful |= acc[j][d][r] != acc[j][d][r];
-        careful = __any(careful);
-        if (!careful) break;
+                for (int r = 0; r < 4; ++r) odd |= acc[j][d][r] != acc[j][d][r];
+        if (__any(odd)) {
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+                again<FMT, DP>(a, table, seq, head, row0 + 16 * i + (lane & 15), len, t0, t1, hi_t[i], acc[i], m[i], l[i]);
         }
 
         // join the waves; then the rows are done, or partial where the item goes on elsewhere
         const bool full = tile == 0 && n == span.tiles;
-        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (tile == 0 ? 1 : 0);
+        const int64_t slot = (static_cast<int64_t>(blockIdx.y) * a.workers + blockIdx.x) * 2 + (tile == 0 ? 1 : 0);
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
             l[j] += __shfl_xor(l[j], 16, 64);
@@ -516,7 +550,7 @@ __global__ __launch_bounds__(kAttnThreads, MT *DP *(QT == 1 ? 1 : 2) <= 128 ? 2 
                         mx = fmaxf(mx, lds_m[w][r]);
                     }
                     if (full) {
-                        attn_finish(a, seq, len, h, row, d, make_float4(o.x, o.y, o.z, o.w), mx, sum);
+                        attn_finish(a, seq, head, row, d, o, mx, sum);
                     } else {
                         *reinterpret_cast<f32x4 *>(a.part_o + (slot * a.tile_rows + in_tile) * a.head_dim + d) = o;
                         if (d == 0) a.part_ml[slot * a.tile_rows + in_tile] = make_float2(mx, sum);
@@ -525,46 +559,50 @@ __global__ __launch_bounds__(kAttnThreads, MT *DP *(QT == 1 ? 1 : 2) <= 128 ? 2 
             }
             __syncthreads();
         }
+        if (tile == 0 && !full) {
+            const uint32_t last = static_cast<uint32_t>(x + span.tiles - 1) / static_cast<uint32_t>(plan.each);
+            open = {seq, head, static_cast<int32_t>(last) - static_cast<int32_t>(blockIdx.x) + 1, 0};
+        }
 
         x += n;
         tile = 0;
-        if (n == left && ++item == items) {
-            item = 0;
-            ++seq;
-            if (x < end) span = attn_span(a, seq);
+        if (n == left && ++head == a.n_kv) {
+            head = 0;
+            if (++seq >= a.n_seq) break;
+            if (x < end) span = wave_span(a, seq);
         }
     }
+    if (a.open != nullptr && blockIdx.y == 0 && tid == 0) a.open[blockIdx.x] = open;
     if (__any(bad) && lane == 0 && a.status != nullptr) atomicOr(a.status, WSL_STATUS_INDEX);
 }
 
+// Workgroups for all row tiles together fill the chip once.  Those of one token range lie `workers`
+// apart, a multiple of 8, so that they run at the same time on the same XCD and what one reads the
+// others find in its L2.
 template <int FMT, int DP, int MT, int QT>
-void go(const AttnArgs &a, bool uni, hipStream_t s) {
-    const dim3 grid(static_cast<unsigned>(a.workers)), block(kAttnThreads);
-    if (uni) hipLaunchKernelGGL((attn_kernel<FMT, DP, MT, QT, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((attn_kernel<FMT, DP, MT, QT, false>), grid, block, 0, s, a);
+void go(AttnArgs &a, hipStream_t s) {
+    const int fit = kAttnCus * attn_waves<FMT, DP, MT, QT>();
+    const int most = a.row_tiles * 8 >= fit ? 8 : fit / a.row_tiles / 8 * 8;
+    a.workers = a.workers < most ? a.workers : most;
+    hipLaunchKernelGGL((attn_kernel<FMT, DP, MT, QT>), dim3(static_cast<unsigned>(a.workers), static_cast<unsigned>(a.row_tiles)),
+                       dim3(kAttnThreads), 0, s, a);
 }
 
 template <int FMT, int DP>
-void go_rows(const AttnArgs &a, bool uni, int mt, hipStream_t s) {
-    if (a.qfmt == WSL_OUT_BF16) {
-        if (mt == 1) go<FMT, DP, 1, 1>(a, uni, s);
-        else if (mt == 2 || DP == 256) go<FMT, DP, 2, 1>(a, uni, s);
-        else if constexpr (DP < 256) go<FMT, DP, 4, 1>(a, uni, s);
-    } else {
-        if (mt == 1 || DP == 256) go<FMT, DP, 1, 3>(a, uni, s);
-        else if constexpr (DP < 256) go<FMT, DP, 2, 3>(a, uni, s);
-    }
+void go_rows(AttnArgs &a, int mt, hipStream_t s) {
+    if (a.qfmt != WSL_OUT_BF16) go<FMT, DP, 1, 3>(a, s);
+    else if (mt == 1 || DP > 128) go<FMT, DP, 1, 1>(a, s);
+    else if constexpr (DP <= 128) go<FMT, DP, 2, 1>(a, s);
 }
 
 }  // namespace
 
 template <int FMT>
-int launch_attn_fmt(const AttnArgs &a, int mt, hipStream_t s) {
-    // groups of 16 tokens that never leave a page, and reach less than 2 GiB
-    const bool uni = a.page_size % 16 == 0 && a.token_stride < (int64_t(1) << 26);
-    if (a.head_dim <= 64) go_rows<FMT, 64>(a, uni, mt, s);
-    else if (a.head_dim <= 128) go_rows<FMT, 128>(a, uni, mt, s);
-    else go_rows<FMT, 256>(a, uni, mt, s);
+int launch_attn_fmt(AttnArgs &a, int mt, hipStream_t s) {
+    if (a.head_dim <= 64) go_rows<FMT, 64>(a, mt, s);
+    else if (a.head_dim <= 128) go_rows<FMT, 128>(a, mt, s);
+    else if (a.head_dim <= 192) go_rows<FMT, 192>(a, mt, s);
+    else go_rows<FMT, 256>(a, mt, s);
     return WSL_OK;
 }
 
