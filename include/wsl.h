@@ -469,7 +469,8 @@ int attn_decode(const wsl_kv_cache *h_cache, const void *d_q, int qfmt, int64_t 
  * d_accepted device int32 [n_seq]: r.   d_tokens device int32 [n_seq][width + 1]: the r drafts
  *            that stand, the next token, then -1.  If the weights do not sum to a positive finite
  *            number the next token is -1 (WSL_STATUS_NONFINITE).
- * d_ws       device workspace, 8-byte aligned, of verify_drafts_workspace_bytes (else WSL_E_RANGE).
+ * d_ws       device workspace, 16-byte aligned, of verify_drafts_workspace_bytes (else WSL_E_RANGE;
+ *            none where that is 0: small vocabularies).
  *            Its contents on entry do not matter.  Calls that share a workspace must not overlap.
  */
 #define WSL_VERIFY_MAX_DRAFTS 64

@@ -102,8 +102,8 @@ def test_attn_workspace_sizes():
 def test_verify_refusals():
     L = wsl.lib()
 
-    def call(p=A, q=A, fmt=0, n=2, width=3, vocab=100, ld_p=100, ld_q=100, drafts=A, nd=None, u=A, acc=A, tok=A, ws=A,
-             nb=1 << 20):
+    def call(p=A, q=A, fmt=0, n=2, width=3, vocab=100, ld_p=100000, ld_q=100000, drafts=A, nd=None, u=A, acc=A, tok=A,
+             ws=A, nb=1 << 20):
         return L.verify_drafts(p, q, fmt, n, width, vocab, ld_p, ld_q, drafts, nd, u, acc, tok, ws, nb, None, None)
 
     assert call(n=0, p=None, u=None) == OK
@@ -112,10 +112,12 @@ def test_verify_refusals():
     assert call(vocab=0) == SHAPE and call(vocab=(1 << 30) + 1) == SHAPE
     assert call(p=None) == NULL and call(drafts=None) == NULL and call(u=None) == NULL
     assert call(acc=None) == NULL and call(tok=None) == NULL
-    assert call(ld_p=99) == SHAPE and call(ld_q=99) == SHAPE
+    assert call(ld_p=99) == SHAPE and call(ld_q=99) == SHAPE and call(vocab=100001) == SHAPE
     assert call(p=4098) == ALIGN and call(q=ODD) == ALIGN and call(drafts=4098) == ALIGN and call(nd=ODD) == ALIGN
-    assert call(ws=None) == NULL and call(ws=4100) == ALIGN
-    assert call(nb=wsl.verify_drafts_workspace_bytes(2, 100) - 1) == RANGE
+    big = 100000
+    assert call(vocab=big, ws=None) == NULL and call(vocab=big, ws=4104) == ALIGN
+    assert call(vocab=big, nb=wsl.verify_drafts_workspace_bytes(2, big) - 1) == RANGE
+    assert wsl.verify_drafts_workspace_bytes(2, 100) == 0       # one launch, nothing to keep between two
     assert wsl.verify_drafts_workspace_bytes(0, 100) == 0 == wsl.verify_drafts_workspace_bytes(3, 0)
 
 

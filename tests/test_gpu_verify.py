@@ -49,7 +49,8 @@ def _check(p, q, drafts, u, n_drafts=None, **kw):
 @pytest.mark.parametrize("one_hot", [False, True])
 @pytest.mark.parametrize("n,width,vocab,pad", [
     (1, 4, 1000, 0), (7, 3, 1, 0), (5, 0, 4097, 0), (64, 2, 4096, 0), (3, 12, 8191, 3), (2, 64, 501, 1),
-    (16, 1, 32000, 0), (4, 5, 151937, 7)])
+    (16, 1, 32000, 0), (4, 5, 151937, 7), (3, 2, 1024, 1), (3, 2, 1025, 1), (2, 3, 2049, 0), (2, 1, 32768, 0),
+    (2, 1, 32769, 1), (33, 2, 65536, 3)])
 def test_against_the_definition(n, width, vocab, pad, bf16, one_hot):
     say(f"verify n={n} width={width} vocab={vocab} pad={pad} bf16={bf16} one_hot={one_hot}")
     for seed in range(3):
@@ -73,12 +74,13 @@ def test_ragged_drafts_and_bad_ones():
             assert acc[4] == 2 and st.item() == wsl.WSL_STATUS_INDEX
 
 
-def test_borders():
+@pytest.mark.parametrize("step", [1024, 1000, 7, 8192])
+def test_borders(step):
     """Dyadic probabilities, so that every sum is exact: ties and the borders of each token."""
     import torch
-    vocab = 8192
+    vocab = 8 * step
     p = torch.zeros(1, 2, vocab, device="cuda")
-    p[0, :, ::1024] = 0.125              # 8 tokens of 1/8: 0, 1024, ..
+    p[0, :, ::step] = 0.125              # 8 tokens of 1/8: 0, step, ..
     q = torch.zeros(1, 1, vocab, device="cuda")
     q[0, 0, 0], q[0, 0, 5] = 0.25, 0.75
     d0 = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
@@ -87,17 +89,17 @@ def test_borders():
         assert acc[0] == stands
     for i in range(8):                   # after acceptance: 8 equal parts; the border belongs to the next
         _, tok = _check(p, q, d0, torch.tensor([[0.0, i / 8]], device="cuda"))
-        assert tok[0, 1] == 1024 * i
+        assert tok[0, 1] == step * i
     for u1 in (1.0, 2.0, -1.0, float("nan"), float(np.nextafter(np.float32(1), np.float32(0)))):
         _check(p, q, d0, torch.tensor([[0.0, u1]], device="cuda"))
         _check(p, q, d0, torch.tensor([[0.9, u1]], device="cuda"))
     # nothing left of p once q is off it: p itself
     _, tok = _check(p, p[:, :1].contiguous(), d0 + 1, torch.tensor([[0.5, 0.99]], device="cuda"))
-    assert tok[0, 0] == 7168
+    assert tok[0, 0] == 7 * step
     # a drafter that was certain of a token that p gives everything
     sure = torch.zeros(1, 2, vocab, device="cuda")
-    sure[0, :, 77] = 1.0
-    _check(sure, None, d0 + 77, torch.tensor([[1.0, 0.3]], device="cuda"))
+    sure[0, :, 37] = 1.0
+    _check(sure, None, d0 + 37, torch.tensor([[1.0, 0.3]], device="cuda"))
 
 
 def test_rows_that_give_nothing():
@@ -126,11 +128,12 @@ def test_a_large_vocabulary():
         _check(p, q, torch.tensor([[7], [9]], dtype=torch.int32, device="cuda"), u)
 
 
-def test_streams_graphs_and_workspaces():
+@pytest.mark.parametrize("vocab", [20011, 40009])
+def test_streams_graphs_and_workspaces(vocab):
     import torch
-    p, q, drafts, u = _case(3, 6, 4, 20011, False, False)
+    p, q, drafts, u = _case(3, 6, 4, vocab, False, False)
     want = _want(p, q, drafts, u)
-    ws = torch.full((wsl.verify_drafts_workspace_bytes(6, 20011) // 8,), float("nan"), dtype=torch.float64, device="cuda")
+    ws = torch.full((wsl.verify_drafts_workspace_bytes(6, vocab) // 8,), float("nan"), dtype=torch.float64, device="cuda")
     torch.cuda.synchronize()
     s = torch.cuda.Stream()
     acc, tok = wsl.verify_drafts(p, q, drafts, u, workspace=ws, stream=s)

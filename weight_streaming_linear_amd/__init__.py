@@ -19,6 +19,7 @@ Entry points (same names as the C ABI):
 """
 
 import ctypes
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -132,7 +133,7 @@ def _check(rc, where):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _require(t, name, dtypes, device=None, contiguous=False, ndim=None):
@@ -148,9 +149,10 @@ def _require(t, name, dtypes, device=None, contiguous=False, ndim=None):
         raise ValueError(f"{name}: on {t.device}, expected {device}")
     if ndim is not None and t.dim() != ndim:
         raise ValueError(f"{name}: expected {ndim} dimensions, got shape {tuple(t.shape)}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-    if t.dim() > 0 and t.numel() > 1 and t.stride(-1) != 1:
+    if contiguous:
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: must be contiguous")
+    elif t.dim() > 0 and t.numel() > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name}: last dimension must have stride 1 (got strides {t.stride()})")
 
 
@@ -172,10 +174,12 @@ def _weight(w, wfmt, n_out, k, name="w"):
 
 
 def _stream(stream):
-    import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    """The handle of a stream, or of the current one.  That one is asked for as a number: making a
+    Stream object of it takes 2.7 us of the host, as long as a launch."""
+    if stream is not None:
+        return stream.cuda_stream
+    from torch import _C
+    return _C._cuda_getCurrentRawStream(_C._cuda_getDevice())
 
 
 # ---------------------------------------------------------------- format helpers
@@ -547,6 +551,7 @@ def kv_cache_read(cache, slots, k=None, v=None, ofmt=WSL_OUT_BF16, status=None, 
     return k, v
 
 
+@functools.lru_cache(maxsize=256)
 def attn_decode_workspace_bytes(qfmt, n_seq, q_len, n_heads, n_kv, head_dim, pages_per_seq, page_size):
     return int(lib().attn_decode_workspace_bytes(int(qfmt), int(n_seq), int(q_len), int(n_heads), int(n_kv),
                                                  int(head_dim), int(pages_per_seq), int(page_size)))
@@ -574,7 +579,10 @@ def attn_decode(cache, q, block_table, kv_lens, scale=None, window=0, out=None, 
         raise ValueError(f"{n_seq} sequences, block_table {tuple(block_table.shape)}, kv_lens {tuple(kv_lens.shape)}")
     ofmt = (qfmt if out is None else _float_format(out, "out")) if ofmt is None else int(ofmt)
     if out is None:
-        out = _new(shape, _float_dtype(ofmt), dev, stream)
+        if ofmt == qfmt and stream is None:
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        else:
+            out = _new(shape, _float_dtype(ofmt), dev, stream)
     elif out.dtype != _float_dtype(ofmt):
         raise ValueError(f"out: dtype {out.dtype}, expected {_float_dtype(ofmt)}")
     ld_out = _head_rows(out, "out", dev, shape)
@@ -585,10 +593,9 @@ def attn_decode(cache, q, block_table, kv_lens, scale=None, window=0, out=None, 
     _status(status, dev)
     L = lib()
     if workspace is None:
-        need = L.attn_decode_workspace_bytes(qfmt, n_seq, q_len, n_heads, cache.n_kv, dim, pages, cache.page_size)
-        ws_bytes = need
-        if need:
-            workspace = _new(need, torch.uint8, dev, stream)
+        ws_bytes = attn_decode_workspace_bytes(qfmt, n_seq, q_len, n_heads, cache.n_kv, dim, pages, cache.page_size)
+        if ws_bytes:
+            workspace = _new(ws_bytes, torch.uint8, dev, stream)
     else:
         _require(workspace, "workspace", (workspace.dtype,), device=dev, contiguous=True)
         ws_bytes = workspace.numel() * workspace.element_size()
@@ -600,6 +607,7 @@ def attn_decode(cache, q, block_table, kv_lens, scale=None, window=0, out=None, 
     return out
 
 
+@functools.lru_cache(maxsize=256)
 def verify_drafts_workspace_bytes(n_seq, vocab):
     return int(lib().verify_drafts_workspace_bytes(int(n_seq), int(vocab)))
 
@@ -657,7 +665,7 @@ def verify_drafts(p, q, drafts, u, n_drafts=None, accepted=None, tokens=None, wo
         tokens = _new((n_seq, rows), torch.int32, dev, stream)
     L = lib()
     if workspace is None:
-        ws_bytes = L.verify_drafts_workspace_bytes(n_seq, vocab)
+        ws_bytes = verify_drafts_workspace_bytes(n_seq, vocab)
         if ws_bytes:
             workspace = _new(ws_bytes, torch.uint8, dev, stream)
     else:

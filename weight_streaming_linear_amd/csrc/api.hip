@@ -247,7 +247,7 @@ int verify_drafts(const void *d_p, const void *d_q, int pfmt, int64_t n_seq, int
     int rc = wsl::check_verify(d_p, d_q, pfmt, n_seq, width, vocab, ld_p, ld_q, d_drafts, d_n_drafts, d_u, d_accepted,
                                d_tokens);
     if (rc != WSL_OK || n_seq == 0) return rc;
-    if ((rc = wsl::check_workspace(d_ws, ws_bytes, wsl::verify_ws_bytes(n_seq, vocab), 8)) != WSL_OK) return rc;
+    if ((rc = wsl::check_workspace(d_ws, ws_bytes, wsl::verify_ws_bytes(n_seq, vocab), 16)) != WSL_OK) return rc;
     if ((rc = wsl::device_ok()) != WSL_OK) return rc;
     return wsl::after_launch(wsl::launch_verify(d_p, d_q, pfmt, n_seq, width, vocab, ld_p, ld_q, d_drafts, d_n_drafts,
                                                 d_u, d_accepted, d_tokens, d_ws, d_status, wsl::as_stream(stream)));
