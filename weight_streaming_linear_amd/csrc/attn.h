@@ -14,9 +14,9 @@ constexpr int kAttnMaxWaves = 4;                   // of a SIMD, over all varian
 constexpr int64_t kAttnMaxTokens = 0x7fffffff - 4 * kAttnTile;   // positions stay in 32 bits some rounds past the end
 constexpr int kAttnJoinRows = 4;                   // rows a workgroup of the joining kernel takes
 
-// An item that a workgroup began and others go on with: its sequence, kv head and workgroups.
+// What became of an item: the worker that began it and how many workers hold parts of it.
 struct AttnOpen {
-    int32_t seq, head, parts, pad;
+    int32_t seq, head, worker, parts;
 };
 
 struct AttnArgs {
@@ -27,7 +27,7 @@ struct AttnArgs {
     float *lse;
     float *part_o;        // [row_tiles][2 * workers][tile_rows][head_dim]: unnormalised sums
     float2 *part_ml;      // [row_tiles][2 * workers][tile_rows]: running maximum (log2 domain) and sum
-    AttnOpen *open;       // [workers]; null where nothing can be split
+    AttnOpen *open;       // of each item, or of the last one that each worker began; null if nothing can be split
     const int32_t *table, *lens;
     uint32_t *status;
     int64_t page_stride, head_stride, token_stride;   // bytes
@@ -37,6 +37,7 @@ struct AttnArgs {
     int32_t capacity;     // tokens a table row can name
     int32_t n_seq, q_len, n_kv, group, rows, head_dim, page_size, n_pages;
     int32_t row_tiles, tile_rows, workers, qfmt, ofmt;
+    int32_t by_item;      // how `open` is indexed: by whichever there are fewer of
 };
 
 // A sequence's length and the token tiles that some row of it sees.  A sequence with nothing to see

@@ -5,58 +5,74 @@
 namespace wsl {
 namespace {
 
-// Workgroup (w, y) joins rows y * kAttnJoinRows .. of the item that worker w began and left open,
-// if there is one: with the parts' maxima m_i, sums l_i and O_i, M = max m_i, the result is
-// sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.  Parts are split over the threads as well (one after
-// the other they would be that many trips to memory), each thread takes every kGroups-th of them,
-// and the groups are added in order.
-constexpr int kJoinThreads = 512;
-__global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a) {
-    __shared__ f32x4 lds_o[kJoinThreads];
-    __shared__ float lds_l[kJoinThreads];
-    const int32_t w = static_cast<int32_t>(blockIdx.x);
-    const AttnOpen it = a.open[w];
+// Workgroup (i, y) joins rows y * kAttnJoinRows .. of the item of entry i, if it has several parts: with the parts' maxima m_i, sums l_i and O_i, M = max m_i, the result is
+// sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.  Bound by trips to memory, so the parts are split over
+// groups of threads, each of which asks for several at a time and keeps a running maximum; the
+// groups are then joined in order.
+constexpr int kJoinMany = 1024, kJoinFew = 256, kJoinAhead = 4;
+constexpr int kJoinLds = sizeof(f32x4) + 2 * sizeof(float);  // of a thread
+__global__ __launch_bounds__(kJoinMany) void attn_join_kernel(AttnArgs a) {
+    extern __shared__ f32x4 lds_o[];
+    const int threads = static_cast<int>(blockDim.x);
+    float *lds_m = reinterpret_cast<float *>(lds_o + threads), *lds_l = lds_m + threads;
+    AttnOpen it = a.open[blockIdx.x];
+    // (never so unless the lengths changed while the workers read them, and an item was nobody's)
+    if (it.worker < 0 || it.worker >= a.workers || it.parts > a.workers - it.worker) return;
     if (it.parts <= 1) return;
+    const int32_t w = it.worker;
+    if (a.by_item) {
+        it.seq = static_cast<int32_t>(blockIdx.x) / a.n_kv;
+        it.head = static_cast<int32_t>(blockIdx.x) - it.seq * a.n_kv;
+    }
     const int tid = static_cast<int>(threadIdx.x);
     const int per_row = a.head_dim / 4, cells = kAttnJoinRows * per_row;
-    const int groups = kJoinThreads / cells;                 // 2 .. 32
+    const int groups = threads / cells;                      // 1 .. 64
     const int grp = tid / cells, cell = tid - grp * cells, r = cell / per_row, d = (cell - r * per_row) * 4;
     const int32_t row = static_cast<int32_t>(blockIdx.y) * kAttnJoinRows + r;
     const bool in = grp < groups && row < a.rows;
     const int32_t rt = row / a.tile_rows, in_tile = row - rt * a.tile_rows;
     // worker w holds the item's beginning (its second slot), the others go on (their first)
     const int64_t base = static_cast<int64_t>(rt) * a.workers * 2;
-    float top = -__builtin_huge_valf();
+    float top = -__builtin_huge_valf(), l = 0.f;
     f32x4 o = {0, 0, 0, 0};
-    float l = 0.f;
-    if (in) {
-#pragma unroll 4
-        for (int32_t i = 0; i < it.parts; ++i)
-            top = fmaxf(top, a.part_ml[(base + 2 * (w + i) + (i == 0)) * a.tile_rows + in_tile].x);
-        const float ref = top == -__builtin_huge_valf() ? 0.f : top;
-#pragma unroll 4
-        for (int32_t i = grp; i < it.parts; i += groups) {
-            const int64_t at = (base + 2 * (w + i) + (i == 0)) * a.tile_rows + in_tile;
-            const float2 ml = a.part_ml[at];
-            const float f = __builtin_amdgcn_exp2f(ml.x - ref);
-            o += *reinterpret_cast<const f32x4 *>(a.part_o + at * a.head_dim + d) * f;
-            l += ml.y * f;
+    auto add = [&](float m1, float l1, f32x4 o1) {
+        const float best = fmaxf(top, m1), ref = best == -__builtin_huge_valf() ? 0.f : best;
+        const float f0 = __builtin_amdgcn_exp2f(top - ref), f1 = __builtin_amdgcn_exp2f(m1 - ref);
+        o = o * f0 + o1 * f1;
+        l = l * f0 + l1 * f1;
+        top = best;
+    };
+    if (in)
+        for (int32_t i0 = grp; i0 < it.parts; i0 += groups * kJoinAhead) {
+            float2 ml[kJoinAhead];
+            f32x4 po[kJoinAhead];
+#pragma unroll
+            for (int e = 0; e < kJoinAhead; ++e) {
+                const int32_t i = i0 + e * groups;
+                const int64_t at = (base + 2 * (w + i) + (i == 0)) * a.tile_rows + in_tile;
+                ml[e] = make_float2(-__builtin_huge_valf(), 0.f);
+                po[e] = f32x4{0, 0, 0, 0};
+                if (i < it.parts) {
+                    ml[e] = a.part_ml[at];
+                    po[e] = *reinterpret_cast<const f32x4 *>(a.part_o + at * a.head_dim + d);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < kJoinAhead; ++e) add(ml[e].x, ml[e].y, po[e]);
         }
-    }
     lds_o[tid] = o;
+    lds_m[tid] = top;
     lds_l[tid] = l;
     __syncthreads();
     if (!in || grp != 0) return;
-    for (int i = 1; i < groups; ++i) {
-        o += lds_o[i * cells + cell];
-        l += lds_l[i * cells + cell];
-    }
+    const int n = groups < it.parts ? groups : it.parts;
+    for (int i = 1; i < n; ++i) add(lds_m[i * cells + cell], lds_l[i * cells + cell], lds_o[i * cells + cell]);
     attn_finish(a, it.seq, it.head, row, d, o, top, l);
 }
 
 struct AttnShape {
     int mt, tile_rows, row_tiles;
-    int64_t workers;          // at most
+    int64_t workers, entries; // at most
     bool may_split;
 };
 
@@ -71,6 +87,7 @@ AttnShape shape_of(int qfmt, int64_t n_seq, int64_t rows, int64_t n_kv, int64_t 
     const int64_t items = n_seq * n_kv, most = s.row_tiles * 8 >= fit ? 8 : fit / s.row_tiles / 8 * 8;
     s.may_split = tiles > 1;
     s.workers = tiles >= most || items >= most || items * tiles >= most ? most : items * tiles;
+    s.entries = items < s.workers ? items : s.workers;
     return s;
 }
 
@@ -84,7 +101,7 @@ size_t attn_ws_bytes(int qfmt, int64_t n_seq, int64_t rows, int64_t n_kv, int64_
     const AttnShape s = shape_of(qfmt, n_seq, rows, n_kv, head_dim, capacity);
     if (!s.may_split) return 0;
     return parts_of(s) * (static_cast<size_t>(head_dim) * sizeof(float) + sizeof(float2)) +
-           static_cast<size_t>(s.workers) * sizeof(AttnOpen);
+           static_cast<size_t>(s.entries) * sizeof(AttnOpen);
 }
 
 int launch_attn(const wsl_kv_cache *c, const void *q, int qfmt, int64_t n_seq, int64_t q_len, int64_t n_heads,
@@ -111,14 +128,19 @@ int launch_attn(const wsl_kv_cache *c, const void *q, int qfmt, int64_t n_seq, i
     // the parts' sums first (16-byte aligned), then the open items, then the parts' maxima and sums
     a.part_o = static_cast<float *>(ws);
     a.open = sh.may_split ? reinterpret_cast<AttnOpen *>(a.part_o + parts_of(sh) * c->head_dim) : nullptr;
-    a.part_ml = sh.may_split ? reinterpret_cast<float2 *>(a.open + sh.workers) : nullptr;
+    a.part_ml = sh.may_split ? reinterpret_cast<float2 *>(a.open + sh.entries) : nullptr;
+    a.by_item = n_seq * c->n_kv <= sh.workers ? 1 : 0;
     if (c->fmt == WSL_KV_BF16) launch_attn_fmt<WSL_KV_BF16>(a, sh.mt, s);
     else launch_attn_fmt<WSL_KV_E4M3>(a, sh.mt, s);
-    if (sh.may_split)
+    if (sh.may_split) {
+        // A few long sequences leave items in many parts, many sequences leave many items in two or
+        // three.  MEASURE
+        const int threads = a.workers >= 16 * n_seq * c->n_kv ? kJoinMany : kJoinFew;
         hipLaunchKernelGGL(attn_join_kernel,
-                           dim3(static_cast<unsigned>(a.workers),
+                           dim3(static_cast<unsigned>(a.by_item ? n_seq * c->n_kv : a.workers),
                                 static_cast<unsigned>((rows + kAttnJoinRows - 1) / kAttnJoinRows)),
-                           dim3(kJoinThreads), 0, s, a);
+                           dim3(threads), threads * kJoinLds, s, a);
+    }
     return WSL_OK;
 }
 

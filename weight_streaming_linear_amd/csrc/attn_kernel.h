@@ -14,6 +14,19 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(b), c, 0, 0, 0);
 }
 
+// The lane's number and the kernel's arguments, made out anew: what is derived from them for an item's
+// end or a rare case is not computed before the loop over the tokens and held in registers throughout
+// (that took 80 vector registers and spilled as many scalar ones).
+__device__ __forceinline__ int fresh(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+__device__ __forceinline__ const AttnArgs &fresh_args() {
+    auto p = __builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return *(const AttnArgs *)p;
+}
+
 // Two bf16 numbers of two e4m3 codes (exact).
 __device__ __forceinline__ uint32_t fp8_pair(uint32_t w, bool hi) {
     return hi ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.f, true))
@@ -88,7 +101,8 @@ __device__ __forceinline__ uint32_t find_tokens(const AttnArgs &a, WaveLds &w, c
 
 // Keys as the A operand of S^T = K Q^T: lane l holds key l % 16 and, of its head_dim, the
 // 8 consecutive elements per matrix instruction that lane group l / 16 owns.
-template <int FMT, int DP>
+// FULL: head_dim is DP; else the places past it are read from the row's beginning and dropped.
+template <int FMT, int DP, bool FULL>
 __device__ __forceinline__ void load_keys(const AttnArgs &a, const WaveLds &w, Keys<FMT, DP> &k) {
     const int lane = static_cast<int>(threadIdx.x & 63);
     constexpr int kElem = FMT == WSL_KV_BF16 ? 2 : 1, kPer = 16 / kElem;    // elements of a 16-byte load
@@ -98,15 +112,18 @@ __device__ __forceinline__ void load_keys(const AttnArgs &a, const WaveLds &w, K
 #pragma unroll
         for (int c = 0; c < Keys<FMT, DP>::kLoads; ++c) {
             const int d = c * 4 * kPer + (lane >> 4) * kPer;
-            k.x[i][c] = *reinterpret_cast<const u32x4 *>(row + (d < a.head_dim ? d : 0) * kElem);
+            k.x[i][c] = *reinterpret_cast<const u32x4 *>(row + (FULL || d < a.head_dim ? d : 0) * kElem);
         }
     }
 }
 
 // Values for the A operand of O^T = V^T P: lane l takes its group's 8 tokens (those whose scores
 // S^T leaves in this lane) and, of each, the kVec elements that start at (l % 16) * kVec: whole
-// rows are read in order, and the 8 x kVec block is transposed inside the lane.
-template <int FMT, int DP>
+// rows are read in order, and the 8 x kVec block is transposed inside the lane.  They are streamed: a
+// line of values is read by one instruction once, where one of keys is read by two.  (Keys and values
+// streamed alike, or neither: 44, 42 against 39 us for 16 sequences of up to 4224 tokens with five
+// queries, 48, 52 against 47 us for 32 of up to 8192 in e4m3.)
+template <int FMT, int DP, bool FULL>
 __device__ __forceinline__ void load_values(const AttnArgs &a, const WaveLds &w, Values<FMT, DP> &v) {
     typedef Values<FMT, DP> V;
     const int lane = static_cast<int>(threadIdx.x & 63);
@@ -117,16 +134,16 @@ __device__ __forceinline__ void load_values(const AttnArgs &a, const WaveLds &w,
 #pragma unroll
         for (int n = 0; n < V::kLoads; ++n) {
             int d = n * 16 * V::kVec + (lane & 15) * V::kVec;
-            d = d < a.head_dim ? d : 0;              // columns past head_dim: computed, never written
+            d = FULL || d < a.head_dim ? d : 0;      // columns past head_dim: computed, never written
             const uint32_t *src = reinterpret_cast<const uint32_t *>(row + d * kElem);
             if constexpr (V::kWords == 4) {
-                const u32x4 x = *reinterpret_cast<const u32x4 *>(src);
+                const u32x4 x = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(src));
                 v.x[i][n][0] = x.x, v.x[i][n][1] = x.y, v.x[i][n][2] = x.z, v.x[i][n][3] = x.w;
             } else if constexpr (V::kWords == 2) {
-                const u32x2 x = *reinterpret_cast<const u32x2 *>(src);
+                const u32x2 x = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(src));
                 v.x[i][n][0] = x.x, v.x[i][n][1] = x.y;
             } else {
-                v.x[i][n][0] = src[0];
+                v.x[i][n][0] = __builtin_nontemporal_load(src);
             }
         }
     }
@@ -239,11 +256,12 @@ __device__ __forceinline__ float element(const char *row, int32_t d, float scale
 // A wave's part of one row block (the lane's row), token by token in fp32: a row's sums take nothing
 // from a token that it does not see.  Only for tokens among which a NaN or an infinity was found.
 template <int FMT, int DP>
-__device__ __forceinline__ void again(const AttnArgs &a, const int32_t *table, int32_t seq, int32_t h, int32_t row,
+__device__ __forceinline__ void again(const int32_t *table, int32_t seq, int32_t h, int32_t row,
                                       int32_t len, int32_t t0, int32_t t1, int32_t hi, f32x4 (&acc)[DP / 16], float &m,
                                       float &l) {
     constexpr int kVec = Values<FMT, DP>::kVec;
-    const int g = static_cast<int>(threadIdx.x & 63) >> 4;
+    const AttnArgs &a = fresh_args();
+    const int g = fresh(static_cast<int>(threadIdx.x & 63)) >> 4;
     const int32_t pos = row < a.rows ? row / a.group : 0, head = h * a.group + (row < a.rows ? row - pos * a.group : 0);
     const int64_t at_q = (static_cast<int64_t>(seq) * a.q_len + pos) * a.ld_q + static_cast<int64_t>(head) * a.head_dim;
     m = -__builtin_huge_valf();
@@ -314,7 +332,7 @@ constexpr int attn_waves() {
 // Each wave works on 32 tokens of its own in a round, and the four join at an item's end.  In a
 // round it asks for this round's values, then works on the keys that it asked for a round before,
 // asks for the next round's keys and the table's entries for the round after that.
-template <int FMT, int DP, int MT, int QT>
+template <int FMT, int DP, int MT, int QT, bool FULL>
 __global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void attn_kernel(AttnArgs a) {
     constexpr int kPad = DP + 4, PT = QT == 1 ? 2 : 3;
     __shared__ float lds_o[kAttnWaves][16][kPad];
@@ -328,7 +346,7 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void
     const AttnPlan plan = attn_plan(a, blockIdx.x);
     const int32_t begin = static_cast<int32_t>(blockIdx.x) * plan.each;
     const int32_t end = plan.total - begin < plan.each ? plan.total : begin + plan.each;
-    AttnOpen open = {0, 0, 0, 0};
+    AttnOpen open = {0, 0, 0, 1};
     bool bad = false;
     int32_t seq = plan.seq, head = 0, tile = 0;
     AttnSpan span = {};
@@ -372,21 +390,25 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void
         for (int i = 0; i < MT; ++i) {
 #pragma unroll
             for (int j = 0; j < DP / 16; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < DP / 16; ++j) asm volatile("" : "+v"(acc[i][j]));   // now, not after the first loads
             m[i] = -__builtin_huge_valf();
             l[i] = 0.f;
         }
+        __builtin_amdgcn_sched_barrier(0);
         Keys<FMT, DP> k;
         Values<FMT, DP> v;
         uint32_t kb = 127, vb = 127, there_next = 0;
         Look next = {0, 0};
         if (t0 < t1) {
             there_next = find_tokens<FMT>(a, mem, here, head, len, t0, kb, vb, bad);
-            load_keys<FMT, DP>(a, mem, k);
+            load_keys<FMT, DP, FULL>(a, mem, k);
             next = look_up(a, table, len, t0 + kAttnTile);
         }
         for (int32_t t = t0; t < t1; t += kAttnTile) {
             const uint32_t there = there_next;
-            load_values<FMT, DP>(a, mem, v);
+            load_values<FMT, DP, FULL>(a, mem, v);
+            __builtin_amdgcn_sched_barrier(0);       // asked for before anything waits for the keys
             f32x4 ks[2], vs[2];
             if constexpr (FMT == WSL_KV_E4M3) {
                 // (a byte of 255 is none that a write leaves; 254 keeps what it gives finite)
@@ -417,9 +439,10 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void
                         kc = u32x4{fp8_pair(w0, false), fp8_pair(w0, true), fp8_pair(w1, false), fp8_pair(w1, true)};
                         d = (c >> 1) * 64 + g * 16;
                     }
-                    const bool in = a.head_dim == DP || d < a.head_dim;     // else the load's place was made up
+                    if constexpr (!FULL) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) kc[e] = in ? kc[e] : 0;
+                        for (int e = 0; e < 4; ++e) kc[e] = d < a.head_dim ? kc[e] : 0;
+                    }
 #pragma unroll
                     for (int j = 0; j < MT; ++j)
 #pragma unroll
@@ -429,7 +452,7 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void
             // the next keys, in flight under the softmax and the product with V
             if (t + kAttnTile < t1) {
                 there_next = find_tokens<FMT>(a, mem, next, head, len, t + kAttnTile, kb, vb, bad);
-                load_keys<FMT, DP>(a, mem, k);
+                load_keys<FMT, DP, FULL>(a, mem, k);
                 if (t + 2 * kAttnTile < t1) next = look_up(a, table, len, t + 2 * kAttnTile);
             }
 #pragma unroll
@@ -506,10 +529,13 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void
         if (__any(odd)) {
 #pragma unroll
             for (int i = 0; i < MT; ++i)
-                again<FMT, DP>(a, table, seq, head, row0 + 16 * i + (lane & 15), len, t0, t1, hi_t[i], acc[i], m[i], l[i]);
+                again<FMT, DP>(table, seq, head, row0 + 16 * i + fresh(lane & 15), len, t0, t1, hi_t[i], acc[i], m[i], l[i]);
         }
 
         // join the waves; then the rows are done, or partial where the item goes on elsewhere
+        {
+        const AttnArgs &a = fresh_args();
+        const int tid = fresh(static_cast<int>(threadIdx.x)), lane = tid & 63, g = lane >> 4;
         const bool full = tile == 0 && n == span.tiles;
         const int64_t slot = (static_cast<int64_t>(blockIdx.y) * a.workers + blockIdx.x) * 2 + (tile == 0 ? 1 : 0);
 #pragma unroll
@@ -559,9 +585,11 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void
             }
             __syncthreads();
         }
-        if (tile == 0 && !full) {
+        if (tile == 0) {
             const uint32_t last = static_cast<uint32_t>(x + span.tiles - 1) / static_cast<uint32_t>(plan.each);
-            open = {seq, head, static_cast<int32_t>(last) - static_cast<int32_t>(blockIdx.x) + 1, 0};
+            open = {seq, head, static_cast<int32_t>(blockIdx.x), static_cast<int32_t>(last - blockIdx.x) + 1};
+            if (a.open != nullptr && a.by_item && blockIdx.y == 0 && tid == 0) a.open[seq * a.n_kv + head] = open;
+        }
         }
 
         x += n;
@@ -572,7 +600,7 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void
             if (x < end) span = wave_span(a, seq);
         }
     }
-    if (a.open != nullptr && blockIdx.y == 0 && tid == 0) a.open[blockIdx.x] = open;
+    if (a.open != nullptr && !a.by_item && blockIdx.y == 0 && tid == 0) a.open[blockIdx.x] = open;
     if (__any(bad) && lane == 0 && a.status != nullptr) atomicOr(a.status, WSL_STATUS_INDEX);
 }
 
@@ -584,8 +612,9 @@ void go(AttnArgs &a, hipStream_t s) {
     const int fit = kAttnCus * attn_waves<FMT, DP, MT, QT>();
     const int most = a.row_tiles * 8 >= fit ? 8 : fit / a.row_tiles / 8 * 8;
     a.workers = a.workers < most ? a.workers : most;
-    hipLaunchKernelGGL((attn_kernel<FMT, DP, MT, QT>), dim3(static_cast<unsigned>(a.workers), static_cast<unsigned>(a.row_tiles)),
-                       dim3(kAttnThreads), 0, s, a);
+    const dim3 grid(static_cast<unsigned>(a.workers), static_cast<unsigned>(a.row_tiles));
+    if (a.head_dim == DP) hipLaunchKernelGGL((attn_kernel<FMT, DP, MT, QT, true>), grid, dim3(kAttnThreads), 0, s, a);
+    else hipLaunchKernelGGL((attn_kernel<FMT, DP, MT, QT, false>), grid, dim3(kAttnThreads), 0, s, a);
 }
 
 template <int FMT, int DP>
