@@ -47,9 +47,8 @@ struct AttnSpan {
     bool bad;
 };
 
-__device__ __forceinline__ AttnSpan attn_span(const AttnArgs &a, int32_t seq) {
+__device__ __forceinline__ AttnSpan attn_span(const AttnArgs &a, int32_t raw) {
     AttnSpan s;
-    const int32_t raw = a.lens[seq];
     s.bad = raw < 0 || raw > a.capacity;
     s.len = raw < 0 ? 0 : (raw > a.capacity ? a.capacity : raw);
     s.first = 0;
@@ -71,42 +70,54 @@ __device__ __forceinline__ AttnSpan attn_span(const AttnArgs &a, int32_t seq) {
 struct AttnPlan {
     int32_t total, each;      // tiles in all; of a worker
     int32_t seq, before;      // the worker's first sequence and the tiles (of one head) before it
+    int32_t lens;             // of up to 64 sequences: lane l holds the length of sequence l
 };
 
+// Length of a sequence, the same for the whole wave.
+__device__ __forceinline__ int32_t attn_len(const AttnArgs &a, const AttnPlan &p, int32_t seq) {
+    return a.n_seq <= 64 ? __builtin_amdgcn_readlane(p.lens, seq) : __builtin_amdgcn_readfirstlane(a.lens[seq]);
+}
+
+// Sums over lanes 0 .. l, by moves inside the rows of 16 lanes and from row to row.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int32_t attn_lanes_add(int32_t v) {
+    return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false);
+}
+__device__ __forceinline__ int32_t attn_lanes_before(int32_t v) {
+    v = attn_lanes_add<0x111, 0xf>(v);      // from 1, 2, 4 and 8 lanes before in the row
+    v = attn_lanes_add<0x112, 0xf>(v);
+    v = attn_lanes_add<0x114, 0xf>(v);
+    v = attn_lanes_add<0x118, 0xf>(v);
+    v = attn_lanes_add<0x142, 0xa>(v);      // rows 1 and 3: the row before's last lane
+    return attn_lanes_add<0x143, 0xc>(v);   // rows 2 and 3: lane 31
+}
+
 __device__ __forceinline__ int32_t attn_lane_tiles(const AttnArgs &a, int32_t first, int32_t count, int32_t per,
-                                                   int32_t &mine) {
+                                                   int32_t &raw) {
     const int lane = static_cast<int>(threadIdx.x & 63);
-    mine = 0;
+    int32_t mine = 0;
+    raw = 0;
     for (int32_t i = 0; i < per; ++i) {
         const int32_t b = lane * per + i;
-        if (b < count) mine += attn_span(a, first + b).tiles;
+        if (b < count) {
+            raw = a.lens[first + b];
+            mine += attn_span(a, raw).tiles;
+        }
     }
-    int32_t run = mine;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const int32_t o = __shfl_up(run, off, 64);
-        if (lane >= off) run += o;
-    }
-    return run;
+    return mine;
 }
 
 __device__ __forceinline__ AttnPlan attn_plan(const AttnArgs &a, uint32_t w) {
     AttnPlan p;
     p.seq = p.before = 0;
     const uint32_t heads = static_cast<uint32_t>(a.n_kv), workers = static_cast<uint32_t>(a.workers);
-    if (a.n_seq == 1) {
-        const uint32_t total = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(attn_span(a, 0).tiles)) * heads;
-        p.total = static_cast<int32_t>(total);
-        p.each = static_cast<int32_t>((total + workers - 1) / workers);
-        return p;
-    }
-    int32_t count = a.n_seq, mine;
-    int32_t per = (count + 63) / 64, run = attn_lane_tiles(a, 0, count, per, mine);
+    int32_t count = a.n_seq, per = (count + 63) / 64;
+    int32_t mine = attn_lane_tiles(a, 0, count, per, p.lens), run = attn_lanes_before(mine);
     const uint32_t total = static_cast<uint32_t>(__builtin_amdgcn_readlane(run, 63)) * heads;
     p.total = static_cast<int32_t>(total);
     p.each = static_cast<int32_t>((total + workers - 1) / workers);
     const uint32_t x = w * static_cast<uint32_t>(p.each);
-    if (x >= total) return p;
+    if (x >= total || a.n_seq == 1) return p;
     const int32_t y = static_cast<int32_t>(x / heads);
     for (;;) {
         // (the bound holds by itself unless the lengths change while they are read: then the rows are
@@ -118,7 +129,9 @@ __device__ __forceinline__ AttnPlan attn_plan(const AttnArgs &a, uint32_t w) {
         if (per == 1) return p;
         count = count - j * per < per ? count - j * per : per;
         per = (count + 63) / 64;
-        run = attn_lane_tiles(a, p.seq, count, per, mine);
+        int32_t raw;
+        mine = attn_lane_tiles(a, p.seq, count, per, raw);
+        run = attn_lanes_before(mine);
     }
 }
 

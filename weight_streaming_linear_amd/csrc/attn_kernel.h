@@ -238,14 +238,6 @@ __device__ __forceinline__ void load_queries(const AttnArgs &a, int32_t seq, int
     }
 }
 
-__device__ __forceinline__ AttnSpan wave_span(const AttnArgs &a, int32_t seq) {
-    AttnSpan s = attn_span(a, seq);
-    s.len = __builtin_amdgcn_readfirstlane(s.len);
-    s.first = __builtin_amdgcn_readfirstlane(s.first);
-    s.tiles = __builtin_amdgcn_readfirstlane(s.tiles);
-    return s;
-}
-
 // Element d of a row of keys or values, exactly.
 template <int FMT>
 __device__ __forceinline__ float element(const char *row, int32_t d, float scale) {
@@ -335,8 +327,8 @@ constexpr int attn_waves() {
 template <int FMT, int DP, int MT, int QT, bool FULL>
 __global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void attn_kernel(AttnArgs a) {
     constexpr int kPad = DP + 4, PT = QT == 1 ? 2 : 3;
-    __shared__ float lds_o[kAttnWaves][16][kPad];
-    __shared__ float lds_m[kAttnWaves][16], lds_l[kAttnWaves][16];
+    __shared__ float lds_o[kAttnWaves][16 * MT][kPad];
+    __shared__ float lds_m[kAttnWaves][16 * MT], lds_l[kAttnWaves][16 * MT];
     __shared__ WaveLds lds_w[kAttnWaves];
 
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, g = lane >> 4;
@@ -351,7 +343,7 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void
     int32_t seq = plan.seq, head = 0, tile = 0;
     AttnSpan span = {};
     if (begin < end) {
-        span = wave_span(a, seq);
+        span = attn_span(a, attn_len(a, plan, seq));
         const int32_t rest = begin - plan.before * a.n_kv;
         head = static_cast<int32_t>(static_cast<uint32_t>(rest) / static_cast<uint32_t>(span.tiles));
         head = head < a.n_kv ? head : a.n_kv - 1;      // (as in attn_plan)
@@ -533,23 +525,26 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void
         }
 
         // join the waves; then the rows are done, or partial where the item goes on elsewhere
-        {
-        const AttnArgs &a = fresh_args();
-        const int tid = fresh(static_cast<int>(threadIdx.x)), lane = tid & 63, g = lane >> 4;
         const bool full = tile == 0 && n == span.tiles;
+        {
+        const AttnArgs a = fresh_args();
+        const int tid = fresh(static_cast<int>(threadIdx.x)), lane = tid & 63, g = lane >> 4;
         const int64_t slot = (static_cast<int64_t>(blockIdx.y) * a.workers + blockIdx.x) * 2 + (tile == 0 ? 1 : 0);
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
             l[j] += __shfl_xor(l[j], 16, 64);
             l[j] += __shfl_xor(l[j], 32, 64);
-            if (g == 0) lds_m[wave][lane] = m[j];
-            __syncthreads();
-            float top = lds_m[0][lane & 15];
+            if (g == 0) lds_m[wave][16 * j + lane] = m[j];
+        }
+        __syncthreads();
 #pragma unroll
-            for (int w = 1; w < kAttnWaves; ++w) top = fmaxf(top, lds_m[w][lane & 15]);
+        for (int j = 0; j < MT; ++j) {
+            float top = lds_m[0][16 * j + (lane & 15)];
+#pragma unroll
+            for (int w = 1; w < kAttnWaves; ++w) top = fmaxf(top, lds_m[w][16 * j + (lane & 15)]);
             const float ref = top == -__builtin_huge_valf() ? 0.f : top;
             const float f = __builtin_amdgcn_exp2f(m[j] - ref);
-            if (g == 0) lds_l[wave][lane] = l[j] * f;
+            if (g == 0) lds_l[wave][16 * j + lane] = l[j] * f;
             // acc[j][n * kVec + e][r] is element n * 16 * kVec + (4 g + r) * kVec + e of row l % 16
             constexpr int kVec = Values<FMT, DP>::kVec;
 #pragma unroll
@@ -559,31 +554,30 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void
 #pragma unroll
                     for (int e = 0; e < kVec; e += 4) {
                         const int i = c * kVec + e;
-                        *reinterpret_cast<f32x4 *>(&lds_o[wave][lane & 15][c * 16 * kVec + (4 * g + r) * kVec + e]) =
+                        *reinterpret_cast<f32x4 *>(&lds_o[wave][16 * j + (lane & 15)][c * 16 * kVec + (4 * g + r) * kVec + e]) =
                             f32x4{acc[j][i][r] * f, acc[j][i + 1][r] * f, acc[j][i + 2][r] * f, acc[j][i + 3][r] * f};
                     }
-            __syncthreads();
-            for (int i = tid; i < 16 * (DP / 4); i += kAttnThreads) {
-                const int r = i / (DP / 4), d = (i - r * (DP / 4)) * 4;
-                const int32_t in_tile = 16 * j + r, row = row0 + in_tile;
-                if (d < a.head_dim && in_tile < a.tile_rows && row < a.rows) {
-                    f32x4 o = {0, 0, 0, 0};
-                    float sum = 0.f, mx = lds_m[0][r];
+        }
+        __syncthreads();
+        for (int i = tid; i < 16 * MT * (DP / 4); i += kAttnThreads) {
+            const int r = i / (DP / 4), d = (i - r * (DP / 4)) * 4;
+            const int32_t row = row0 + r;
+            if (d < a.head_dim && r < a.tile_rows && row < a.rows) {
+                f32x4 o = {0, 0, 0, 0};
+                float sum = 0.f, mx = lds_m[0][r];
 #pragma unroll
-                    for (int w = 0; w < kAttnWaves; ++w) {
-                        o += *reinterpret_cast<const f32x4 *>(&lds_o[w][r][d]);
-                        sum += lds_l[w][r];
-                        mx = fmaxf(mx, lds_m[w][r]);
-                    }
-                    if (full) {
-                        attn_finish(a, seq, head, row, d, o, mx, sum);
-                    } else {
-                        *reinterpret_cast<f32x4 *>(a.part_o + (slot * a.tile_rows + in_tile) * a.head_dim + d) = o;
-                        if (d == 0) a.part_ml[slot * a.tile_rows + in_tile] = make_float2(mx, sum);
-                    }
+                for (int w = 0; w < kAttnWaves; ++w) {
+                    o += *reinterpret_cast<const f32x4 *>(&lds_o[w][r][d]);
+                    sum += lds_l[w][r];
+                    mx = fmaxf(mx, lds_m[w][r]);
+                }
+                if (full) {
+                    attn_finish(a, seq, head, row, d, o, mx, sum);
+                } else {
+                    *reinterpret_cast<f32x4 *>(a.part_o + (slot * a.tile_rows + r) * a.head_dim + d) = o;
+                    if (d == 0) a.part_ml[slot * a.tile_rows + r] = make_float2(mx, sum);
                 }
             }
-            __syncthreads();
         }
         if (tile == 0) {
             const uint32_t last = static_cast<uint32_t>(x + span.tiles - 1) / static_cast<uint32_t>(plan.each);
@@ -593,11 +587,12 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void
         }
 
         x += n;
+        if (x < end) __syncthreads();      // LDS is free again
         tile = 0;
         if (n == left && ++head == a.n_kv) {
             head = 0;
             if (++seq >= a.n_seq) break;
-            if (x < end) span = wave_span(a, seq);
+            if (x < end) span = attn_span(a, attn_len(a, plan, seq));
         }
     }
     if (a.open != nullptr && !a.by_item && blockIdx.y == 0 && tid == 0) a.open[blockIdx.x] = open;
