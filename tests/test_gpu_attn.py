@@ -210,6 +210,24 @@ def test_same_bits_every_time_and_streams():
         assert torch.equal(out, first)
 
 
+@pytest.mark.parametrize("heads,n_kv,dim,ql", [(1, 1, 64, 1), (6, 1, 128, 1), (5, 1, 128, 3), (7, 1, 128, 1), (40, 1, 64, 2),
+                                               (24, 2, 128, 5), (3, 1, 256, 3), (12, 1, 192, 2), (1, 1, 16, 1)])
+def test_parts_are_joined(heads, n_kv, dim, ql):
+    """Few and many rows (one and several row tiles, fewer and more elements than threads), two and
+    many parts, fewer and more items than workgroups; on a workspace of NaNs."""
+    import torch
+    for lens in ([3000], [4099, 700, 129], [300, 1, 0, 5000] + [257] * 90, [140] * 600):
+        say(f"attn join heads={heads}/{n_kv} dim={dim} q_len={ql} {len(lens)} sequences")
+        c = CacheCase(20 + ql, lens, n_kv, dim, 16, False, "cuda")
+        q = _q(20, len(lens), ql, heads, dim, False)
+        n = wsl.attn_decode_workspace_bytes(1, len(lens), ql, heads, n_kv, dim, c.table.shape[1], 16)
+        ws = torch.full((n // 4,), float("nan"), device="cuda")
+        lse = torch.full(q.shape[:3], float("nan"), device="cuda")
+        for _ in range(2):
+            out = wsl.attn_decode(c.cache, q, c.table, c.kv_lens, lse=lse, workspace=ws)
+        _check(c, q, out, lse, dim ** -0.5, 0)
+
+
 def test_a_captured_step_follows_growing_lengths():
     """Write, attend and advance, captured once; lengths grow on the device."""
     import torch

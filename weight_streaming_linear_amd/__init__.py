@@ -178,8 +178,21 @@ def _stream(stream):
     Stream object of it takes 2.7 us of the host, as long as a launch."""
     if stream is not None:
         return stream.cuda_stream
+    return _raw_stream(_device())
+
+
+def _raw_stream(device):
+    """torch's own function of this kind, which takes this one's place at the first call (as does _device's):
+    the module itself loads without torch."""
+    global _raw_stream, _device
     from torch import _C
-    return _C._cuda_getCurrentRawStream(_C._cuda_getDevice())
+    _raw_stream, _device = _C._cuda_getCurrentRawStream, _C._cuda_getDevice
+    return _raw_stream(device)
+
+
+def _device():
+    from torch import _C
+    return _C._cuda_getDevice()
 
 
 # ---------------------------------------------------------------- format helpers
@@ -461,11 +474,12 @@ class KVCache:
 def _float_format(t, name):
     """WSL_OUT_F32 or WSL_OUT_BF16 of a tensor."""
     import torch
-    if t.dtype == torch.bfloat16:
+    dtype = t.dtype
+    if dtype is torch.bfloat16:
         return WSL_OUT_BF16
-    if t.dtype == torch.float32:
+    if dtype is torch.float32:
         return WSL_OUT_F32
-    raise ValueError(f"{name}: dtype {t.dtype} is neither float32 nor bfloat16")
+    raise ValueError(f"{name}: dtype {dtype} is neither float32 nor bfloat16")
 
 
 def _float_dtype(fmt):
@@ -495,6 +509,8 @@ def _status(status, device):
 def _head_rows(t, name, device, shape):
     """Check a [..., heads, head_dim] tensor whose leading dimensions step as one (a view of a wider
     row of tokens serves); returns the elements from token to token."""
+    if t.device == device and t.shape == shape and t.is_contiguous():      # the common case, in 0.3 us
+        return shape[-2] * shape[-1]
     if not t.is_cuda or t.device != device:
         raise ValueError(f"{name}: on {t.device}, expected {device}")
     if tuple(t.shape) != shape:
@@ -512,42 +528,63 @@ def _head_rows(t, name, device, shape):
     return st[0] if shape[0] > 1 else heads * dim
 
 
+def _plain(t, name, dtype, device, shape):
+    """Check a contiguous tensor of one type and shape."""
+    if t.dtype is dtype and t.device == device and t.shape == shape and t.is_contiguous():
+        return
+    _require(t, name, (dtype,), device=device, contiguous=True)
+    raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
 def _slots(cache, slots):
     import torch
-    _require(slots, "slots", (torch.int64,), device=cache.device, contiguous=True, ndim=1)
-    return int(slots.numel())
+    if slots.dim() != 1:
+        raise ValueError(f"slots: expected 1 dimension, got shape {tuple(slots.shape)}")
+    _plain(slots, "slots", torch.int64, cache.device, slots.shape)
+    return slots.numel()
 
 
 def kv_cache_write(cache, k, v, slots, status=None, stream=None):
     """Put k, v [count][n_kv][head_dim] (fp32 or bf16; views of a fused projection serve) into the
     slots (int64 [count]: page * page_size + place, -1 for none) of a KVCache."""
+    dev = cache.device
     count = _slots(cache, slots)
     shape = (count, cache.n_kv, cache.head_dim)
     xfmt = _float_format(k, "k")
-    if v.dtype != k.dtype:
+    if v.dtype is not k.dtype:
         raise ValueError(f"v: dtype {v.dtype}, k has {k.dtype}")
-    ld_k, ld_v = _head_rows(k, "k", cache.device, shape), _head_rows(v, "v", cache.device, shape)
-    _status(status, cache.device)
+    ld_k, ld_v = _head_rows(k, "k", dev, shape), _head_rows(v, "v", dev, shape)
+    if status is not None:
+        _status(status, dev)
     rc = lib().kv_cache_write(cache.ref, k.data_ptr(), v.data_ptr(), xfmt, count, ld_k, ld_v, slots.data_ptr(),
                               _ptr(status), _stream(stream))
-    _check(rc, "kv_cache_write")
+    if rc:
+        _check(rc, "kv_cache_write")
 
 
 def kv_cache_read(cache, slots, k=None, v=None, ofmt=WSL_OUT_BF16, status=None, stream=None):
-    """The keys and values held in slots, [count][n_kv][head_dim] each of ofmt's type."""
+    """The keys and values held in slots, [count][n_kv][head_dim] each of ofmt's type (new ones are
+    the halves of one tensor)."""
+    dev = cache.device
     count = _slots(cache, slots)
     shape, dtype = (count, cache.n_kv, cache.head_dim), _float_dtype(ofmt)
-    if k is None:
-        k = _new(shape, dtype, cache.device, stream)
-    if v is None:
-        v = _new(shape, dtype, cache.device, stream)
-    if k.dtype != dtype or v.dtype != dtype:
-        raise ValueError(f"k, v: dtypes {k.dtype}, {v.dtype}, expected {dtype}")
-    ld_k, ld_v = _head_rows(k, "k", cache.device, shape), _head_rows(v, "v", cache.device, shape)
-    _status(status, cache.device)
-    rc = lib().kv_cache_read(cache.ref, slots.data_ptr(), count, k.data_ptr(), v.data_ptr(), int(ofmt), ld_k, ld_v,
+    ld_k = ld_v = shape[1] * shape[2]
+    if k is None and v is None:
+        k, v = _new((2, *shape), dtype, dev, stream).unbind(0)
+    else:
+        if k is None:
+            k = _new(shape, dtype, dev, stream)
+        if v is None:
+            v = _new(shape, dtype, dev, stream)
+        if k.dtype is not dtype or v.dtype is not dtype:
+            raise ValueError(f"k, v: dtypes {k.dtype}, {v.dtype}, expected {dtype}")
+        ld_k, ld_v = _head_rows(k, "k", dev, shape), _head_rows(v, "v", dev, shape)
+    if status is not None:
+        _status(status, dev)
+    rc = lib().kv_cache_read(cache.ref, slots.data_ptr(), count, k.data_ptr(), v.data_ptr(), ofmt, ld_k, ld_v,
                              _ptr(status), _stream(stream))
-    _check(rc, "kv_cache_read")
+    if rc:
+        _check(rc, "kv_cache_read")
     return k, v
 
 
@@ -566,32 +603,36 @@ def attn_decode(cache, q, block_table, kv_lens, scale=None, window=0, out=None, 
     query sees, 0 for all; ofmt: q's type unless given; lse: fp32 [n_seq][q_len][n_heads] to be
     written; workspace: a device tensor of attn_decode_workspace_bytes (allocated unless given)."""
     import torch
-    if q.dim() != 4:
-        raise ValueError(f"q: expected 4 dimensions, got shape {tuple(q.shape)}")
-    n_seq, q_len, n_heads, dim = shape = tuple(q.shape)
+    shape = q.shape
+    if len(shape) != 4:
+        raise ValueError(f"q: expected 4 dimensions, got shape {tuple(shape)}")
+    n_seq, q_len, n_heads, dim = shape
     dev = cache.device
     qfmt = _float_format(q, "q")
     ld_q = _head_rows(q, "q", dev, (n_seq, q_len, n_heads, cache.head_dim))
-    _require(block_table, "block_table", (torch.int32,), device=dev, ndim=2)
-    _require(kv_lens, "kv_lens", (torch.int32,), device=dev, contiguous=True, ndim=1)
+    if block_table.dtype is not torch.int32 or block_table.device != dev or block_table.dim() != 2 or \
+            not (block_table.is_contiguous() or block_table.stride(1) == 1) or block_table.shape[0] != n_seq:
+        _require(block_table, "block_table", (torch.int32,), device=dev, ndim=2)
+        raise ValueError(f"block_table: shape {tuple(block_table.shape)}, {n_seq} sequences")
     pages = block_table.shape[1]
-    if block_table.shape[0] != n_seq or kv_lens.shape[0] != n_seq:
-        raise ValueError(f"{n_seq} sequences, block_table {tuple(block_table.shape)}, kv_lens {tuple(kv_lens.shape)}")
+    _plain(kv_lens, "kv_lens", torch.int32, dev, (n_seq,))
     ofmt = (qfmt if out is None else _float_format(out, "out")) if ofmt is None else int(ofmt)
     if out is None:
         if ofmt == qfmt and stream is None:
             out = torch.empty_like(q, memory_format=torch.contiguous_format)
         else:
             out = _new(shape, _float_dtype(ofmt), dev, stream)
-    elif out.dtype != _float_dtype(ofmt):
-        raise ValueError(f"out: dtype {out.dtype}, expected {_float_dtype(ofmt)}")
-    ld_out = _head_rows(out, "out", dev, shape)
+        ld_out = n_heads * dim
+    else:
+        if out.dtype is not _float_dtype(ofmt):
+            raise ValueError(f"out: dtype {out.dtype}, expected {_float_dtype(ofmt)}")
+        ld_out = _head_rows(out, "out", dev, tuple(shape))
     if lse is not None:
         _require(lse, "lse", (torch.float32,), device=dev, contiguous=True)
-        if tuple(lse.shape) != shape[:3]:
-            raise ValueError(f"lse: shape {tuple(lse.shape)}, expected {shape[:3]}")
-    _status(status, dev)
-    L = lib()
+        if lse.shape != shape[:3]:
+            raise ValueError(f"lse: shape {tuple(lse.shape)}, expected {tuple(shape[:3])}")
+    if status is not None:
+        _status(status, dev)
     if workspace is None:
         ws_bytes = attn_decode_workspace_bytes(qfmt, n_seq, q_len, n_heads, cache.n_kv, dim, pages, cache.page_size)
         if ws_bytes:
@@ -599,11 +640,12 @@ def attn_decode(cache, q, block_table, kv_lens, scale=None, window=0, out=None, 
     else:
         _require(workspace, "workspace", (workspace.dtype,), device=dev, contiguous=True)
         ws_bytes = workspace.numel() * workspace.element_size()
-    rc = L.attn_decode(cache.ref, q.data_ptr(), qfmt, n_seq, q_len, n_heads, ld_q, block_table.data_ptr(),
-                       block_table.stride(0) if n_seq > 1 else pages, pages, kv_lens.data_ptr(),
-                       dim ** -0.5 if scale is None else float(scale), int(window), out.data_ptr(), ofmt, ld_out,
-                       _ptr(lse), _ptr(workspace), ws_bytes, _ptr(status), _stream(stream))
-    _check(rc, "attn_decode")
+    rc = lib().attn_decode(cache.ref, q.data_ptr(), qfmt, n_seq, q_len, n_heads, ld_q, block_table.data_ptr(),
+                           block_table.stride(0) if n_seq > 1 else pages, pages, kv_lens.data_ptr(),
+                           dim ** -0.5 if scale is None else float(scale), int(window), out.data_ptr(), ofmt, ld_out,
+                           _ptr(lse), _ptr(workspace), ws_bytes, _ptr(status), _stream(stream))
+    if rc:
+        _check(rc, "attn_decode")
     return out
 
 
@@ -612,15 +654,17 @@ def verify_drafts_workspace_bytes(n_seq, vocab):
     return int(lib().verify_drafts_workspace_bytes(int(n_seq), int(vocab)))
 
 
-def _prob_rows(t, name, lead, vocab):
+def _prob_rows(t, name, device, shape):
     """Check probability rows [n_seq][rows][vocab]; returns the elements from row to row."""
-    if t.dim() != 3 or tuple(t.shape) != (*lead, vocab):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(*lead, vocab)}")
+    if t.device == device and t.shape == shape and t.is_contiguous():
+        return shape[2]
+    if t.device != device or t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} on {t.device}, expected {shape} on {device}")
     st = t.stride()
-    if vocab > 1 and st[2] != 1:
+    if shape[2] > 1 and st[2] != 1:
         raise ValueError(f"{name}: last dimension must have stride 1 (got strides {st})")
-    ld = st[1] if lead[1] > 1 else (st[0] if lead[0] > 1 else vocab)
-    if lead[0] > 1 and st[0] != lead[1] * ld:
+    ld = st[1] if shape[1] > 1 else (st[0] if shape[0] > 1 else shape[2])
+    if shape[0] > 1 and st[0] != shape[1] * ld:
         raise ValueError(f"{name}: the first two dimensions must step as one (strides {st})")
     return ld
 
@@ -643,27 +687,27 @@ def verify_drafts(p, q, drafts, u, n_drafts=None, accepted=None, tokens=None, wo
     if width < 0:
         raise ValueError("p: no rows")
     pfmt = _float_format(p, "p")
-    ld_p, ld_q = _prob_rows(p, "p", (n_seq, rows), vocab), 0
+    ld_p, ld_q = _prob_rows(p, "p", dev, (n_seq, rows, vocab)), 0
     if q is not None and width:
-        _require(q, "q", (p.dtype,), device=dev)
-        ld_q = _prob_rows(q, "q", (n_seq, width), vocab)
-    for t, name, dtype, shape in ((drafts, "drafts", torch.int32, (n_seq, width)), (u, "u", torch.float32, (n_seq, rows)),
-                                  (n_drafts, "n_drafts", torch.int32, (n_seq,)),
-                                  (accepted, "accepted", torch.int32, (n_seq,)),
-                                  (tokens, "tokens", torch.int32, (n_seq, rows))):
-        if t is None:
-            if name in ("drafts", "u"):
-                raise ValueError(f"{name}: missing")
-            continue
-        _require(t, name, (dtype,), device=dev, contiguous=True)
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
-    _status(status, dev)
+        if q.dtype is not p.dtype:
+            raise ValueError(f"q: dtype {q.dtype}, p has {p.dtype}")
+        ld_q = _prob_rows(q, "q", dev, (n_seq, width, vocab))
+    if drafts is None or u is None:
+        raise ValueError("drafts, u: missing")
+    _plain(drafts, "drafts", torch.int32, dev, (n_seq, width))
+    _plain(u, "u", torch.float32, dev, (n_seq, rows))
+    if n_drafts is not None:
+        _plain(n_drafts, "n_drafts", torch.int32, dev, (n_seq,))
+    if status is not None:
+        _status(status, dev)
     if accepted is None:
         accepted = _new((n_seq,), torch.int32, dev, stream)
+    else:
+        _plain(accepted, "accepted", torch.int32, dev, (n_seq,))
     if tokens is None:
         tokens = _new((n_seq, rows), torch.int32, dev, stream)
-    L = lib()
+    else:
+        _plain(tokens, "tokens", torch.int32, dev, (n_seq, rows))
     if workspace is None:
         ws_bytes = verify_drafts_workspace_bytes(n_seq, vocab)
         if ws_bytes:
@@ -671,10 +715,11 @@ def verify_drafts(p, q, drafts, u, n_drafts=None, accepted=None, tokens=None, wo
     else:
         _require(workspace, "workspace", (workspace.dtype,), device=dev, contiguous=True)
         ws_bytes = workspace.numel() * workspace.element_size()
-    rc = L.verify_drafts(p.data_ptr(), q.data_ptr() if ld_q else None, pfmt, n_seq, width, vocab, ld_p, ld_q,
-                         drafts.data_ptr(), _ptr(n_drafts), u.data_ptr(), accepted.data_ptr(), tokens.data_ptr(),
-                         _ptr(workspace), ws_bytes, _ptr(status), _stream(stream))
-    _check(rc, "verify_drafts")
+    rc = lib().verify_drafts(p.data_ptr(), q.data_ptr() if ld_q else None, pfmt, n_seq, width, vocab, ld_p, ld_q,
+                             drafts.data_ptr(), _ptr(n_drafts), u.data_ptr(), accepted.data_ptr(), tokens.data_ptr(),
+                             _ptr(workspace), ws_bytes, _ptr(status), _stream(stream))
+    if rc:
+        _check(rc, "verify_drafts")
     return accepted, tokens
 
 
