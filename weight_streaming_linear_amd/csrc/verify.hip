@@ -136,30 +136,26 @@ __device__ __forceinline__ void load_seg(const char *row, int64_t j0, int64_t vo
     }
 }
 
-// A segment's weights: NaN and negative ones count as zero.
-template <int FMT>
+// A segment of p and of what is taken off it: nothing, q, or infinity at the one draft that fell.
 struct Seg {
     float p[kEach], q[kEach];
 };
 template <int FMT>
-__device__ __forceinline__ void load(const char *p, const char *q, int64_t j0, int64_t vocab, Seg<FMT> &s) {
+__device__ __forceinline__ void load(const char *p, const char *q, int64_t j0, int64_t vocab, int32_t one_hot, Seg &s) {
     load_seg<FMT>(p, j0, vocab, s.p);
     if (q) {
         load_seg<FMT>(q, j0, vocab, s.q);
     } else {
+        const int64_t at = one_hot - j0;
+        const int lane = static_cast<int>(threadIdx.x & 63);
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) s.q[i] = 0.f;
+        for (int i = 0; i < kEach; ++i) s.q[i] = entry_of<FMT>(lane, i) == at ? __builtin_huge_valf() : 0.f;
     }
 }
-template <int FMT>
-__device__ __forceinline__ double top_of(const Seg<FMT> &s, int i) {
-    return s.p[i] > 0 ? static_cast<double>(s.p[i]) : 0.0;
-}
-template <int FMT>
-__device__ __forceinline__ double weight_of(const Seg<FMT> &s, int i, int64_t j0, int32_t one_hot) {
-    const double d = static_cast<double>(s.p[i]) - static_cast<double>(s.q[i]);
-    const int lane = static_cast<int>(threadIdx.x & 63);
-    return d > 0 && j0 + entry_of<FMT>(lane, i) != one_hot ? d : 0.0;
+// Weights: NaN and negative ones count as zero (the maximum with zero is zero for both).
+__device__ __forceinline__ double top_of(const Seg &s, int i) { return __builtin_fmax(static_cast<double>(s.p[i]), 0.0); }
+__device__ __forceinline__ double weight_of(const Seg &s, int i) {
+    return __builtin_fmax(static_cast<double>(s.p[i]) - static_cast<double>(s.q[i]), 0.0);
 }
 
 // Sums over lanes 0 .. l, by moves inside the rows of 16 lanes and from row to row.
@@ -186,18 +182,33 @@ __device__ __forceinline__ double lane_value(double v, int lane) {
 }
 __device__ __forceinline__ double lanes_total(double v) { return lane_value(lanes_before(v), 63); }
 
+// A segment's sums over the wave: of the weights, and of the tops if that is zero.  They are asked for
+// only where all weights of a row are zero, and then each segment's are.
+__device__ __forceinline__ double2 sums_of(const Seg &s) {
+    double sw = 0, sp = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) sw += weight_of(s, i);
+    sw = lanes_total(sw);
+    if (sw == 0) {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) sp += top_of(s, i);
+        sp = lanes_total(sp);
+    }
+    return make_double2(sw, sp);
+}
+
 // In the order of the entries: the first of a segment whose running sum (from `run` on) passes the
-// target goes to `first`, the last with a weight to `last`; true if one passes.
+// target; where none does, the last with a weight.
 template <int FMT>
-__device__ __forceinline__ bool look_through(const Seg<FMT> &s, int64_t j0, int32_t one_hot, bool tops, double target,
-                                             double &run, int64_t &first, int64_t &last) {
+__device__ __forceinline__ int32_t look_through(const Seg &s, int64_t j0, bool tops, double target, double run) {
     constexpr int V = kVec<FMT>;
+    int64_t last = -1;
 #pragma unroll
     for (int b = 0; b < kEach; b += V) {
         double w[V], sum = 0;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            w[e] = tops ? top_of(s, b + e) : weight_of(s, b + e, j0, one_hot);
+            w[e] = tops ? top_of(s, b + e) : weight_of(s, b + e);
             sum += w[e];
         }
         const double up = lanes_before(sum);
@@ -217,12 +228,11 @@ __device__ __forceinline__ bool look_through(const Seg<FMT> &s, int64_t j0, int3
         }
         if (hits) {
             const int l = __builtin_ctzll(hits);
-            first = here + l * V + __builtin_amdgcn_readlane(hit, l);
-            return true;
+            return static_cast<int32_t>(here + l * V + __builtin_amdgcn_readlane(hit, l));
         }
         run += lane_value(up, 63);
     }
-    return false;
+    return static_cast<int32_t>(last);
 }
 
 // What running sums have to pass; NaN passes none: the last entry, as for u >= 1.
@@ -245,35 +255,31 @@ __device__ __forceinline__ void write_out(const VerifyArgs &a, int64_t seq, cons
 
 template <int FMT>
 __global__ __launch_bounds__(kSmallWaves * 64) void verify_small_kernel(VerifyArgs a) {
-    __shared__ double lds_w[kSmallWaves], lds_p[kSmallWaves];
+    __shared__ double lds_w[kSmallWaves * kSmallSegs], lds_p[kSmallWaves * kSmallSegs];
     const int64_t seq = blockIdx.x;
     const int lane = static_cast<int>(threadIdx.x & 63), waves = static_cast<int>(blockDim.x >> 6);
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
     const Verdict o = judge<FMT>(a, seq);
     const char *p, *q;
     rows_of<FMT>(a, seq, o, p, q);
-    double sw = 0, sp = 0;
-    {
-        Seg<FMT> s[kSmallSegs];
+    Seg s[kSmallSegs];
 #pragma unroll
-        for (int i = 0; i < kSmallSegs; ++i) load(p, q, (wave * kSmallSegs + i) * kSeg, a.vocab, s[i]);
+    for (int i = 0; i < kSmallSegs; ++i) load<FMT>(p, q, (wave * kSmallSegs + i) * kSeg, a.vocab, o.one_hot, s[i]);
 #pragma unroll
-        for (int i = 0; i < kSmallSegs; ++i)
-#pragma unroll
-            for (int e = 0; e < kEach; ++e) {
-                sw += weight_of(s[i], e, (wave * kSmallSegs + i) * kSeg, o.one_hot);
-                sp += top_of(s[i], e);
-            }
+    for (int i = 0; i < kSmallSegs; ++i) {
+        const double2 sums = sums_of(s[i]);
+        if (lane == 0) lds_w[wave * kSmallSegs + i] = sums.x, lds_p[wave * kSmallSegs + i] = sums.y;
     }
-    sw = lanes_total(sw);
-    sp = lanes_total(sp);
-    if (lane == 0) lds_w[wave] = sw, lds_p[wave] = sp;
     __syncthreads();
-    const double mine_w = lane < waves ? lds_w[lane] : 0.0, mine_p = lane < waves ? lds_p[lane] : 0.0;
-    double mine = mine_w, up = lanes_before(mine), total = lane_value(up, 63);
+    // (the entries stay in registers as they were read: not the weights, which take twice as many)
+#pragma unroll
+    for (int i = 0; i < kSmallSegs; ++i)
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) asm volatile("" : "+v"(s[i].p[e]), "+v"(s[i].q[e]));
+    double mine = lane < waves * kSmallSegs ? lds_w[lane] : 0.0, up = lanes_before(mine), total = lane_value(up, 63);
     const bool tops = !(total > 0);        // nothing left of p once q is off: sample p itself
     if (tops) {
-        mine = mine_p;
+        mine = lane < waves * kSmallSegs ? lds_p[lane] : 0.0;
         up = lanes_before(mine);
         total = lane_value(up, 63);
     }
@@ -282,20 +288,14 @@ __global__ __launch_bounds__(kSmallWaves * 64) void verify_small_kernel(VerifyAr
         return;
     }
     const double target = target_of(a, seq, total);
-    // the first wave whose running sum passes the target; where rounding (or u >= 1) lets none pass,
-    // the last one that holds anything
+    // the first segment whose running sum passes the target; where rounding (or u >= 1) lets none
+    // pass, the last one that holds anything
     const uint64_t hits = __ballot(mine > 0 && up > target), some = __ballot(mine > 0);
     const int which = hits ? __builtin_ctzll(hits) : 63 - __builtin_clzll(some);
-    if (wave != which) return;
-    double run = which == 0 ? 0.0 : lane_value(up, which - 1);
-    // read once more, from the cache: held over the sum they would not fit the registers
-    int64_t first = -1, last = -1;
-    for (int i = 0; i < kSmallSegs && first < 0; ++i) {
-        Seg<FMT> s;
-        load(p, q, (wave * kSmallSegs + i) * kSeg, a.vocab, s);
-        look_through(s, (wave * kSmallSegs + i) * kSeg, o.one_hot, tops, target, run, first, last);
-    }
-    write_out(a, seq, o, static_cast<int32_t>(first >= 0 ? first : last));
+#pragma unroll
+    for (int i = 0; i < kSmallSegs; ++i)
+        if (which == wave * kSmallSegs + i)
+            write_out(a, seq, o, look_through<FMT>(s[i], which * kSeg, tops, target, which == 0 ? 0.0 : lane_value(up, which - 1)));
 }
 
 template <int FMT>
@@ -307,18 +307,11 @@ __global__ __launch_bounds__(256) void verify_sum_kernel(VerifyArgs a) {
     const Verdict o = judge<FMT>(a, seq);
     const char *p, *q;
     rows_of<FMT>(a, seq, o, p, q);
-    Seg<FMT> s;
-    load(p, q, seg * kSeg, a.vocab, s);
-    double sw = 0, sp = 0;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-        sw += weight_of(s, i, seg * kSeg, o.one_hot);
-        sp += top_of(s, i);
-    }
-    sw = lanes_total(sw);
-    sp = lanes_total(sp);
+    Seg s;
+    load<FMT>(p, q, seg * kSeg, a.vocab, o.one_hot, s);
+    const double2 sums = sums_of(s);
     if (lane == 0) {
-        a.sums[seq * a.segs + seg] = make_double2(sw, sp);
+        a.sums[seq * a.segs + seg] = sums;
         if (seg == 0) a.verdicts[seq] = o;
     }
 }
@@ -345,7 +338,7 @@ __global__ __launch_bounds__(64) void verify_pick_kernel(VerifyArgs a) {
         up = lanes_before(mine);
         total = lane_value(up, 63);
     }
-    int64_t token = -1;
+    int32_t token = -1;
     if (total > 0 && total < __builtin_huge_val()) {
         const double target = target_of(a, seq, total);
         int64_t hit = -1, last = -1;
@@ -359,16 +352,14 @@ __global__ __launch_bounds__(64) void verify_pick_kernel(VerifyArgs a) {
         const uint64_t hits = __ballot(hit >= 0), some = __ballot(last >= 0);
         const int l = hits ? __builtin_ctzll(hits) : 63 - __builtin_clzll(some);
         const int64_t seg = __builtin_amdgcn_readlane(static_cast<int>(hits ? hit : last), l);
-        double run = lane_value(hits ? hit_at : last_at, l);
+        const double run = lane_value(hits ? hit_at : last_at, l);
         const char *p, *q;
         rows_of<FMT>(a, seq, o, p, q);
-        Seg<FMT> s;
-        load(p, q, seg * kSeg, a.vocab, s);
-        int64_t first = -1, end = -1;
-        look_through(s, seg * kSeg, o.one_hot, tops, target, run, first, end);
-        token = first >= 0 ? first : end;
+        Seg s;
+        load<FMT>(p, q, seg * kSeg, a.vocab, o.one_hot, s);
+        token = look_through<FMT>(s, seg * kSeg, tops, target, run);
     }
-    write_out(a, seq, o, static_cast<int32_t>(token));
+    write_out(a, seq, o, token);
 }
 
 template <int FMT>
