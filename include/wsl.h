@@ -419,7 +419,7 @@ int kv_cache_read(const wsl_kv_cache *h_cache, const int64_t *d_slots, int64_t c
  *            head_dim elements a token; 16-byte aligned, ld_q a multiple of 16 bytes.
  * n_seq      0 .. 65535 (0 launches nothing).  q_len 1 .. 256.  n_heads a multiple of n_kv.
  *            q_len * n_heads / n_kv <= 2^16, q_len * n_heads <= 2^24, and n_seq * n_kv *
- *            ceil(pages_per_seq * page_size / 128) <= 2^30.
+ *            (ceil(pages_per_seq * page_size / 128) + 4) <= 2^30.
  * d_block_table   device int32 [n_seq][ld_table]: page of token t of a sequence at [t / page_size];
  *            pages_per_seq (1 .. ld_table) entries of a row may be read.
  * d_kv_lens  device int32 [n_seq]: read by the kernels only, so a captured call goes on with

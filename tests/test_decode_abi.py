@@ -80,10 +80,10 @@ def test_attn_refusals():
     assert call(ld_q=255) == SHAPE and call(ld_q=260) == ALIGN and call(ld_o=248) == SHAPE and call(ld_o=257) == ALIGN
     assert call(q=4104) == ALIGN and call(out=4100) == ALIGN and call(table=4098) == ALIGN and call(lens=ODD) == ALIGN
     assert call(lse=4097) == ALIGN
-    # tiles of 128 tokens over all sequences and kv heads: at most 2^30, which 2 * 1024 * 2^19 is
+    # tiles of 128 tokens and four more over all sequences and kv heads: at most 2^30, just below 2 * 1024 * 2^19
     most = cache(page_size=1 << 17, page_stride=1 << 24, head_stride=1 << 23)
-    assert call(c=most, n=1024, pages=1 << 9, ld_t=1 << 9, ws=None) == NULL
-    assert call(c=most, n=1025, pages=1 << 9, ld_t=1 << 9, ws=None) == SHAPE
+    assert call(c=most, n=1023, pages=1 << 9, ld_t=1 << 9, ws=None) == NULL
+    assert call(c=most, n=1024, pages=1 << 9, ld_t=1 << 9, ws=None) == SHAPE
     need = wsl.attn_decode_workspace_bytes(1, 2, 1, 4, 2, 64, 64, 16)
     assert need > 0
     assert call(pages=64, ld_t=64, ws=None) == NULL

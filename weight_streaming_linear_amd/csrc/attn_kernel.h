@@ -340,20 +340,23 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void
     const int32_t end = plan.total - begin < plan.each ? plan.total : begin + plan.each;
     AttnOpen open = {0, 0, 0, 1};
     bool bad = false;
-    int32_t seq = plan.seq, head = 0, tile = 0;
+    int32_t seq = plan.seq, head = 0, unit = 0;
     AttnSpan span = {};
     if (begin < end) {
         span = attn_span(a, attn_len(a, plan, seq));
-        const int32_t rest = begin - plan.before * a.n_kv;
-        head = static_cast<int32_t>(static_cast<uint32_t>(rest) / static_cast<uint32_t>(span.tiles));
+        const int32_t rest = begin - plan.before * a.n_kv, units = span.tiles + plan.cost;
+        head = static_cast<int32_t>(static_cast<uint32_t>(rest) / static_cast<uint32_t>(units));
         head = head < a.n_kv ? head : a.n_kv - 1;      // (as in attn_plan)
-        tile = rest - head * span.tiles;
-        tile = tile < span.tiles ? tile : span.tiles - 1;
+        unit = rest - head * units;
+        unit = unit < units ? unit : units - 1;
     }
 
     for (int32_t x = begin; x < end;) {
-        const int32_t left = span.tiles - tile;
-        const int32_t n = end - x < left ? end - x : left;
+        const int32_t left = span.tiles + plan.cost - unit;
+        const int32_t used = end - x < left ? end - x : left;
+        const int32_t tile = unit > plan.cost ? unit - plan.cost : 0;
+        const int32_t n = unit + used - plan.cost - tile;      // tiles; none where the units all stand for its beginning
+        if (n > 0) {
         const int32_t row0 = static_cast<int32_t>(blockIdx.y) * a.tile_rows;
         const int32_t len = span.len;
         const int32_t *table = a.table + seq * a.ld_table;
@@ -580,16 +583,17 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void
             }
         }
         if (tile == 0) {
-            const uint32_t last = static_cast<uint32_t>(x + span.tiles - 1) / static_cast<uint32_t>(plan.each);
+            const uint32_t last = static_cast<uint32_t>(x + left - 1) / static_cast<uint32_t>(plan.each);
             open = {seq, head, static_cast<int32_t>(blockIdx.x), static_cast<int32_t>(last - blockIdx.x) + 1};
             if (a.open != nullptr && a.by_item && blockIdx.y == 0 && tid == 0) a.open[seq * a.n_kv + head] = open;
         }
         }
+        if (x + used < end) __syncthreads();      // LDS is free again
+        }
 
-        x += n;
-        if (x < end) __syncthreads();      // LDS is free again
-        tile = 0;
-        if (n == left && ++head == a.n_kv) {
+        x += used;
+        unit = 0;
+        if (used == left && ++head == a.n_kv) {
             head = 0;
             if (++seq >= a.n_seq) break;
             if (x < end) span = attn_span(a, attn_len(a, plan, seq));

@@ -220,9 +220,9 @@ int check_attn_shape(int qfmt, int64_t n_seq, int64_t q_len, int64_t n_heads, in
     if (n_heads / n_kv * q_len > 65536 || n_heads * q_len > (int64_t(1) << 24)) return WSL_E_SHAPE;
     if (head_dim < 16 || head_dim > 256 || head_dim % 16 != 0) return WSL_E_SHAPE;
     if (pages_per_seq < 1 || pages_per_seq > 0x7fffffff || page_size < 1 || page_size > kMaxDim) return WSL_E_SHAPE;
-    // the kernels count tiles of 128 tokens over all sequences and kv heads in 32 bits
+    // the kernels count tiles of 128 tokens, and some more of each, over all sequences and kv heads in 32 bits
     const int64_t capacity = pages_per_seq * page_size, tokens = capacity < 0x7fffffff ? capacity : 0x7fffffff;
-    if (n_seq * n_kv > (int64_t(1) << 30) / ((tokens + 127) / 128)) return WSL_E_SHAPE;
+    if (n_seq * n_kv > (int64_t(1) << 30) / ((tokens + 127) / 128 + 4)) return WSL_E_SHAPE;
     return WSL_OK;
 }
 
