@@ -141,6 +141,53 @@ def test_masked_places_may_hold_anything():
     assert torch.cuda.is_available()
 
 
+@pytest.mark.parametrize("dim,heads,n_kv,ql,window,f32,e4m3,page", [
+    (128, 5, 1, 5, 0, False, False, 16), (128, 5, 1, 5, 0, True, False, 24), (128, 40, 2, 3, 100, False, True, 16),
+    (256, 4, 1, 4, 0, False, False, 16), (256, 4, 1, 4, 60, True, True, 7), (192, 6, 2, 2, 0, False, True, 16),
+    (80, 12, 1, 5, 33, False, False, 16), (64, 16, 1, 4, 0, False, False, 48), (48, 2, 2, 6, 0, True, False, 1)])
+def test_odd_values_reach_only_what_sees_them(dim, heads, n_kv, ql, window, f32, e4m3, page):
+    """NaNs among the values: in the newest positions (seen by the last queries alone) and before the
+    window's reach of the last ones; sequences of one and of many parts.  What sees none is as exact as
+    ever; what sees one is NaN in that element and exact in the others."""
+    say(f"attn odd dim={dim} heads={heads}/{n_kv} q_len={ql} window={window} f32={f32} e4m3={e4m3} page={page}")
+    lens = [130, 3000, 9]
+
+    def fill(b, x):
+        n = lens[b]
+        x[n - 1, :, dim - 1] = np.nan
+        if ql > 2:
+            x[n - 2, 0, 1] = np.nan
+        if window:
+            x[max(0, n - ql - window + 1), :, 7] = np.nan      # seen by the first query alone
+
+    c = CacheCase(40 + ql, lens, n_kv, dim, page, e4m3, "cuda", v_fill=fill)
+    q = _q(40, 3, ql, heads, dim, f32)
+    got = f32_of(wsl.attn_decode(c.cache, q, c.table, c.kv_lens, window=window))
+    for b, n in enumerate(lens):
+        ref, _, extra = od.attn_ref(f32_of(q)[b], c.values[0][b], c.values[1][b], n, dim ** -0.5, window)
+        assert np.array_equal(np.isnan(got[b]), np.isnan(ref))
+        fine = ~np.isnan(ref)
+        assert not fine.all()
+        extra = {k: np.where(np.isnan(x), 0, x) for k, x in extra.items()}
+        bound = od.attn_bound(extra, dim, n, ref, 2.0 ** -24 if f32 else 2.0 ** -8)
+        assert (np.abs(got[b] - ref)[fine] <= bound[fine]).all()
+
+
+def test_rows_whose_pages_are_all_bad_are_zero():
+    import torch
+    for n, lens_heads in ((60, 4), (3000, 24)):
+        c = CacheCase(60, [n, n], 2, 64, 16, False, "cuda")
+        q = _q(60, 2, 2, lens_heads, 64, False)
+        table = c.table.clone()
+        table[0] = -1
+        st, lse = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros(q.shape[:3], device="cuda")
+        out = wsl.attn_decode(c.cache, q, table, c.kv_lens, lse=lse, status=st)
+        assert st.item() == wsl.WSL_STATUS_INDEX
+        assert (out[0] == 0).all() and torch.isneginf(lse[0]).all()
+        ref, _, extra = od.attn_ref(f32_of(q)[1], c.values[0][1], c.values[1][1], n, 0.125)
+        assert (np.abs(f32_of(out)[1] - ref) <= od.attn_bound(extra, 64, n, ref, 2.0 ** -8)).all()
+
+
 def test_bad_pages_and_lengths_are_reported():
     import torch
     for page in (16, 10):
