@@ -36,11 +36,14 @@ def _check(c, q, out, lse, scale, window, where=""):
             assert (e <= od.lse_bound(extra, dim, n, rl) + 1e-6).all(), f"{where} lse of sequence {b}"
 
 
-def _run(seed, lens, heads, n_kv, dim, page, e4m3, ql=1, f32=False, ofmt=None, window=0, order="phtd", scale=None, **kw):
+def _run(seed, lens, heads, n_kv, dim, page, e4m3, ql=1, f32=False, ofmt=None, window=0, order="phtd", scale=None, wide=0, **kw):
+    """wide: entries (none of the cache's pages) behind each row of the table, as where lengths may yet
+    grow: the split is decided by what a row has room for."""
     import torch
     say(f"attn lens={lens[:6]}.. heads={heads}/{n_kv} dim={dim} page={page} e4m3={e4m3} q_len={ql} f32={f32} "
         f"ofmt={ofmt} window={window} {order}")
     c = CacheCase(seed, lens, n_kv, dim, page, e4m3, "cuda", order=order, **kw)
+    c.table = torch.cat((c.table, torch.full((len(lens), wide), -1, dtype=torch.int32, device="cuda")), 1)
     q = _q(seed, len(lens), ql, heads, dim, f32)
     lse = torch.full(q.shape[:3], float("nan"), device="cuda")
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
@@ -57,15 +60,17 @@ EDGES = [0, 1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 2
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("f32", [False, True])
 @pytest.mark.parametrize("page", [16, 24])
-def test_lengths_around_every_edge(e4m3, f32, page):
-    _run(1, EDGES, 10, 2, 128, page, e4m3, f32=f32)
+@pytest.mark.parametrize("wide", [0, 100])
+def test_lengths_around_every_edge(e4m3, f32, page, wide):
+    _run(1, EDGES, 10, 2, 128, page, e4m3, f32=f32, wide=wide)
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("ql", [2, 5, 8])
-def test_drafts_see_what_is_before_them(e4m3, ql):
+@pytest.mark.parametrize("wide", [0, 100])
+def test_drafts_see_what_is_before_them(e4m3, ql, wide):
     """Lengths below q_len leave the first queries with nothing to see."""
-    _run(2, EDGES, 6, 2, 64, 16, e4m3, ql=ql)
+    _run(2, EDGES, 6, 2, 64, 16, e4m3, ql=ql, wide=wide)
 
 
 @pytest.mark.parametrize("heads,n_kv,dim,page,e4m3,ql,f32,order", [
@@ -85,8 +90,19 @@ def test_head_layouts(heads, n_kv, dim, page, e4m3, ql, f32, order, ofmt):
 
 @pytest.mark.parametrize("e4m3,page", [(False, 16), (True, 24)])
 @pytest.mark.parametrize("window", [1, 2, 31, 100, 128, 1000])
-def test_windows(e4m3, page, window):
-    _run(4, [0, 1, 99, 100, 101, 260, 700], 4, 2, 64, page, e4m3, ql=3, window=window)
+@pytest.mark.parametrize("wide", [0, 100])
+def test_windows(e4m3, page, window, wide):
+    _run(4, [0, 1, 99, 100, 101, 260, 500], 4, 2, 64, page, e4m3, ql=3, window=window, wide=wide)
+    _run(4, [0, 1, 99, 100, 101, 260, 700], 4, 2, 64, page, e4m3, ql=3, window=window, wide=wide)
+
+
+@pytest.mark.parametrize("n", [1, 63, 64, 65, 200, 4100])
+def test_many_sequences_and_empty_ones(n):
+    """The sequence of a share of the work is found by dividing the sequences among 64 lanes."""
+    g = np.random.default_rng(n)
+    lens = [int(x) if i % 5 else 0 for i, x in enumerate(g.integers(0, 40, n))]
+    lens[n // 2] = 700
+    _run(70, lens, 2, 1, 16, 16, False, wide=100)
 
 
 @pytest.mark.parametrize("e4m3", [False, True])

@@ -37,6 +37,7 @@ struct AttnArgs {
     int32_t capacity;     // tokens a table row can name
     int32_t n_seq, q_len, n_kv, group, rows, head_dim, page_size, n_pages;
     int32_t row_tiles, tile_rows, workers, qfmt, ofmt;
+    int32_t whole;        // a workgroup takes one whole item
     int32_t by_item;      // how `open` is indexed: by whichever there are fewer of
 };
 
@@ -83,7 +84,7 @@ struct AttnPlan {
 
 // Length of a sequence, the same for the whole wave.
 __device__ __forceinline__ int32_t attn_len(const AttnArgs &a, const AttnPlan &p, int32_t seq) {
-    return a.n_seq <= 64 ? __builtin_amdgcn_readlane(p.lens, seq) : __builtin_amdgcn_readfirstlane(a.lens[seq]);
+    return a.n_seq <= 64 && !a.whole ? __builtin_amdgcn_readlane(p.lens, seq) : __builtin_amdgcn_readfirstlane(a.lens[seq]);
 }
 
 // Sums over lanes 0 .. l, by moves inside the rows of 16 lanes and from row to row.
@@ -119,6 +120,11 @@ __device__ __forceinline__ AttnPlan attn_plan(const AttnArgs &a, uint32_t w) {
     AttnPlan p;
     p.seq = p.before = 0;
     const uint32_t heads = static_cast<uint32_t>(a.n_kv), workers = static_cast<uint32_t>(a.workers);
+    if (a.whole) {
+        p.seq = static_cast<int32_t>(w / heads);
+        p.cost = 0;
+        return p;
+    }
     const int lane = static_cast<int>(threadIdx.x & 63);
     int32_t count = a.n_seq, per = (count + 63) / 64;
     int32_t mine = attn_lane_units(a, 0, count, per, kAttnCost, p.lens), run = attn_lanes_before(mine);

@@ -336,19 +336,25 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void
     WaveLds &mem = lds_w[wave];
 
     const AttnPlan plan = attn_plan(a, blockIdx.x);
-    const int32_t begin = static_cast<int32_t>(blockIdx.x) * plan.each;
-    const int32_t end = plan.total - begin < plan.each ? plan.total : begin + plan.each;
+    int32_t begin = 0, end = 1;
+    if (!a.whole) {
+        begin = static_cast<int32_t>(blockIdx.x) * plan.each;
+        end = plan.total - begin < plan.each ? plan.total : begin + plan.each;
+    }
     AttnOpen open = {0, 0, 0, 1};
     bool bad = false;
     int32_t seq = plan.seq, head = 0, unit = 0;
     AttnSpan span = {};
     if (begin < end) {
         span = attn_span(a, attn_len(a, plan, seq));
-        const int32_t rest = begin - plan.before * a.n_kv, units = span.tiles + plan.cost;
+        const int32_t units = span.tiles + plan.cost;
+        const int32_t rest = a.whole ? static_cast<int32_t>(blockIdx.x - static_cast<uint32_t>(seq * a.n_kv)) * units
+                                     : begin - plan.before * a.n_kv;
         head = static_cast<int32_t>(static_cast<uint32_t>(rest) / static_cast<uint32_t>(units));
         head = head < a.n_kv ? head : a.n_kv - 1;      // (as in attn_plan)
         unit = rest - head * units;
         unit = unit < units ? unit : units - 1;
+        if (a.whole) end = units;
     }
 
     for (int32_t x = begin; x < end;) {
@@ -603,14 +609,15 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void
     if (__any(bad) && lane == 0 && a.status != nullptr) atomicOr(a.status, WSL_STATUS_INDEX);
 }
 
-// Workgroups for all row tiles together fill the chip once.  Those of one token range lie `workers`
-// apart, a multiple of 8, so that they run at the same time on the same XCD and what one reads the
-// others find in its L2.
+// Workgroups for all row tiles together fill the chip once, or there is one for each item and row tile.
+// Those of one token range lie `workers` apart, a multiple of 8 where it can be, so that they run at the
+// same time on the same XCD and what one reads the others find in its L2.
 template <int FMT, int DP, int MT, int QT>
 void go(AttnArgs &a, hipStream_t s) {
     const int fit = kAttnCus * attn_waves<FMT, DP, MT, QT>();
     const int most = a.row_tiles * 8 >= fit ? 8 : fit / a.row_tiles / 8 * 8;
-    a.workers = a.workers < most ? a.workers : most;
+    if (a.whole) a.workers = a.n_seq * a.n_kv;
+    else a.workers = a.workers < most ? a.workers : most;
     const dim3 grid(static_cast<unsigned>(a.workers), static_cast<unsigned>(a.row_tiles));
     if (a.head_dim == DP) hipLaunchKernelGGL((attn_kernel<FMT, DP, MT, QT, true>), grid, dim3(kAttnThreads), 0, s, a);
     else hipLaunchKernelGGL((attn_kernel<FMT, DP, MT, QT, false>), grid, dim3(kAttnThreads), 0, s, a);
