@@ -19,7 +19,22 @@ struct AttnOpen {
     int32_t seq, head, worker, parts;
 };
 
+// Division of a number n < 2^31 by one that the host knows, 1 <= by <= 2^30: with 2^shift the least
+// power of two >= by and mul = floor(2^32 (2^shift - by) / by) + 1, n / by = (n mul / 2^32 + n) >> shift.
+// (32 ragged sequences over e4m3 43.4 -> 42.4 us against the hardware's steps for a division.)
+struct AttnDiv {
+    uint32_t mul, shift;
+};
+inline AttnDiv attn_div(uint32_t by) {
+    AttnDiv d = {1, 0};
+    while ((uint32_t(1) << d.shift) < by) ++d.shift;
+    d.mul = static_cast<uint32_t>((((uint64_t(1) << d.shift) - by) << 32) / by + 1);
+    return d;
+}
+__device__ __forceinline__ uint32_t attn_over(uint32_t n, const AttnDiv &d) { return (__umulhi(n, d.mul) + n) >> d.shift; }
+
 struct AttnArgs {
+    AttnDiv over_page, over_group, over_heads;
     const char *k, *v;
     const uint8_t *ke, *ve;
     const void *q;
@@ -121,7 +136,7 @@ __device__ __forceinline__ AttnPlan attn_plan(const AttnArgs &a, uint32_t w) {
     p.seq = p.before = 0;
     const uint32_t heads = static_cast<uint32_t>(a.n_kv), workers = static_cast<uint32_t>(a.workers);
     if (a.whole) {
-        p.seq = static_cast<int32_t>(w / heads);
+        p.seq = static_cast<int32_t>(attn_over(w, a.over_heads));
         p.cost = 0;
         return p;
     }
@@ -146,7 +161,7 @@ __device__ __forceinline__ AttnPlan attn_plan(const AttnArgs &a, uint32_t w) {
     p.each = few ? 2 : static_cast<int32_t>((total + workers - 1) / workers);
     const uint32_t x = w * static_cast<uint32_t>(p.each);
     if (x >= total || a.n_seq == 1) return p;
-    const int32_t y = static_cast<int32_t>(x / heads);
+    const int32_t y = static_cast<int32_t>(attn_over(x, a.over_heads));
     for (;;) {
         // (the bound holds by itself unless the lengths change while they are read: then the rows are
         // wrong, but nothing outside the tables is touched)
@@ -176,7 +191,7 @@ __device__ __forceinline__ void attn_store(const AttnArgs &a, int64_t at, f32x4 
 // nothing was seen, and at least one otherwise (the maximum's own term).
 __device__ __forceinline__ void attn_finish(const AttnArgs &a, int32_t seq, int32_t h, int32_t row, int32_t d, f32x4 o,
                                             float m, float l) {
-    const int32_t i = row / a.group, head = h * a.group + row - i * a.group;
+    const int32_t i = static_cast<int32_t>(attn_over(static_cast<uint32_t>(row), a.over_group)), head = h * a.group + row - i * a.group;
     const int64_t tok = static_cast<int64_t>(seq) * a.q_len + i;
     const float r = l == 0.f ? 0.f : 1.f / l;
     attn_store(a, tok * a.ld_out + static_cast<int64_t>(head) * a.head_dim + d, o * r);

@@ -131,6 +131,8 @@ int launch_attn(const wsl_kv_cache *c, const void *q, int qfmt, int64_t n_seq, i
     a.group = static_cast<int32_t>(group), a.rows = static_cast<int32_t>(rows);
     a.head_dim = static_cast<int32_t>(c->head_dim), a.page_size = static_cast<int32_t>(c->page_size);
     a.n_pages = static_cast<int32_t>(c->n_pages);
+    a.over_page = attn_div(static_cast<uint32_t>(c->page_size)), a.over_group = attn_div(static_cast<uint32_t>(group));
+    a.over_heads = attn_div(static_cast<uint32_t>(c->n_kv));
     a.row_tiles = sh.row_tiles, a.tile_rows = sh.tile_rows, a.workers = static_cast<int32_t>(sh.workers);
     a.qfmt = qfmt, a.ofmt = ofmt;
     // the parts' sums first (16-byte aligned), then the open items, then the parts' maxima and sums

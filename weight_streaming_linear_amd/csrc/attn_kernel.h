@@ -69,7 +69,7 @@ __device__ __forceinline__ Look look_up(const AttnArgs &a, const int32_t *table,
     t += static_cast<int32_t>(threadIdx.x & 31);
     Look p = {0, 0};
     if (t < len) {
-        const uint32_t i = static_cast<uint32_t>(t) / static_cast<uint32_t>(a.page_size);
+        const uint32_t i = attn_over(static_cast<uint32_t>(t), a.over_page);
         p.at = t - static_cast<int32_t>(i * static_cast<uint32_t>(a.page_size));
         p.page = table[i];
     }
@@ -207,7 +207,7 @@ __device__ __forceinline__ void load_queries(const AttnArgs &a, int32_t seq, int
     for (int m = 0; m < MT; ++m) {
         const int32_t row = row0 + 16 * m + (lane & 15);
         const bool in_row = row < a.rows;
-        const int32_t i = in_row ? row / a.group : 0, head = h * a.group + (in_row ? row - i * a.group : 0);
+        const int32_t i = in_row ? static_cast<int32_t>(attn_over(static_cast<uint32_t>(row), a.over_group)) : 0, head = h * a.group + (in_row ? row - i * a.group : 0);
         const int64_t at = (static_cast<int64_t>(seq) * a.q_len + i) * a.ld_q + static_cast<int64_t>(head) * a.head_dim;
 #pragma unroll
         for (int c = 0; c < DP / 32; ++c) {
@@ -254,7 +254,7 @@ __device__ __forceinline__ void again(const int32_t *table, int32_t seq, int32_t
     constexpr int kVec = Values<FMT, DP>::kVec;
     const AttnArgs &a = fresh_args();
     const int g = fresh(static_cast<int>(threadIdx.x & 63)) >> 4;
-    const int32_t pos = row < a.rows ? row / a.group : 0, head = h * a.group + (row < a.rows ? row - pos * a.group : 0);
+    const int32_t pos = row < a.rows ? static_cast<int32_t>(attn_over(static_cast<uint32_t>(row), a.over_group)) : 0, head = h * a.group + (row < a.rows ? row - pos * a.group : 0);
     const int64_t at_q = (static_cast<int64_t>(seq) * a.q_len + pos) * a.ld_q + static_cast<int64_t>(head) * a.head_dim;
     m = -__builtin_huge_valf();
     l = 0.f;
@@ -262,7 +262,7 @@ __device__ __forceinline__ void again(const int32_t *table, int32_t seq, int32_t
     for (int j = 0; j < DP / 16; ++j) acc[j] = f32x4{0, 0, 0, 0};
     for (int32_t sub = t0; sub < t1; sub += kAttnTile)
         for (int32_t t = sub; t < sub + kAttnSub && t < len; ++t) {
-            const uint32_t i = static_cast<uint32_t>(t) / static_cast<uint32_t>(a.page_size);
+            const uint32_t i = attn_over(static_cast<uint32_t>(t), a.over_page);
             const int64_t page = table[i], at = t - static_cast<int32_t>(i * static_cast<uint32_t>(a.page_size));
             const bool see = t <= hi && (a.window == 0 || t > hi - a.window);
             if (page < 0 || page >= a.n_pages || !__any(see)) continue;
@@ -301,12 +301,14 @@ __device__ __forceinline__ void again(const int32_t *table, int32_t seq, int32_t
     l = g == 0 ? l : 0.f;       // the lanes of a row add theirs up
 }
 
-// Waves of a SIMD that the registers are shared among (a workgroup is one wave on each): what is in
-// flight has to cover the memory's latency, and a wave has a round's keys and values under way.
+// Waves of a SIMD that the registers are shared among (a workgroup is one wave on each): as many as do
+// without scratch memory.  What is in flight has to cover the memory's latency, and a wave has a round's
+// keys and values under way; more waves with spilled registers lost (8 sequences of 8192 tokens in e4m3,
+// heads of 256, fp32 queries: 106 us with two, 73 with one), and more without (three instead of two in
+// e4m3 at 128) changed nothing.
 template <int FMT, int DP, int MT, int QT>
 constexpr int attn_waves() {
-    if (DP > 128) return FMT == WSL_KV_BF16 ? 1 : 2;
-    if (FMT == WSL_KV_BF16) return DP == 64 ? 3 : 2;
+    if (DP > 128) return FMT == WSL_KV_BF16 || (DP > 192 && QT == 3) ? 1 : 2;
     return DP == 64 ? 3 : 2;
 }
 
@@ -380,7 +382,7 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
             const int32_t row = row0 + 16 * i + (lane & 15);
-            hi_t[i] = row < a.rows ? len - a.q_len + row / a.group : -1;
+            hi_t[i] = row < a.rows ? len - a.q_len + static_cast<int32_t>(attn_over(static_cast<uint32_t>(row), a.over_group)) : -1;
         }
         // positions that every row sees: [all_lo, all_hi]; that some row sees: from any_lo on
         const int32_t all_hi = len - a.q_len;
