@@ -701,11 +701,11 @@ def verify_drafts(p, q, drafts, u, n_drafts=None, accepted=None, tokens=None, wo
     if status is not None:
         _status(status, dev)
     if accepted is None:
-        accepted = _new((n_seq,), torch.int32, dev, stream)
+        accepted = drafts.new_empty((n_seq,)) if stream is None else _new((n_seq,), torch.int32, dev, stream)
     else:
         _plain(accepted, "accepted", torch.int32, dev, (n_seq,))
     if tokens is None:
-        tokens = _new((n_seq, rows), torch.int32, dev, stream)
+        tokens = drafts.new_empty((n_seq, rows)) if stream is None else _new((n_seq, rows), torch.int32, dev, stream)
     else:
         _plain(tokens, "tokens", torch.int32, dev, (n_seq, rows))
     if workspace is None:
