@@ -82,7 +82,9 @@ def test_drafts_see_what_is_before_them(e4m3, ql, wide):
     (6, 3, 192, 16, True, 1, False, "phtd"), (10, 2, 256, 40, False, 1, True, "phtd"),
     (64, 2, 256, 16, True, 2, False, "phtd"), (33, 3, 64, 5, False, 9, True, "phtd"),
     (128, 1, 64, 16, False, 3, False, "phtd"), (5, 1, 48, 16, True, 7, False, "pthd"),
-    (2, 2, 144, 16, False, 17, True, "phtd"), (20, 4, 112, 128, True, 40, False, "phtd")])
+    (2, 2, 144, 16, False, 17, True, "phtd"), (20, 4, 112, 128, True, 40, False, "phtd"),
+    (24, 2, 192, 16, False, 2, False, "phtd"), (18, 1, 160, 7, False, 3, False, "pthd"), (17, 1, 192, 16, True, 2, False, "phtd"),
+    (9, 1, 208, 16, False, 2, False, "phtd"), (3, 1, 240, 24, True, 6, True, "phtd"), (20, 1, 176, 16, True, 1, False, "pthd")])
 @pytest.mark.parametrize("ofmt", [wsl.WSL_OUT_F32, wsl.WSL_OUT_BF16])
 def test_head_layouts(heads, n_kv, dim, page, e4m3, ql, f32, order, ofmt):
     _run(3, [130, 1, 517, 40], heads, n_kv, dim, page, e4m3, ql=ql, f32=f32, order=order, ofmt=ofmt)
@@ -113,6 +115,31 @@ def test_long_and_many(e4m3, n, heads, n_kv):
     longest = 6000 if n <= 3 else 400
     lens = [longest] + [int(x) for x in np.exp(g.uniform(0, np.log(longest), n - 1))]
     _run(5 + n, lens, heads, n_kv, 128, 16, e4m3)
+
+
+def test_65535_sequences():
+    """As many sequences as a call takes, on shared pages: three divisions among 64 lanes."""
+    import torch
+    n, pages, page = 65535, 40, 16
+    g = torch.Generator(device="cuda").manual_seed(9)
+    k, v = (torch.randn((pages, 1, page, 16), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    table = torch.randint(0, pages, (n, 36), generator=g, device="cuda", dtype=torch.int32)
+    lens = torch.randint(0, 33, (n,), generator=g, device="cuda", dtype=torch.int32)
+    q = torch.randn((n, 1, 1, 16), generator=g, device="cuda").to(torch.bfloat16)
+    cache = wsl.KVCache(k, v)
+    for wide in (2, 36):        # 32 tokens of room: whole items; 576: shares
+        out = wsl.attn_decode(cache, q, table[:, :wide].contiguous(), lens)
+        kk, vv = (t[table[:, :2].long(), 0].flatten(1, 2).double() for t in (k, v))
+        s = (kk @ q[:, 0, 0, :, None].double())[..., 0] * 0.25
+        seen = torch.arange(32, device="cuda") < lens[:, None]
+        s = s.masked_fill(~seen, -torch.inf)
+        w = torch.softmax(s, -1).nan_to_num(0)
+        ref = (w[:, None] @ vv)[:, 0]
+        extra = {"pv": (w[:, None] @ vv.abs())[:, 0].cpu().numpy(),
+                 "score": (kk.abs() @ q[:, 0, 0, :, None].double().abs())[..., 0].amax(-1).mul(0.25).cpu().numpy()}
+        ref = ref.cpu().numpy()
+        bound = od.attn_bound(extra, 16, 32, ref, 2.0 ** -8)
+        assert (np.abs(f32_of(out)[:, 0, 0] - ref) <= bound).all()
 
 
 def test_scales_and_large_scores():

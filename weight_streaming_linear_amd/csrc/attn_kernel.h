@@ -631,8 +631,8 @@ void go(AttnArgs &a, hipStream_t s) {
 template <int FMT, int DP>
 void go_rows(AttnArgs &a, int mt, hipStream_t s) {
     if (a.qfmt != WSL_OUT_BF16) go<FMT, DP, 1, 3>(a, s);
-    else if (mt == 1 || DP > 128) go<FMT, DP, 1, 1>(a, s);
-    else if constexpr (DP <= 128) go<FMT, DP, 2, 1>(a, s);
+    else if (mt == 1) go<FMT, DP, 1, 1>(a, s);
+    else if constexpr (DP <= (FMT == WSL_KV_BF16 ? 192 : 128)) go<FMT, DP, 2, 1>(a, s);
 }
 
 }  // namespace
