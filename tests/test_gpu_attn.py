@@ -86,8 +86,10 @@ def test_drafts_see_what_is_before_them(e4m3, ql, wide):
     (24, 2, 192, 16, False, 2, False, "phtd"), (18, 1, 160, 7, False, 3, False, "pthd"), (17, 1, 192, 16, True, 2, False, "phtd"),
     (9, 1, 208, 16, False, 2, False, "phtd"), (3, 1, 240, 24, True, 6, True, "phtd"), (20, 1, 176, 16, True, 1, False, "pthd")])
 @pytest.mark.parametrize("ofmt", [wsl.WSL_OUT_F32, wsl.WSL_OUT_BF16])
-def test_head_layouts(heads, n_kv, dim, page, e4m3, ql, f32, order, ofmt):
-    _run(3, [130, 1, 517, 40], heads, n_kv, dim, page, e4m3, ql=ql, f32=f32, order=order, ofmt=ofmt)
+@pytest.mark.parametrize("room", [0, 70000])
+def test_head_layouts(heads, n_kv, dim, page, e4m3, ql, f32, order, ofmt, room):
+    """room: tokens that may yet come; with many, a workgroup takes two blocks of 16 rows."""
+    _run(3, [130, 1, 517, 40], heads, n_kv, dim, page, e4m3, ql=ql, f32=f32, order=order, ofmt=ofmt, wide=room // page)
 
 
 @pytest.mark.parametrize("e4m3,page", [(False, 16), (True, 24)])
@@ -188,10 +190,12 @@ def test_masked_places_may_hold_anything():
     (128, 5, 1, 5, 0, False, False, 16), (128, 5, 1, 5, 0, True, False, 24), (128, 40, 2, 3, 100, False, True, 16),
     (256, 4, 1, 4, 0, False, False, 16), (256, 4, 1, 4, 60, True, True, 7), (192, 6, 2, 2, 0, False, True, 16),
     (80, 12, 1, 5, 33, False, False, 16), (64, 16, 1, 4, 0, False, False, 48), (48, 2, 2, 6, 0, True, False, 1)])
-def test_odd_values_reach_only_what_sees_them(dim, heads, n_kv, ql, window, f32, e4m3, page):
+@pytest.mark.parametrize("room", [0, 70000])
+def test_odd_values_reach_only_what_sees_them(dim, heads, n_kv, ql, window, f32, e4m3, page, room):
     """NaNs among the values: in the newest positions (seen by the last queries alone) and before the
     window's reach of the last ones; sequences of one and of many parts.  What sees none is as exact as
     ever; what sees one is NaN in that element and exact in the others."""
+    import torch
     say(f"attn odd dim={dim} heads={heads}/{n_kv} q_len={ql} window={window} f32={f32} e4m3={e4m3} page={page}")
     lens = [130, 3000, 9]
 
@@ -204,6 +208,7 @@ def test_odd_values_reach_only_what_sees_them(dim, heads, n_kv, ql, window, f32,
             x[max(0, n - ql - window + 1), :, 7] = np.nan      # seen by the first query alone
 
     c = CacheCase(40 + ql, lens, n_kv, dim, page, e4m3, "cuda", v_fill=fill)
+    c.table = torch.cat((c.table, torch.full((3, room // page), -1, dtype=torch.int32, device="cuda")), 1)
     q = _q(40, 3, ql, heads, dim, f32)
     got = f32_of(wsl.attn_decode(c.cache, q, c.table, c.kv_lens, window=window))
     for b, n in enumerate(lens):

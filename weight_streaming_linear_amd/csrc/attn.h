@@ -33,6 +33,12 @@ inline AttnDiv attn_div(uint32_t by) {
 }
 __device__ __forceinline__ uint32_t attn_over(uint32_t n, const AttnDiv &d) { return (__umulhi(n, d.mul) + n) >> d.shift; }
 
+// Two blocks of 16 rows in a workgroup at one time: where the registers allow (figures: blocks_of).
+constexpr bool attn_two_blocks(int fmt, int qfmt, int64_t head_dim) {
+    if (qfmt == WSL_OUT_BF16) return head_dim <= (fmt == WSL_KV_BF16 ? 192 : 128);
+    return fmt == WSL_KV_BF16 && head_dim > 64 && head_dim <= 128;
+}
+
 struct AttnArgs {
     AttnDiv over_page, over_group, over_heads;
     const char *k, *v;

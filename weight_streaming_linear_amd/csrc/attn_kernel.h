@@ -309,7 +309,7 @@ __device__ __forceinline__ void again(const int32_t *table, int32_t seq, int32_t
 template <int FMT, int DP, int MT, int QT>
 constexpr int attn_waves() {
     if (DP > 128) return FMT == WSL_KV_BF16 || (DP > 192 && QT == 3) ? 1 : 2;
-    return DP == 64 ? 3 : 2;
+    return QT == 3 && MT == 2 ? 1 : DP == 64 ? 3 : 2;
 }
 
 // One pass over a range of token tiles with the running maximum and sum of a softmax:
@@ -630,9 +630,13 @@ void go(AttnArgs &a, hipStream_t s) {
 
 template <int FMT, int DP>
 void go_rows(AttnArgs &a, int mt, hipStream_t s) {
-    if (a.qfmt != WSL_OUT_BF16) go<FMT, DP, 1, 3>(a, s);
-    else if (mt == 1) go<FMT, DP, 1, 1>(a, s);
-    else if constexpr (DP <= (FMT == WSL_KV_BF16 ? 192 : 128)) go<FMT, DP, 2, 1>(a, s);
+    if (a.qfmt != WSL_OUT_BF16) {
+        if (mt == 1) go<FMT, DP, 1, 3>(a, s);
+        else if constexpr (attn_two_blocks(FMT, WSL_OUT_F32, DP)) go<FMT, DP, 2, 3>(a, s);
+        return;
+    }
+    if (mt == 1) go<FMT, DP, 1, 1>(a, s);
+    else if constexpr (attn_two_blocks(FMT, WSL_OUT_BF16, DP)) go<FMT, DP, 2, 1>(a, s);
 }
 
 }  // namespace
