@@ -60,40 +60,39 @@ __device__ __forceinline__ void wave_lds_fence() {
 }
 
 // Lane l's token (l % 32) of 32 successive ones: its place in its page, and its page as the table
-// names it.  The table is read two rounds before the tokens are, so that nobody waits for it.
+// names it.  The table is read two rounds before the tokens are, so that nobody waits for it.  Tokens
+// from `end` on stand for the last one before it (and for the first, if there is none): the load is
+// made in any case, as all are (see attn_kernel).
 struct Look {
     int32_t at, page;
 };
 
-__device__ __forceinline__ Look look_up(const AttnArgs &a, const int32_t *table, int32_t len, int32_t t) {
+__device__ __forceinline__ Look look_up(const AttnArgs &a, const int32_t *table, int32_t end, int32_t t) {
     t += static_cast<int32_t>(threadIdx.x & 31);
-    Look p = {0, 0};
-    if (t < len) {
-        const uint32_t i = attn_over(static_cast<uint32_t>(t), a.over_page);
-        p.at = t - static_cast<int32_t>(i * static_cast<uint32_t>(a.page_size));
-        p.page = table[i];
-    }
+    t = t < end ? t : end - 1;
+    t = t < 0 ? 0 : t;
+    const uint32_t i = attn_over(static_cast<uint32_t>(t), a.over_page);
+    Look p;
+    p.at = t - static_cast<int32_t>(i * static_cast<uint32_t>(a.page_size));
+    p.page = table[i];
     return p;
 }
 
 // The byte offsets of the 32 tokens from t on go into LDS (their scale bytes are fetched); returns
-// which of the tokens are there at all: before the sequence's end, on a page that the cache has.
-// A token that is not there gets a safe offset and the scale 1.
+// which of the tokens are there at all: before `end`, on a page that the cache has.  A token that is
+// not there gets a safe offset and the scale 1.
 template <int FMT>
-__device__ __forceinline__ uint32_t find_tokens(const AttnArgs &a, WaveLds &w, const Look &p, int32_t h, int32_t len,
+__device__ __forceinline__ uint32_t find_tokens(const AttnArgs &a, WaveLds &w, const Look &p, int32_t h, int32_t end,
                                                 int32_t t, uint32_t &kb, uint32_t &vb, bool &bad) {
     const int32_t lane = static_cast<int32_t>(threadIdx.x & 31);
-    const bool in = t + lane < len, ok = in && static_cast<uint32_t>(p.page) < static_cast<uint32_t>(a.n_pages);
+    const bool in = t + lane < end, ok = in && static_cast<uint32_t>(p.page) < static_cast<uint32_t>(a.n_pages);
     bad |= in && !ok;
     const int64_t page = ok ? p.page : 0, at = ok ? p.at : 0;
     wave_lds_fence();
     w.off[lane] = page * a.page_stride + h * a.head_stride + at * a.token_stride;
     if constexpr (FMT == WSL_KV_E4M3) {
-        kb = vb = 127;
-        if (ok) {
-            const int64_t cell = (page * a.n_kv + h) * a.page_size + at;
-            kb = a.ke[cell], vb = a.ve[cell];
-        }
+        const int64_t cell = (page * a.n_kv + h) * a.page_size + at;
+        kb = a.ke[cell], vb = a.ve[cell];
     }
     wave_lds_fence();
     return static_cast<uint32_t>(__ballot(ok));
@@ -198,42 +197,54 @@ __device__ __forceinline__ void keep_values(Values<FMT, DP> &v, uint32_t keep) {
 }
 
 // Query rows as the B operand: lane l holds row l % 16 and the elements that match load_keys.
-// QT == 1: bf16 queries; QT == 3: fp32 queries as a sum of three bf16 numbers (24 bits).
-template <int FMT, int DP, int MT, int QT>
-__device__ __forceinline__ void load_queries(const AttnArgs &a, int32_t seq, int32_t h, int32_t row0,
-                                             u32x4 (&q)[MT][QT][DP / 32]) {
-    const int lane = static_cast<int>(threadIdx.x & 63), g = lane >> 4;
+// QT == 1: bf16 queries; QT == 3: fp32 queries as a sum of three bf16 numbers (24 bits).  All loads are
+// made, a row past the last one being the first again: a load in a branch could not be counted.
+template <int DP, int QT>
+struct Queries {
+    u32x4 x[DP / 32][QT == 1 ? 1 : 2];      // as loaded
+};
+template <int FMT, int DP, int QT, bool FULL>
+__device__ __forceinline__ void load_queries(const AttnArgs &a, int32_t seq, int32_t h, int32_t row, Queries<DP, QT> &q) {
+    const int g = static_cast<int>(threadIdx.x & 63) >> 4;
+    row = row < a.rows ? row : 0;
+    const int32_t i = static_cast<int32_t>(attn_over(static_cast<uint32_t>(row), a.over_group)), head = h * a.group + row - i * a.group;
+    const int64_t at = (static_cast<int64_t>(seq) * a.q_len + i) * a.ld_q + static_cast<int64_t>(head) * a.head_dim;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        const int32_t row = row0 + 16 * m + (lane & 15);
-        const bool in_row = row < a.rows;
-        const int32_t i = in_row ? static_cast<int32_t>(attn_over(static_cast<uint32_t>(row), a.over_group)) : 0, head = h * a.group + (in_row ? row - i * a.group : 0);
-        const int64_t at = (static_cast<int64_t>(seq) * a.q_len + i) * a.ld_q + static_cast<int64_t>(head) * a.head_dim;
+    for (int c = 0; c < DP / 32; ++c) {
+        const int d = FMT == WSL_KV_BF16 ? c * 32 + g * 8 : (c >> 1) * 64 + g * 16 + (c & 1) * 8;
+        const int64_t from = at + (FULL || d < a.head_dim ? d : 0);
+        if constexpr (QT == 1) {
+            q.x[c][0] = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.q) + from);
+        } else {
+            const u32x4 *src = reinterpret_cast<const u32x4 *>(static_cast<const float *>(a.q) + from);
+            q.x[c][0] = src[0], q.x[c][1] = src[1];
+        }
+    }
+}
+template <int FMT, int DP, int QT, bool FULL>
+__device__ __forceinline__ void split_queries(const AttnArgs &a, const Queries<DP, QT> &q, u32x4 (&out)[QT][DP / 32]) {
+    const int g = static_cast<int>(threadIdx.x & 63) >> 4;
 #pragma unroll
-        for (int c = 0; c < DP / 32; ++c) {
-            const int d = FMT == WSL_KV_BF16 ? c * 32 + g * 8 : (c >> 1) * 64 + g * 16 + (c & 1) * 8;
-            const bool in = in_row && d < a.head_dim;
-            if constexpr (QT == 1) {
-                u32x4 x = {0, 0, 0, 0};
-                if (in) x = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.q) + at + d);
-                q[m][0][c] = x;
-            } else {
-                f32x4 x[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-                if (in) {
-                    const f32x4 *src = reinterpret_cast<const f32x4 *>(static_cast<const float *>(a.q) + at + d);
-                    x[0] = src[0], x[1] = src[1];
+    for (int c = 0; c < DP / 32; ++c) {
+        const int d = FMT == WSL_KV_BF16 ? c * 32 + g * 8 : (c >> 1) * 64 + g * 16 + (c & 1) * 8;
+        const bool in = FULL || d < a.head_dim;
+        if constexpr (QT == 1) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) out[0][c][w] = in ? q.x[c][0][w] : 0;
+        } else {
+            f32x4 x[2] = {__builtin_bit_cast(f32x4, q.x[c][0]), __builtin_bit_cast(f32x4, q.x[c][1])};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) x[0][w] = in ? x[0][w] : 0.f, x[1][w] = in ? x[1][w] : 0.f;
+#pragma unroll
+            for (int t = 0; t < QT; ++t)
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const int half = w >> 1, e = 2 * (w & 1);
+                    const uint32_t b = pack_bf16x2(x[half][e], x[half][e + 1]);
+                    out[t][c][w] = b;
+                    x[half][e] -= bf16_lo(b);
+                    x[half][e + 1] -= bf16_hi(b);
                 }
-#pragma unroll
-                for (int t = 0; t < QT; ++t)
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const int half = w >> 1, e = 2 * (w & 1);
-                        const uint32_t b = pack_bf16x2(x[half][e], x[half][e + 1]);
-                        q[m][t][c][w] = b;
-                        x[half][e] -= bf16_lo(b);
-                        x[half][e + 1] -= bf16_hi(b);
-                    }
-            }
         }
     }
 }
@@ -326,6 +337,9 @@ constexpr int attn_waves() {
 // Each wave works on 32 tokens of its own in a round, and the four join at an item's end.  In a
 // round it asks for this round's values, then works on the keys that it asked for a round before,
 // asks for the next round's keys and the table's entries for the round after that.
+// No load stands in a branch: the waits count the loads since, and where there may be more or fewer of
+// them the compiler waits for all.  So a wave without tokens, and the keys after a range's last round, are
+// a row of the cache that nobody uses.
 // Bound: the cached keys and values, read once.  8 sequences of 32768 tokens, 8 kv heads of 128, bf16
 // (1.07 GB): 159 us, 6.7 TB/s, against 7.3 of a plain read.  Short calls are a chain of five trips to
 // memory (lengths, table, keys, values, result): 7 us for one sequence of 37 tokens.
@@ -375,10 +389,11 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void
 
         const int32_t t0 = (span.first + tile) * kAttnTile + wave * kAttnSub;
         const int32_t t1 = (span.first + tile + n) * kAttnTile < len ? (span.first + tile + n) * kAttnTile : len;
-        Look here = {0, 0};
-        if (t0 < t1) here = look_up(a, table, len, t0);
-        u32x4 q[MT][QT][DP / 32];
-        load_queries<FMT, DP, MT, QT>(a, seq, head, row0, q);
+        const Look here = look_up(a, table, t1, t0);
+        Queries<DP, QT> raw[MT];
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+            load_queries<FMT, DP, QT, FULL>(a, seq, head, row0 + 16 * i + (lane & 15), raw[i]);
         f32x4 acc[MT][DP / 16];
         float m[MT], l[MT];
         int32_t hi_t[MT];         // last position that the lane's row sees
@@ -404,12 +419,19 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void
         __builtin_amdgcn_sched_barrier(0);
         Keys<FMT, DP> k;
         Values<FMT, DP> v;
-        uint32_t kb = 127, vb = 127, there_next = 0;
-        Look next = {0, 0};
-        if (t0 < t1) {
-            there_next = find_tokens<FMT>(a, mem, here, head, len, t0, kb, vb, bad);
-            load_keys<FMT, DP, FULL>(a, mem, k);
-            next = look_up(a, table, len, t0 + kAttnTile);
+        uint32_t kb = 127, vb = 127;
+        u32x4 q[MT][QT][DP / 32];
+        uint32_t there_next = find_tokens<FMT>(a, mem, here, head, t1, t0, kb, vb, bad);
+        load_keys<FMT, DP, FULL>(a, mem, k);
+        Look next = look_up(a, table, t1, t0 + kAttnTile);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            split_queries<FMT, DP, QT, FULL>(a, raw[i], q[i]);
+            // they are here before the loop: in it, their wait would be one for a round's own loads
+#pragma unroll
+            for (int e = 0; e < QT; ++e)
+#pragma unroll
+                for (int c = 0; c < DP / 32; ++c) asm volatile("" : "+v"(q[i][e][c]));
         }
         for (int32_t t = t0; t < t1; t += kAttnTile) {
             const uint32_t there = there_next;
@@ -418,8 +440,9 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void
             f32x4 ks[2], vs[2];
             if constexpr (FMT == WSL_KV_E4M3) {
                 // (a byte of 255 is none that a write leaves; 254 keeps what it gives finite)
-                mem.ks[lane & 31] = __builtin_bit_cast(float, (kb < 254u ? kb : 254u) << 23);
-                mem.vs[lane & 31] = __builtin_bit_cast(float, (vb < 254u ? vb : 254u) << 23);
+                const bool ok = (there >> (lane & 31)) & 1;
+                mem.ks[lane & 31] = __builtin_bit_cast(float, (ok ? (kb < 254u ? kb : 254u) : 127u) << 23);
+                mem.vs[lane & 31] = __builtin_bit_cast(float, (ok ? (vb < 254u ? vb : 254u) : 127u) << 23);
                 wave_lds_fence();
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -456,11 +479,9 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void
                 }
             }
             // the next keys, in flight under the softmax and the product with V
-            if (t + kAttnTile < t1) {
-                there_next = find_tokens<FMT>(a, mem, next, head, len, t + kAttnTile, kb, vb, bad);
-                load_keys<FMT, DP, FULL>(a, mem, k);
-                if (t + 2 * kAttnTile < t1) next = look_up(a, table, len, t + 2 * kAttnTile);
-            }
+            there_next = find_tokens<FMT>(a, mem, next, head, t1, t + kAttnTile, kb, vb, bad);
+            load_keys<FMT, DP, FULL>(a, mem, k);
+            next = look_up(a, table, t1, t + 2 * kAttnTile);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
