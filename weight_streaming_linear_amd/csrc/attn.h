@@ -10,7 +10,7 @@ constexpr int kAttnSub = 32;                       // tokens a wave takes at a t
 constexpr int kAttnTile = kAttnWaves * kAttnSub;   // tokens a workgroup takes at a time
 constexpr int kAttnThreads = kAttnWaves * 64;
 constexpr int kAttnCus = 256;
-constexpr int kAttnMaxWaves = 4;                   // of a SIMD, over all variants
+constexpr int kAttnMaxWaves = 3;                   // of a SIMD, over all variants
 constexpr int64_t kAttnMaxTokens = 0x7fffffff - 4 * kAttnTile;   // positions stay in 32 bits some rounds past the end
 constexpr int kAttnJoinRows = 4;                   // rows a workgroup of the joining kernel takes
 
@@ -90,8 +90,8 @@ __device__ __forceinline__ AttnSpan attn_span(const AttnArgs &a, int32_t raw) {
 // Where equal shares of tiles alone end with the items, or are a tile or two, there is nothing to weigh
 // up (cost 0).  (16 sequences of up to 4224 tokens with five queries 32.2 us at cost 0, 31.5, 30.5, 30.9,
 // 30.9 and 31.8 at 1, 2, 3, 4 and 6; 32 of up to 8192 in e4m3 44.9, 44.5, 43.3, 44.0, 44.5 and 45.7.)
-// A few long items are not cut finer than two tiles where that leaves most workers one each: half as
-// many parts are to be joined (one sequence of 8192 tokens, 8 kv heads: 16.1 -> 15.2 us).
+// A few long items are not cut finer than two tiles where that leaves a worker for most compute units:
+// half as many parts are to be joined (one sequence of 8192 tokens, 8 kv heads: 16.1 -> 15.2 us).
 // The lengths are on the device, so every wave works this out for itself: without LDS or barriers,
 // each lane adds up the units of `per` successive sequences, a scan over the lanes finds the lane whose
 // sequences hold the wanted unit, and its sequences are divided among the lanes again until one is left.
@@ -155,7 +155,7 @@ __device__ __forceinline__ AttnPlan attn_plan(const AttnArgs &a, uint32_t w) {
     if (per == 1) {
         const uint32_t tiles = total - heads * static_cast<uint32_t>(count) * kAttnCost;
         const uint32_t each = (tiles + workers - 1) / workers;
-        few = each == 1 && 2 * tiles > workers && tiles >= 16 * heads * static_cast<uint32_t>(count);
+        few = each == 1 && tiles > kAttnCus && tiles >= 16 * heads * static_cast<uint32_t>(count);
         if (each <= 2 || !__any(lane < count && static_cast<uint32_t>(mine - kAttnCost) % each != 0)) {
             p.cost = 0;
             run -= (lane < count ? lane + 1 : count) * kAttnCost;

@@ -89,10 +89,10 @@ struct AttnShape {
 // tokens, bf16: 59 us against 75 with one, over e4m3 26.0 against 25.8; at 256, with spilled registers,
 // 41.7 against 36.3; fp32 queries, 25 rows of 128, 16 sequences of up to 4224 tokens: 33.6 against 39.2,
 // over e4m3 33.8 against 29.0, at 64 24.9 against 25.4) and there is enough to do for all compute units
-// (25 rows of 128, one sequence of 300 tokens 11.2 against 8.8, of 2000 15.2 against 13.2, of 8192 18.2
-// against 20.0; 64 of up to 500 19.8 against 27.5).
-int blocks_of(int fmt, int qfmt, int64_t rows, int64_t head_dim, int64_t shares) {
-    if (rows <= 16 || shares <= 2 * kAttnCus / ((rows + 15) / 16)) return 1;
+// (25 rows of 128, one sequence of 300 tokens 11.2 against 8.8, of 4000 14.8 against 13.8, of 8192 18.2
+// against 20.0; 16 of up to 500 13.5 against 10.8, 32 of them 13.2 against 17.1).
+int blocks_of(int fmt, int qfmt, int64_t rows, int64_t head_dim, bool whole, int64_t shares) {
+    if (rows <= 16 || shares <= (whole ? 1 : 2) * kAttnCus / ((rows + 15) / 16)) return 1;
     return attn_two_blocks(fmt, qfmt, head_dim) ? 2 : 1;
 }
 
@@ -100,7 +100,7 @@ AttnShape shape_of(int fmt, int qfmt, int64_t n_seq, int64_t rows, int64_t n_kv,
     AttnShape s;
     const int64_t tiles = (capacity + kAttnTile - 1) / kAttnTile, items = n_seq * n_kv;
     s.whole = attn_whole(tiles, items);
-    s.mt = blocks_of(fmt, qfmt, rows, head_dim, s.whole || tiles > (1 << 20) ? items : items * tiles);
+    s.mt = blocks_of(fmt, qfmt, rows, head_dim, s.whole, s.whole || tiles > (1 << 20) ? items : items * tiles);
     s.tile_rows = static_cast<int>(rows < 16 * s.mt ? rows : 16 * s.mt);
     s.row_tiles = static_cast<int>((rows + s.tile_rows - 1) / s.tile_rows);
     const int64_t fit = kAttnCus * kAttnMaxWaves, most = s.row_tiles * 8 >= fit ? 8 : fit / s.row_tiles / 8 * 8;

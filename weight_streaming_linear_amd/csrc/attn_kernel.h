@@ -315,12 +315,13 @@ __device__ __forceinline__ void again(const int32_t *table, int32_t seq, int32_t
 // Waves of a SIMD that the registers are shared among (a workgroup is one wave on each): as many as do
 // without scratch memory.  What is in flight has to cover the memory's latency, and a wave has a round's
 // keys and values under way; more waves with spilled registers lost (8 sequences of 8192 tokens in e4m3,
-// heads of 256, fp32 queries: 106 us with two, 73 with one), and more without (three instead of two in
-// e4m3 at 128) changed nothing.
+// heads of 256, fp32 queries: 106 us with two, 73 with one; 16 of up to 4224 with 25 rows of 64 21.5 with
+// three, 20.2 with two), and more without did not help (three instead of two in e4m3 at 128: 32 ragged
+// sequences 44.7 against 42.4).
 template <int FMT, int DP, int MT, int QT>
 constexpr int attn_waves() {
     if (DP > 128) return FMT == WSL_KV_BF16 || (DP > 192 && QT == 3) ? 1 : 2;
-    return QT == 3 && MT == 2 ? 1 : DP == 64 ? 3 : 2;
+    return QT == 3 && MT == 2 ? 1 : DP == 64 && MT == 1 ? 3 : 2;
 }
 
 // One pass over a range of token tiles with the running maximum and sum of a softmax:
@@ -635,12 +636,17 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void
     if (__any(bad) && lane == 0 && a.status != nullptr) atomicOr(a.status, WSL_STATUS_INDEX);
 }
 
-// Workgroups for all row tiles together fill the chip once, or there is one for each item and row tile.
+// There is a workgroup for each whole item and row tile; or else, over bf16, one for each compute unit:
+// its four waves' rounds of 16 KB keep the memory busy, and fewer shares have fewer beginnings, ends and
+// parts (two on each: 16 sequences of up to 4224 tokens with five queries 30.1 us against 27.7, 64 of up to
+// 2048 47.9 against 44.5, 8 of 32768 164.9 against 163.9); over e4m3, whose rounds are half as long, as
+// many as the registers allow (one: 32 ragged sequences 45.3 against 42.4).
 // Those of one token range lie `workers` apart, a multiple of 8 where it can be, so that they run at the
 // same time on the same XCD and what one reads the others find in its L2.
 template <int FMT, int DP, int MT, int QT>
 void go(AttnArgs &a, hipStream_t s) {
-    const int fit = kAttnCus * attn_waves<FMT, DP, MT, QT>();
+    const int fit = kAttnCus * (FMT == WSL_KV_BF16 ? 1 : attn_waves<FMT, DP, MT, QT>());
+    static_assert(attn_waves<FMT, DP, MT, QT>() <= kAttnMaxWaves, "workspaces are for so many");
     const int most = a.row_tiles * 8 >= fit ? 8 : fit / a.row_tiles / 8 * 8;
     if (a.whole) a.workers = a.n_seq * a.n_kv;
     else a.workers = a.workers < most ? a.workers : most;
