@@ -342,7 +342,7 @@ constexpr int attn_waves() {
 // them the compiler waits for all.  So a wave without tokens, and the keys after a range's last round, are
 // a row of the cache that nobody uses.
 // Bound: the cached keys and values, read once.  8 sequences of 32768 tokens, 8 kv heads of 128, bf16
-// (1.07 GB): 159 us, 6.7 TB/s, against 7.3 of a plain read.  Short calls are a chain of five trips to
+// (1.07 GB): 160 us, 6.7 TB/s, against 7.3 of a plain read.  Short calls are a chain of five trips to
 // memory (lengths, table, keys, values, result): 7 us for one sequence of 37 tokens.
 template <int FMT, int DP, int MT, int QT, bool FULL>
 __global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void attn_kernel(AttnArgs a) {
