@@ -666,6 +666,8 @@ def _prob_rows(t, name, device, shape):
     ld = st[1] if shape[1] > 1 else (st[0] if shape[0] > 1 else shape[2])
     if shape[0] > 1 and st[0] != shape[1] * ld:
         raise ValueError(f"{name}: the first two dimensions must step as one (strides {st})")
+    if ld < shape[2]:
+        raise ValueError(f"{name}: rows of {shape[2]} entries lie {ld} apart (a broadcast tensor needs .contiguous())")
     return ld
 
 
@@ -674,9 +676,9 @@ def verify_drafts(p, q, drafts, u, n_drafts=None, accepted=None, tokens=None, wo
     """Which drafts stand, and the token after them, from given random numbers.
 
     p: [n_seq][width + 1][vocab] target probabilities, q: [n_seq][width][vocab] the drafter's, or
-    None where each draft was certain (fp32 or bf16, the same); drafts: int32 [n_seq][width]; u:
-    fp32 [n_seq][width + 1] in [0, 1); n_drafts: int32 [n_seq], width unless given.  Returns
-    (accepted int32 [n_seq], tokens int32 [n_seq][width + 1]: the drafts that stand, the next
+    None where each draft was certain (fp32 or bf16, the same; every row in memory of its own, none
+    broadcast); drafts: int32 [n_seq][width]; u: fp32 [n_seq][width + 1] in [0, 1); n_drafts: int32
+    [n_seq], width unless given.  Returns (accepted int32 [n_seq], tokens int32 [n_seq][width + 1]: the drafts that stand, the next
     token, -1s)."""
     import torch
     if p.dim() != 3 or not p.is_cuda:
@@ -688,7 +690,8 @@ def verify_drafts(p, q, drafts, u, n_drafts=None, accepted=None, tokens=None, wo
         raise ValueError("p: no rows")
     pfmt = _float_format(p, "p")
     ld_p, ld_q = _prob_rows(p, "p", dev, (n_seq, rows, vocab)), 0
-    if q is not None and width:
+    has_q = q is not None and width > 0
+    if has_q:
         if q.dtype is not p.dtype:
             raise ValueError(f"q: dtype {q.dtype}, p has {p.dtype}")
         ld_q = _prob_rows(q, "q", dev, (n_seq, width, vocab))
@@ -715,7 +718,7 @@ def verify_drafts(p, q, drafts, u, n_drafts=None, accepted=None, tokens=None, wo
     else:
         _require(workspace, "workspace", (workspace.dtype,), device=dev, contiguous=True)
         ws_bytes = workspace.numel() * workspace.element_size()
-    rc = lib().verify_drafts(p.data_ptr(), q.data_ptr() if ld_q else None, pfmt, n_seq, width, vocab, ld_p, ld_q,
+    rc = lib().verify_drafts(p.data_ptr(), q.data_ptr() if has_q else None, pfmt, n_seq, width, vocab, ld_p, ld_q,
                              drafts.data_ptr(), _ptr(n_drafts), u.data_ptr(), accepted.data_ptr(), tokens.data_ptr(),
                              _ptr(workspace), ws_bytes, _ptr(status), _stream(stream))
     if rc:
