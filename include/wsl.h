@@ -424,7 +424,8 @@ int kv_cache_read(const wsl_kv_cache *h_cache, const int64_t *d_slots, int64_t c
  *            pages_per_seq (1 .. ld_table) entries of a row may be read.
  * d_kv_lens  device int32 [n_seq]: read by the kernels only, so a captured call goes on with
  *            lengths that grow.  One outside [0, pages_per_seq * page_size] is clamped to it
- *            and reported; so is, as if it were not seen, a token whose page is outside [0, n_pages).
+ *            and reported; so is, as if it were not seen, a token that a query sees and whose page is
+ *            outside [0, n_pages) (entries of pages that lie wholly behind the window may be anything).
  * scale      the factor of the scores.  window >= 0 (0: none).
  * d_out      device [n_seq * q_len][ld_out] of ofmt, 16-byte aligned, ld_out a multiple of 16 bytes.
  * d_lse      device fp32 [n_seq][q_len][n_heads] or NULL: log sum_t exp(s_t), -infinity where

@@ -31,3 +31,41 @@ def test_a_drafter_with_one_distribution_for_every_position(n, width, vocab):
     for b in range(n):
         r, t = od.verify_ref(f32_of(p)[b], f32_of(q)[b], drafts[b].cpu().numpy(), u[b].cpu().numpy(), width, vocab)
         assert acc[b].item() == r and np.array_equal(tok[b].cpu().numpy(), t)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("ql", [1, 5])
+@pytest.mark.parametrize("lens,window,page,wide", [
+    ([500, 400, 385, 384, 383, 260, 129, 128, 90, 3], 100, 16, 0), ([511, 300, 257, 200], 33, 24, 0),
+    ([1100, 1151, 1152, 1153, 1279, 1280, 1281, 1025, 1024, 700], 1024, 16, 0), ([130, 3000, 40, 555], 1, 7, 100),
+    ([4099], 300, 16, 500)])
+def test_pages_behind_the_window_may_be_gone(lens, window, page, wide, ql, e4m3):
+    """Table entries of pages that no query sees any more are -1, wherever the window begins in a tile:
+    nothing is reported.  A page that some query sees is; in whole items and in shares."""
+    import torch
+    heads, n_kv, dim = 4, 2, 64
+    say(f"attn window {window} q_len={ql} page={page} e4m3={e4m3} lens={lens[:5]} wide={wide}")
+    c = CacheCase(80 + ql, lens, n_kv, dim, page, e4m3, "cuda")
+    lowest = [max(0, n - ql - window + 1) for n in lens]
+    for b, lo in enumerate(lowest):
+        c.table[b, :lo // page] = -1
+    c.table = torch.cat((c.table, torch.full((len(lens), wide), -1, dtype=torch.int32, device="cuda")), 1)
+    q = torch.randn((len(lens), ql, heads, dim), device="cuda", generator=torch.Generator("cuda").manual_seed(5)).to(torch.bfloat16)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def check(bad=None):
+        out = f32_of(wsl.attn_decode(c.cache, q, c.table, c.kv_lens, window=window, status=st))
+        for b, n in enumerate(lens):
+            if b != bad:
+                ref, _, extra = od.attn_ref(f32_of(q)[b], c.values[0][b], c.values[1][b], n, dim ** -0.5, window)
+                assert (np.abs(out[b] - ref) <= od.attn_bound(extra, dim, n, ref, 2.0 ** -8)).all(), f"sequence {b}"
+
+    check()
+    assert st.item() == 0
+    for b in range(len(lens)):      # the page of the lowest token that is seen, and that of the newest
+        for at in (lowest[b] // page, (lens[b] - 1) // page):
+            st.zero_()
+            was, c.table[b, at] = c.table[b, at].item(), -1
+            check(b)
+            assert st.item() == wsl.WSL_STATUS_INDEX, f"sequence {b}"
+            c.table[b, at] = was

@@ -69,15 +69,17 @@ struct AttnSpan {
     bool bad;
 };
 
+// The lowest position that some row of a sequence of `len` tokens sees.
+__device__ __forceinline__ int32_t attn_lowest(const AttnArgs &a, int32_t len) {
+    const int64_t lo = static_cast<int64_t>(len) - a.q_len - a.window + 1;
+    return a.window > 0 && lo > 0 ? static_cast<int32_t>(lo) : 0;
+}
+
 __device__ __forceinline__ AttnSpan attn_span(const AttnArgs &a, int32_t raw) {
     AttnSpan s;
     s.bad = raw < 0 || raw > a.capacity;
     s.len = raw < 0 ? 0 : (raw > a.capacity ? a.capacity : raw);
-    s.first = 0;
-    if (a.window > 0) {
-        const int64_t lo = static_cast<int64_t>(s.len) - a.q_len - a.window + 1;
-        if (lo > 0) s.first = static_cast<int32_t>(lo / kAttnTile);
-    }
+    s.first = attn_lowest(a, s.len) / kAttnTile;
     const int32_t n = (s.len + kAttnTile - 1) / kAttnTile - s.first;
     s.tiles = n > 0 ? n : 1;
     return s;

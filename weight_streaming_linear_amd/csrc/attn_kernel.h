@@ -79,13 +79,15 @@ __device__ __forceinline__ Look look_up(const AttnArgs &a, const int32_t *table,
 }
 
 // The byte offsets of the 32 tokens from t on go into LDS (their scale bytes are fetched); returns
-// which of the tokens are there at all: before `end`, on a page that the cache has.  A token that is
-// not there gets a safe offset and the scale 1.
+// which of the tokens are there at all: from `low` on and before `end`, on a page that the cache has
+// (bad: one between the two is not).  A token that is not there gets a safe offset and the scale 1.
+// `low`, the lowest position that some row sees, may lie inside the first tile: what is before it is
+// nobody's, and its page may be gone.
 template <int FMT>
-__device__ __forceinline__ uint32_t find_tokens(const AttnArgs &a, WaveLds &w, const Look &p, int32_t h, int32_t end,
-                                                int32_t t, uint32_t &kb, uint32_t &vb, bool &bad) {
+__device__ __forceinline__ uint32_t find_tokens(const AttnArgs &a, WaveLds &w, const Look &p, int32_t h, int32_t low,
+                                                int32_t end, int32_t t, uint32_t &kb, uint32_t &vb, bool &bad) {
     const int32_t lane = static_cast<int32_t>(threadIdx.x & 31);
-    const bool in = t + lane < end, ok = in && static_cast<uint32_t>(p.page) < static_cast<uint32_t>(a.n_pages);
+    const bool in = t + lane >= low && t + lane < end, ok = in && static_cast<uint32_t>(p.page) < static_cast<uint32_t>(a.n_pages);
     bad |= in && !ok;
     const int64_t page = ok ? p.page : 0, at = ok ? p.at : 0;
     wave_lds_fence();
@@ -403,10 +405,10 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void
             const int32_t row = row0 + 16 * i + (lane & 15);
             hi_t[i] = row < a.rows ? len - a.q_len + static_cast<int32_t>(attn_over(static_cast<uint32_t>(row), a.over_group)) : -1;
         }
-        // positions that every row sees: [all_lo, all_hi]; that some row sees: from any_lo on
+        // positions that every row sees: [all_lo, all_hi]; that some row sees: from low on
         const int32_t all_hi = len - a.q_len;
         const int64_t all_lo = a.window > 0 ? static_cast<int64_t>(len) - a.window : 0;
-        const int64_t any_lo = a.window > 0 ? static_cast<int64_t>(len) - a.q_len - a.window + 1 : 0;
+        const int32_t low = attn_lowest(a, len);
 
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
@@ -422,7 +424,7 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void
         Values<FMT, DP> v;
         uint32_t kb = 127, vb = 127;
         u32x4 q[MT][QT][DP / 32];
-        uint32_t there_next = find_tokens<FMT>(a, mem, here, head, t1, t0, kb, vb, bad);
+        uint32_t there_next = find_tokens<FMT>(a, mem, here, head, low, t1, t0, kb, vb, bad);
         load_keys<FMT, DP, FULL>(a, mem, k);
         Look next = look_up(a, table, t1, t0 + kAttnTile);
 #pragma unroll
@@ -480,7 +482,7 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void
                 }
             }
             // the next keys, in flight under the softmax and the product with V
-            there_next = find_tokens<FMT>(a, mem, next, head, t1, t + kAttnTile, kb, vb, bad);
+            there_next = find_tokens<FMT>(a, mem, next, head, low, t1, t + kAttnTile, kb, vb, bad);
             load_keys<FMT, DP, FULL>(a, mem, k);
             next = look_up(a, table, t1, t + 2 * kAttnTile);
 #pragma unroll
@@ -498,7 +500,7 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const int32_t at = t + 16 * i + 4 * g + r;
-                        const bool ok = ((there >> (16 * i + 4 * g + r)) & 1) && at >= any_lo;
+                        const bool ok = (there >> (16 * i + 4 * g + r)) & 1;
                         keep |= ok ? 1u << (4 * i + r) : 0u;
 #pragma unroll
                         for (int j = 0; j < MT; ++j) {
