@@ -61,8 +61,9 @@ class Decoder:
         return torch.cat((a * c - b * s, b * c + a * s), -1)
 
     def step(self, tokens, lens):
-        """Takes in tokens [n_seq, q_len] behind the `lens` [n_seq] that the cache holds of each sequence;
-        returns the probabilities [n_seq, q_len, vocab] of what follows each."""
+        """Takes in tokens [n_seq, q_len] behind the `lens` [n_seq] that the cache holds of each sequence
+        (on the device: that lens + q_len is within the capacity is for the caller to see to); returns the
+        probabilities [n_seq, q_len, vocab] of what follows each."""
         n_seq, q_len = tokens.shape
         at = lens[:, None] + torch.arange(q_len, device="cuda")
         slots = (self.table.gather(1, at // self.page).long() * self.page + at % self.page).view(-1)
@@ -87,12 +88,23 @@ def pick(p, u):
     return wsl.verify_drafts(p[:, None], None, torch.empty(len(p), 0, dtype=torch.int32, device="cuda"), u[:, None])[1]
 
 
+def most_tokens(length, width, rounds):
+    """The tokens that the caches of a sequence hold at most: its prompt, and all drafts standing in every round."""
+    return length + rounds * (width + 1)
+
+
 def decode(target, drafter, prompt, width, rounds, uniform):
     """Continues prompt [n_seq, length] by `rounds` rounds of `width` drafts; uniform(n, m) gives random
     numbers in [0, 1) on the device.  Returns the tokens that every round added, -1 where there is none,
     and how many drafts stood, [rounds, n_seq, width + 1] and [rounds, n_seq]."""
     n_seq, length = prompt.shape
-    lens = torch.zeros(n_seq, dtype=torch.int64, device="cuda")
+    if width < 0 or rounds < 1:
+        raise ValueError(f"{rounds} rounds of {width} drafts")
+    for model in (target, drafter):     # lengths are on the device from here on: nothing checks them there
+        room = model.table.shape[1] * model.page
+        if most_tokens(length, width, rounds) > room:
+            raise ValueError(f"{length} tokens and {rounds} rounds of {width} drafts do not fit into {room}")
+    lens = torch.zeros(n_seq, dtype=torch.int64, device=prompt.device)
     for i in range(0, length, 64):
         chunk = prompt[:, i:i + 64]
         p = target.step(chunk, lens)
@@ -128,12 +140,14 @@ def main():
     ap.add_argument("--e4m3", action="store_true", help="an 8-bit cache")
     a = ap.parse_args()
     fmt = wsl.WSL_KV_E4M3 if a.e4m3 else wsl.WSL_KV_BF16
-    target = Decoder(a.seqs, a.layers, fmt=fmt)
-    drafter = Decoder(a.seqs, max(1, a.layers // 2), fmt=fmt)       # its weights only in the first layers: some drafts stand
+    length, rounds = 100, -(-a.tokens // (a.width + 1))
+    kw = dict(fmt=fmt, capacity=max(1024, most_tokens(length, a.width, rounds)))
+    target = Decoder(a.seqs, a.layers, **kw)
+    drafter = Decoder(a.seqs, max(1, a.layers // 2), **kw)      # its weights only in the first layers: some drafts stand
     gen = torch.Generator(device="cuda").manual_seed(1)
-    prompt = torch.randint(0, target.vocab, (a.seqs, 100), generator=gen, device="cuda", dtype=torch.int32)
-    for name, model in (("another model", drafter), ("the target itself", Decoder(a.seqs, a.layers, fmt=fmt))):
-        added, stood = decode(target, model, prompt, a.width, -(-a.tokens // (a.width + 1)),
+    prompt = torch.randint(0, target.vocab, (a.seqs, length), generator=gen, device="cuda", dtype=torch.int32)
+    for name, model in (("another model", drafter), ("the target itself", Decoder(a.seqs, a.layers, **kw))):
+        added, stood = decode(target, model, prompt, a.width, rounds,
                               lambda n, m: torch.rand((n, m), generator=gen, device="cuda"))
         print(f"drafts of {name}: {stood.float().mean():.2f} of {a.width} stand; sequence 0 goes on "
               f"{[t for t in added[:, 0].flatten().tolist() if t >= 0][:12]} ..")

@@ -31,3 +31,59 @@ def test_rows_of_their_own_keep_their_step():
     assert wsl._prob_rows(wide[:, :1, :7], "p", CPU, (2, 1, 7)) == 33
     assert wsl._prob_rows(wide[:1, 1:2, :7], "p", CPU, (1, 1, 7)) == 7
     assert wsl._prob_rows(wide[:0], "p", CPU, (0, 3, 11)) == 11
+
+
+def _example():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "speculative_decode.py")
+    spec = importlib.util.spec_from_file_location("speculative_decode", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    return m
+
+
+class _Model:
+    """What decode() asks a model before it runs it; running it is a mistake of its own here."""
+
+    class Ran(Exception):
+        pass
+
+    def __init__(self, pages, page=16):
+        self.table, self.page = torch.zeros((2, pages), dtype=torch.int32), page
+
+    def step(self, tokens, lens):
+        raise self.Ran
+
+
+@pytest.mark.parametrize("pages,fits", [((7, 7), True), ((6, 7), False), ((7, 6), False), ((1, 1), False)])
+def test_the_example_counts_its_tokens_before_it_starts(pages, fits):
+    """70 tokens and 8 rounds of 4 drafts and a token: 110, all of which may stand."""
+    ex = _example()
+    models = [_Model(n) for n in pages]
+    prompt = torch.zeros((2, 70), dtype=torch.int32)
+    with pytest.raises(_Model.Ran if fits else ValueError):
+        ex.decode(*models, prompt, 4, 8, lambda n, m: torch.zeros(n, m))
+
+
+def test_the_example_makes_room_for_what_it_is_asked_for(monkeypatch):
+    ex = _example()
+    made = []
+
+    class Decoder(_Model):
+        vocab = 8000
+
+        def __init__(self, n_seq, layers, capacity=1024, page=16, **kw):
+            super().__init__(-(-capacity // page), page)
+            made.append(self)
+
+    monkeypatch.setattr(ex, "Decoder", Decoder)
+    for name in ("randint", "zeros"):
+        plain = getattr(torch, name)
+        monkeypatch.setattr(ex.torch, name, lambda *a, device=None, plain=plain, **kw: plain(*a, **kw))
+    generator = torch.Generator
+    monkeypatch.setattr(ex.torch, "Generator", lambda device=None: generator())
+    monkeypatch.setattr("sys.argv", ["speculative_decode.py", "--tokens", "5000", "--width", "7"])
+    with pytest.raises(_Model.Ran):         # past the check, into the first step
+        ex.main()
+    assert made and all(m.table.shape[1] * m.page >= 100 + 5000 for m in made)

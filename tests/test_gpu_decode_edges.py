@@ -69,3 +69,18 @@ def test_pages_behind_the_window_may_be_gone(lens, window, page, wide, ql, e4m3)
             check(b)
             assert st.item() == wsl.WSL_STATUS_INDEX, f"sequence {b}"
             c.table[b, at] = was
+
+
+def test_the_example_goes_past_a_thousand_tokens(monkeypatch, capsys):
+    """All drafts of the target itself stand, so its sequences grow to about 100 + 1100 tokens."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "speculative_decode.py")
+    spec = importlib.util.spec_from_file_location("speculative_decode", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    say("example: 1 layer, 2 sequences, 1100 tokens")
+    monkeypatch.setattr("sys.argv", ["speculative_decode.py", "--tokens", "1100", "--width", "10", "--layers", "1",
+                                     "--seqs", "2", "--e4m3"])
+    ex.main()
+    assert "the target itself" in capsys.readouterr().out
