@@ -87,3 +87,20 @@ def test_the_example_makes_room_for_what_it_is_asked_for(monkeypatch):
     with pytest.raises(_Model.Ran):         # past the check, into the first step
         ex.main()
     assert made and all(m.table.shape[1] * m.page >= 100 + 5000 for m in made)
+
+
+def test_the_division_of_the_attention_work(tmp_path):
+    """attn_plan on 64 simulated lanes, unset variables filled with a pattern."""
+    import os
+    import shutil
+    import subprocess
+    here = os.path.dirname(os.path.abspath(__file__))
+    clang = os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "llvm", "bin", "clang++")
+    clang = clang if os.path.exists(clang) else shutil.which("clang++")
+    if clang is None:
+        pytest.skip("clang++ not available")
+    exe = str(tmp_path / "attn_plan")
+    subprocess.run([clang, "-std=c++17", "-O1", "-ftrivial-auto-var-init=pattern", "-isystem", os.path.join(here, "cpp", "wave"),
+                    os.path.join(here, "cpp", "attn_plan_main.cpp"), "-o", exe], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout[-2000:] + r.stderr

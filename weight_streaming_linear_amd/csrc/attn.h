@@ -145,7 +145,9 @@ __device__ __forceinline__ AttnPlan attn_plan(const AttnArgs &a, uint32_t w) {
     const uint32_t heads = static_cast<uint32_t>(a.n_kv), workers = static_cast<uint32_t>(a.workers);
     if (a.whole) {
         p.seq = static_cast<int32_t>(attn_over(w, a.over_heads));
-        p.cost = 0;
+        p.total = a.workers;      // here a unit is a whole item
+        p.each = 1;
+        p.cost = p.lens = 0;
         return p;
     }
     const int lane = static_cast<int>(threadIdx.x & 63);

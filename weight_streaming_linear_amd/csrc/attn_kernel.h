@@ -617,10 +617,10 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void
                 }
             }
         }
-        if (tile == 0) {
+        if (tile == 0 && a.open != nullptr) {
             const uint32_t last = static_cast<uint32_t>(x + left - 1) / static_cast<uint32_t>(plan.each);
             open = {seq, head, static_cast<int32_t>(blockIdx.x), static_cast<int32_t>(last - blockIdx.x) + 1};
-            if (a.open != nullptr && a.by_item && blockIdx.y == 0 && tid == 0) a.open[seq * a.n_kv + head] = open;
+            if (a.by_item && blockIdx.y == 0 && tid == 0) a.open[seq * a.n_kv + head] = open;
         }
         }
         if (x + used < end) __syncthreads();      // LDS is free again
