@@ -71,6 +71,18 @@ int main() {
                     check_shares(lens, n_kv, workers, 5000, 5, window);
                     ++cases;
                 }
+    // the lowest position that is seen, for windows up to the largest number there is
+    for (const int64_t window : {int64_t(1), int64_t(5), int64_t(1) << 31, int64_t(1) << 40, INT64_MAX - 300, INT64_MAX - 1, INT64_MAX})
+        for (int32_t len = 0; len < 600; ++len)
+            for (const int q_len : {1, 2, 5, 256}) {
+                AttnArgs a = args_of({}, 1, 8, 5000, q_len, attn_window(window, 5000));
+                int32_t want = 0;       // the first row that stands at a token at all is at 0 or at len - q_len
+                const int32_t at = len > q_len ? len - q_len : 0;
+                if (window <= at) want = at - static_cast<int32_t>(window) + 1;
+                if (attn_lowest(a, len) != want)
+                    ++fails, std::printf("FAILED: lowest of %d with %d queries, window %lld: %d\n", len, q_len,
+                                         static_cast<long long>(window), attn_lowest(a, len));
+            }
     // whole items: nothing is shared out, but what a worker is told is still defined
     for (const int n : {1, 7, 300})
         for (const int n_kv : {1, 8}) {

@@ -84,3 +84,23 @@ def test_the_example_goes_past_a_thousand_tokens(monkeypatch, capsys):
                                      "--seqs", "2", "--e4m3"])
     ex.main()
     assert "the target itself" in capsys.readouterr().out
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("wide", [0, 100])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 + 7, 2 ** 63 - 1, 2 ** 64 + 3])
+def test_a_window_without_an_end(window, wide, e4m3):
+    """Windows of any size, among them those larger than every position, beside sequences shorter than q_len."""
+    import torch
+    lens = [0, 1, 2, 3, 4, 5, 6, 9, 300]
+    say(f"attn window {window} e4m3={e4m3} wide={wide}")
+    c = CacheCase(90, lens, 2, 64, 16, e4m3, "cuda")
+    c.table = torch.cat((c.table, torch.full((len(lens), wide), -1, dtype=torch.int32, device="cuda")), 1)
+    q = torch.randn((len(lens), 5, 4, 64), device="cuda", generator=torch.Generator("cuda").manual_seed(6)).to(torch.bfloat16)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = wsl.attn_decode(c.cache, q, c.table, c.kv_lens, window=window, status=st)
+    assert st.item() == 0
+    assert torch.equal(got, wsl.attn_decode(c.cache, q, c.table, c.kv_lens))
+    for b, n in enumerate(lens):
+        ref, _, extra = od.attn_ref(f32_of(q)[b], c.values[0][b], c.values[1][b], n, 0.125)
+        assert (np.abs(f32_of(got)[b] - ref) <= od.attn_bound(extra, 64, n, ref, 2.0 ** -8)).all()

@@ -642,7 +642,7 @@ def attn_decode(cache, q, block_table, kv_lens, scale=None, window=0, out=None, 
         ws_bytes = workspace.numel() * workspace.element_size()
     rc = lib().attn_decode(cache.ref, q.data_ptr(), qfmt, n_seq, q_len, n_heads, ld_q, block_table.data_ptr(),
                            block_table.stride(0) if n_seq > 1 else pages, pages, kv_lens.data_ptr(),
-                           dim ** -0.5 if scale is None else float(scale), int(window), out.data_ptr(), ofmt, ld_out,
+                           dim ** -0.5 if scale is None else float(scale), min(int(window), 2 ** 63 - 1), out.data_ptr(), ofmt, ld_out,
                            _ptr(lse), _ptr(workspace), ws_bytes, _ptr(status), _stream(stream))
     if rc:
         _check(rc, "attn_decode")

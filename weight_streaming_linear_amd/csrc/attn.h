@@ -53,8 +53,8 @@ struct AttnArgs {
     uint32_t *status;
     int64_t page_stride, head_stride, token_stride;   // bytes
     int64_t ld_q, ld_out, ld_table;                   // elements
-    int64_t window;
     float scale_log2;
+    int32_t window;       // below capacity: attn_window
     int32_t capacity;     // tokens a table row can name
     int32_t n_seq, q_len, n_kv, group, rows, head_dim, page_size, n_pages;
     int32_t row_tiles, tile_rows, workers, qfmt, ofmt;
@@ -69,10 +69,18 @@ struct AttnSpan {
     bool bad;
 };
 
+// A window as the kernels take it: one that reaches back over all that a table row can name is none (0),
+// so that positions less any other stay in 32 bits.
+inline int32_t attn_window(int64_t window, int64_t capacity) {
+    static_assert(kAttnMaxTokens + 256 <= 0x7fffffff, "a query may stand at up to 256 before the first token");
+    capacity = capacity < kAttnMaxTokens ? capacity : kAttnMaxTokens;
+    return window < capacity ? static_cast<int32_t>(window) : 0;
+}
+
 // The lowest position that some row of a sequence of `len` tokens sees.
 __device__ __forceinline__ int32_t attn_lowest(const AttnArgs &a, int32_t len) {
-    const int64_t lo = static_cast<int64_t>(len) - a.q_len - a.window + 1;
-    return a.window > 0 && lo > 0 ? static_cast<int32_t>(lo) : 0;
+    const int32_t lo = len - a.q_len - a.window + 1;
+    return a.window > 0 && lo > 0 ? lo : 0;
 }
 
 __device__ __forceinline__ AttnSpan attn_span(const AttnArgs &a, int32_t raw) {

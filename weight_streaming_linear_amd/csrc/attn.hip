@@ -140,7 +140,7 @@ int launch_attn(const wsl_kv_cache *c, const void *q, int qfmt, int64_t n_seq, i
     a.q = q, a.out = out, a.lse = lse, a.table = table, a.lens = lens, a.status = status;
     a.page_stride = c->page_stride * elem, a.head_stride = c->head_stride * elem, a.token_stride = c->token_stride * elem;
     a.ld_q = ld_q, a.ld_out = ld_out, a.ld_table = ld_table;
-    a.window = window;
+    a.window = attn_window(window, capacity);
     a.capacity = static_cast<int32_t>(capacity < kAttnMaxTokens ? capacity : kAttnMaxTokens);
     a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.44269504088896340736);
     a.n_seq = static_cast<int32_t>(n_seq), a.q_len = static_cast<int32_t>(q_len), a.n_kv = static_cast<int32_t>(c->n_kv);

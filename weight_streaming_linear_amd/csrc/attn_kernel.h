@@ -407,7 +407,7 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void
         }
         // positions that every row sees: [all_lo, all_hi]; that some row sees: from low on
         const int32_t all_hi = len - a.q_len;
-        const int64_t all_lo = a.window > 0 ? static_cast<int64_t>(len) - a.window : 0;
+        const int32_t all_lo = a.window > 0 ? len - a.window : 0;
         const int32_t low = attn_lowest(a, len);
 
 #pragma unroll
