@@ -104,3 +104,32 @@ def test_a_window_without_an_end(window, wide, e4m3):
     for b, n in enumerate(lens):
         ref, _, extra = od.attn_ref(f32_of(q)[b], c.values[0][b], c.values[1][b], n, 0.125)
         assert (np.abs(f32_of(got)[b] - ref) <= od.attn_bound(extra, 64, n, ref, 2.0 ** -8)).all()
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("odd", [float("nan"), float("inf"), 1.0])
+@pytest.mark.parametrize("wide", [0, 100])
+def test_rows_whose_scores_are_all_minus_infinity_are_zero(f32, odd, wide):
+    """Whatever the values are that they weigh with zero; other sequences beside them as ever."""
+    import torch
+    lens = [40, 700, 129]
+    say(f"attn scores of -inf f32={f32} values {odd} wide={wide}")
+
+    def kfill(b, x):
+        if b < 2:
+            x[:, :, 0] = -np.inf
+
+    def vfill(b, x):
+        if b < 2:
+            x[:, :, 3] = odd
+
+    c = CacheCase(95, lens, 2, 64, 16, False, "cuda", k_fill=kfill, v_fill=vfill)
+    c.table = torch.cat((c.table, torch.full((len(lens), wide), -1, dtype=torch.int32, device="cuda")), 1)
+    q = torch.randn((3, 2, 4, 64), device="cuda", generator=torch.Generator("cuda").manual_seed(7))
+    q[..., 0] = q[..., 0].abs() + 0.5
+    q = q if f32 else q.to(torch.bfloat16)
+    lse = torch.zeros(q.shape[:3], device="cuda")
+    out = wsl.attn_decode(c.cache, q, c.table, c.kv_lens, lse=lse)
+    assert (out[:2] == 0).all() and torch.isneginf(lse[:2]).all()
+    ref, rl, extra = od.attn_ref(f32_of(q)[2], c.values[0][2], c.values[1][2], 129, 0.125)
+    assert (np.abs(f32_of(out)[2] - ref) <= od.attn_bound(extra, 64, 129, ref, 2.0 ** (-24 if f32 else -8))).all()

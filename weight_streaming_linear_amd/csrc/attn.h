@@ -206,13 +206,14 @@ __device__ __forceinline__ void attn_store(const AttnArgs &a, int64_t at, f32x4 
 
 // Elements d .. d + 3 of row `row` (query position row / group, head h * group + row % group) of a
 // sequence are done: o and l are its sums, m the maximum they are relative to.  l is zero where
-// nothing was seen, and at least one otherwise (the maximum's own term).
+// nothing was seen but scores of -infinity (and o may be NaN: zero times a value that is not finite), and
+// at least one otherwise (the maximum's own term).
 __device__ __forceinline__ void attn_finish(const AttnArgs &a, int32_t seq, int32_t h, int32_t row, int32_t d, f32x4 o,
                                             float m, float l) {
     const int32_t i = static_cast<int32_t>(attn_over(static_cast<uint32_t>(row), a.over_group)), head = h * a.group + row - i * a.group;
     const int64_t tok = static_cast<int64_t>(seq) * a.q_len + i;
-    const float r = l == 0.f ? 0.f : 1.f / l;
-    attn_store(a, tok * a.ld_out + static_cast<int64_t>(head) * a.head_dim + d, o * r);
+    const f32x4 none = {0, 0, 0, 0};
+    attn_store(a, tok * a.ld_out + static_cast<int64_t>(head) * a.head_dim + d, l == 0.f ? none : o * (1.f / l));
     if (a.lse != nullptr && d == 0)
         a.lse[tok * (a.n_kv * a.group) + head] =
             l == 0.f ? -__builtin_huge_valf() : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994530942f;
