@@ -9,8 +9,10 @@ TEST INFRASTRUCTURE ONLY (see ``oracle/__init__.py``).
 * Attention: softmax over the tokens a query sees, computed from the definition per row.
 * Verification: the definition, draft by draft and entry by entry.
 
-Tolerances (``attn_bound``) count the roundings that the documented computation makes; none
-is fitted to a result.
+Tolerances (``attn_bound``) count the roundings that the documented computation makes at most,
+over all its variants (the weights' 16 bits beside bf16 queries among them); none is fitted to a
+result.  Whether a variant has more bits than that shows on inputs where nearly nothing else rounds
+(tests/precision_cases.py).
 """
 
 import numpy as np
@@ -99,7 +101,7 @@ def attn_ref(q, k, v, length, scale, window=0):
 
 
 def attn_bound(extra, dim, tokens, ref, half_step):
-    """|out - ref| allowed for the documented computation: products accumulated in binary32 over
+    """|out - ref| allowed for the documented computation, whatever the queries' type: products accumulated in binary32 over
     dim terms (queries in 24 bits), one multiplication by the scale, an exponential good to
     2^-22, weights in 16 bits, a sum over `tokens` terms in binary32 with at most one rescale per
     32 of them, one division, and the result's own rounding."""

@@ -133,3 +133,62 @@ def test_rows_whose_scores_are_all_minus_infinity_are_zero(f32, odd, wide):
     assert (out[:2] == 0).all() and torch.isneginf(lse[:2]).all()
     ref, rl, extra = od.attn_ref(f32_of(q)[2], c.values[0][2], c.values[1][2], 129, 0.125)
     assert (np.abs(f32_of(out)[2] - ref) <= od.attn_bound(extra, 64, 129, ref, 2.0 ** (-24 if f32 else -8))).all()
+
+
+def _dyadic_cache(k, v, dim, e4m3):
+    """A cache of one page that holds rows k, v (padded to dim) exactly."""
+    import torch
+    pad = [np.zeros((16, dim), np.float32) for _ in range(2)]
+    for to, x in zip(pad, (k, v)):
+        to[:len(x), :x.shape[1]] = x
+    rows = [torch.from_numpy(x).cuda()[:, None] for x in pad]
+    cache = wsl.KVCache.empty(1, 1, 16, dim, wsl.WSL_KV_E4M3 if e4m3 else wsl.WSL_KV_BF16)
+    slots = torch.arange(16, device="cuda")
+    wsl.kv_cache_write(cache, *rows, slots)
+    back = wsl.kv_cache_read(cache, slots, ofmt=wsl.WSL_OUT_F32)
+    assert all(torch.equal(a, b) for a, b in zip(rows, back))
+    return cache
+
+
+def _check_weights_bits(f32, dim, rows, wide, e4m3):
+    import torch
+    import precision_cases as pc
+    say(f"attn weights' bits f32={f32} dim={dim} rows={rows} wide={wide} e4m3={e4m3}")
+    q, k, v = pc.weight_case(dim + rows, rows, f32)
+    cache = _dyadic_cache(k, v, dim, e4m3)
+    qt = torch.zeros((1, 1, rows, dim), device="cuda")
+    qt[0, 0, :, :pc.DIM] = torch.from_numpy(q)
+    out = wsl.attn_decode(cache, qt if f32 else qt.to(torch.bfloat16), torch.zeros((1, wide), dtype=torch.int32, device="cuda"),
+                          torch.tensor([pc.TOKENS], dtype=torch.int32, device="cuda"), scale=0.5, ofmt=wsl.WSL_OUT_F32)
+    ref, _, _ = od.attn_ref(q[None], k[:, None], v[:, None], pc.TOKENS, 0.5)
+    got = f32_of(out)[0, 0]
+    assert (got[:, pc.DIM:] == 0).all()
+    err, bound = np.abs(got[:, :pc.DIM] - ref[0]), pc.weight_bound(q, k, 0.5, ref[0])
+    assert (err <= bound).all(), f"{(err[bound > 0] / bound[bound > 0]).max()} of the bound"
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("dim", [32, 64, 128, 192, 256])
+@pytest.mark.parametrize("rows", [5, 64])
+@pytest.mark.parametrize("wide", [1, 4200])
+def test_results_of_fp32_queries_have_the_weights_bits(dim, rows, wide, e4m3):
+    _check_weights_bits(True, dim, rows, wide, e4m3)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("dim", [32, 64, 128, 192, 256])
+@pytest.mark.parametrize("rows", [5, 64])
+def test_fp32_queries_keep_their_bits(dim, rows, e4m3):
+    import torch
+    import precision_cases as pc
+    say(f"attn queries' bits dim={dim} rows={rows} e4m3={e4m3}")
+    q, k = pc.query_case(dim + rows, rows)
+    cache = _dyadic_cache(k, k, dim, e4m3)
+    qt = torch.zeros((1, 1, rows, dim), device="cuda")
+    qt[0, 0, :, :pc.DIM] = torch.from_numpy(q)
+    lse = torch.zeros((1, 1, rows), device="cuda")
+    wsl.attn_decode(cache, qt, torch.zeros((1, 1), dtype=torch.int32, device="cuda"),
+                    torch.ones(1, dtype=torch.int32, device="cuda"), scale=0.7, lse=lse)
+    _, ref, _ = od.attn_ref(q[None], k[:, None], k[:, None], 1, np.float64(np.float32(0.7)))
+    err, bound = np.abs(f32_of(lse)[0, 0] - ref[0]), pc.query_bound(ref[0])
+    assert (err <= bound).all(), f"{(err / bound).max()} of the bound"
