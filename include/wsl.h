@@ -436,8 +436,8 @@ int kv_cache_read(const wsl_kv_cache *h_cache, const int64_t *d_slots, int64_t c
  *            a workspace must not overlap.
  * d_status   device uint32 or NULL: WSL_STATUS_INDEX as above.
  * Scores, maxima, sums and products with V are held in fp32.  The matrix instructions take bf16:
- * the weights enter them as two bf16 numbers (16 bits) beside bf16 queries; fp32 queries and the
- * weights beside them as three (24 bits).  Deterministic.
+ * fp32 queries enter them as three bf16 numbers (24 bits), and so do the weights, but as two (16
+ * bits) where queries and result are both bf16.  Deterministic.
  */
 size_t attn_decode_workspace_bytes(int qfmt, int64_t n_seq, int64_t q_len, int64_t n_heads, int64_t n_kv,
                                    int64_t head_dim, int64_t pages_per_seq, int64_t page_size);

@@ -178,6 +178,14 @@ def test_results_of_fp32_queries_have_the_weights_bits(dim, rows, wide, e4m3):
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("dim", [32, 64, 128, 192, 256])
 @pytest.mark.parametrize("rows", [5, 64])
+@pytest.mark.parametrize("wide", [1, 4200])
+def test_fp32_results_of_bf16_queries_have_the_weights_bits(dim, rows, wide, e4m3):
+    _check_weights_bits(False, dim, rows, wide, e4m3)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("dim", [32, 64, 128, 192, 256])
+@pytest.mark.parametrize("rows", [5, 64])
 def test_fp32_queries_keep_their_bits(dim, rows, e4m3):
     import torch
     import precision_cases as pc

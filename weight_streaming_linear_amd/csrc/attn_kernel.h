@@ -334,9 +334,11 @@ constexpr int attn_waves() {
 // the matrix instruction's 8 reduction slots of a lane group are taken to be those 8 keys: the
 // order of the reduction is free as long as V's lanes use the same.  The rows' maxima and sums
 // then sit in the lanes that hold the rows' outputs.
-// P enters the matrix instruction as the sum of two bf16 numbers (16 bits) beside bf16 queries, where
-// one alone would add an error as large as a bf16 result's own rounding, and of three (24 bits)
-// beside fp32 queries.
+// P enters the matrix instruction as the sum of PT bf16 numbers: of three (24 bits), or of two (16 bits)
+// where queries and result are both bf16, whose own rounding is 2^8 times as large (one number alone would
+// add an error of its size).  (Three there too: 16 sequences of up to 4224 tokens with five queries 28.1 us
+// against 27.6, 32 of up to 8192 in e4m3 42.1 against 41.9, and as many results, one or two in 1000, fall
+// to the other side of a rounding as with two: sums in another order do that.)
 // Each wave works on 32 tokens of its own in a round, and the four join at an item's end.  In a
 // round it asks for this round's values, then works on the keys that it asked for a round before,
 // asks for the next round's keys and the table's entries for the round after that.
@@ -346,9 +348,9 @@ constexpr int attn_waves() {
 // Bound: the cached keys and values, read once.  8 sequences of 32768 tokens, 8 kv heads of 128, bf16
 // (1.07 GB): 160 us, 6.7 TB/s, against 7.3 of a plain read.  Short calls are a chain of five trips to
 // memory (lengths, table, keys, values, result): 7 us for one sequence of 37 tokens.
-template <int FMT, int DP, int MT, int QT, bool FULL>
+template <int FMT, int DP, int MT, int QT, int PT, bool FULL>
 __global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void attn_kernel(AttnArgs a) {
-    constexpr int kPad = DP + 4, PT = QT == 1 ? 2 : 3;
+    constexpr int kPad = DP + 4;
     __shared__ float lds_o[kAttnWaves][16 * MT][kPad];
     __shared__ float lds_m[kAttnWaves][16 * MT], lds_l[kAttnWaves][16 * MT];
     __shared__ WaveLds lds_w[kAttnWaves];
@@ -645,7 +647,7 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void
 // many as the registers allow (one: 32 ragged sequences 45.3 against 42.4).
 // Those of one token range lie `workers` apart, a multiple of 8 where it can be, so that they run at the
 // same time on the same XCD and what one reads the others find in its L2.
-template <int FMT, int DP, int MT, int QT>
+template <int FMT, int DP, int MT, int QT, int PT>
 void go(AttnArgs &a, hipStream_t s) {
     const int fit = kAttnCus * (FMT == WSL_KV_BF16 ? 1 : attn_waves<FMT, DP, MT, QT>());
     static_assert(attn_waves<FMT, DP, MT, QT>() <= kAttnMaxWaves, "workspaces are for so many");
@@ -653,19 +655,21 @@ void go(AttnArgs &a, hipStream_t s) {
     if (a.whole) a.workers = a.n_seq * a.n_kv;
     else a.workers = a.workers < most ? a.workers : most;
     const dim3 grid(static_cast<unsigned>(a.workers), static_cast<unsigned>(a.row_tiles));
-    if (a.head_dim == DP) hipLaunchKernelGGL((attn_kernel<FMT, DP, MT, QT, true>), grid, dim3(kAttnThreads), 0, s, a);
-    else hipLaunchKernelGGL((attn_kernel<FMT, DP, MT, QT, false>), grid, dim3(kAttnThreads), 0, s, a);
+    if (a.head_dim == DP) hipLaunchKernelGGL((attn_kernel<FMT, DP, MT, QT, PT, true>), grid, dim3(kAttnThreads), 0, s, a);
+    else hipLaunchKernelGGL((attn_kernel<FMT, DP, MT, QT, PT, false>), grid, dim3(kAttnThreads), 0, s, a);
 }
 
 template <int FMT, int DP>
 void go_rows(AttnArgs &a, int mt, hipStream_t s) {
     if (a.qfmt != WSL_OUT_BF16) {
-        if (mt == 1) go<FMT, DP, 1, 3>(a, s);
-        else if constexpr (attn_two_blocks(FMT, WSL_OUT_F32, DP)) go<FMT, DP, 2, 3>(a, s);
+        if (mt == 1) go<FMT, DP, 1, 3, 3>(a, s);
+        else if constexpr (attn_two_blocks(FMT, WSL_OUT_F32, DP)) go<FMT, DP, 2, 3, 3>(a, s);
         return;
     }
-    if (mt == 1) go<FMT, DP, 1, 1>(a, s);
-    else if constexpr (attn_two_blocks(FMT, WSL_OUT_BF16, DP)) go<FMT, DP, 2, 1>(a, s);
+    const bool exact = a.ofmt != WSL_OUT_BF16;
+    if (mt == 1) exact ? go<FMT, DP, 1, 1, 3>(a, s) : go<FMT, DP, 1, 1, 2>(a, s);
+    else if constexpr (attn_two_blocks(FMT, WSL_OUT_BF16, DP))
+        exact ? go<FMT, DP, 2, 1, 3>(a, s) : go<FMT, DP, 2, 1, 2>(a, s);
 }
 
 }  // namespace
