@@ -200,3 +200,54 @@ def test_fp32_queries_keep_their_bits(dim, rows, e4m3):
     _, ref, _ = od.attn_ref(q[None], k[:, None], k[:, None], 1, np.float64(np.float32(0.7)))
     err, bound = np.abs(f32_of(lse)[0, 0] - ref[0]), pc.query_bound(ref[0])
     assert (err <= bound).all(), f"{(err / bound).max()} of the bound"
+
+
+def _items_in_parts(lens, n_kv, workers, cost=2, tile=128):
+    """How many (sequence, kv head) items lie in the shares of two workers or more, by the arithmetic of the
+    split: an item is its tiles and `cost` units for its beginning, all items in a row are cut into equal shares."""
+    units = [max(1, -(-n // tile)) + cost for n in lens for _ in range(n_kv)]
+    each = -(-sum(units) // workers)
+    at, parts = 0, 0
+    for n in units:
+        parts += (at + cost) // each != (at + n - 1) // each     # (a share that ends in the beginning holds no part)
+        at += n
+    return parts
+
+
+def _some(n, *lens):
+    return [int(x) for x in np.random.default_rng([2026, 15, n]).choice(lens, n)]
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("lens,heads,n_kv,dim,ql", [
+    (_some(786, 140, 700, 1100), 2, 1, 16, 1),      # one row tile: more items than the most workgroups (768)
+    (_some(260, 300, 1300, 0, 77), 6, 3, 32, 1),
+    (_some(80, 900, 130, 2000, 1), 128, 1, 16, 3),  # 384 rows: several row tiles, fewer workgroups for each
+    (_some(90, 1500, 40, 700), 40, 2, 128, 8)])
+def test_parts_of_more_items_than_workgroups(lens, heads, n_kv, dim, ql, e4m3):
+    """What is to be joined is then kept by worker, not by item."""
+    import torch
+    row_tiles = -(-heads // n_kv * ql // 32)        # at least
+    most = max(8, 768 // row_tiles)
+    assert len(lens) > 64 and len(lens) * n_kv > most
+    assert all(_items_in_parts(lens, n_kv, w) > 0 for w in range(8, most + 1, 8))
+    say(f"attn {len(lens) * n_kv} items heads={heads}/{n_kv} dim={dim} q_len={ql} e4m3={e4m3}")
+    c = CacheCase(100 + dim, lens, n_kv, dim, 16, e4m3, "cuda")
+    c.table = torch.cat((c.table, torch.full((len(lens), 100), -1, dtype=torch.int32, device="cuda")), 1)
+    q = torch.randn((len(lens), ql, heads, dim), device="cuda", generator=torch.Generator("cuda").manual_seed(8)).to(torch.bfloat16)
+    n = wsl.attn_decode_workspace_bytes(1, len(lens), ql, heads, n_kv, dim, c.table.shape[1], 16)
+    assert n > 0
+    ws = torch.full((n // 4,), float("nan"), device="cuda")
+    lse, st = torch.full(q.shape[:3], float("nan"), device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    first = wsl.attn_decode(c.cache, q, c.table, c.kv_lens, lse=lse, workspace=ws, status=st)
+    assert torch.equal(first, wsl.attn_decode(c.cache, q, c.table, c.kv_lens, workspace=ws)) and st.item() == 0
+    got, glse, q64 = f32_of(first), f32_of(lse), f32_of(q)
+    for b, length in enumerate(lens):
+        if b % 3 and b > 40 and b < len(lens) - 20:         # (the reference takes the time here)
+            continue
+        ref, rl, extra = od.attn_ref(q64[b], c.values[0][b], c.values[1][b], length, dim ** -0.5)
+        assert (np.abs(got[b] - ref) <= od.attn_bound(extra, dim, length, ref, 2.0 ** -8)).all(), f"sequence {b}"
+        assert np.array_equal(np.isneginf(glse[b]), np.isneginf(rl))
+        some = np.isfinite(rl)
+        bound = od.lse_bound(extra, dim, length, rl) + 1e-6
+        assert (np.abs(glse[b][some] - rl[some]) <= bound[some]).all(), f"lse of sequence {b}"
