@@ -104,3 +104,19 @@ def test_the_division_of_the_attention_work(tmp_path):
                     os.path.join(here, "cpp", "attn_plan_main.cpp"), "-o", exe], check=True)
     r = subprocess.run([exe], capture_output=True, text=True)
     assert r.returncode == 0, r.stdout[-2000:] + r.stderr
+
+
+def test_contiguous_tensors_still_need_a_unit_last_step():
+    """As from the first: a contiguous tensor whose last dimension has one entry and another step is refused."""
+    from types import SimpleNamespace
+
+    def like(t):
+        return SimpleNamespace(is_cuda=True, dtype=t.dtype, device=t.device, dim=t.dim, numel=t.numel, stride=t.stride,
+                               is_contiguous=t.is_contiguous)
+
+    odd = torch.zeros(64).as_strided((5, 1), (1, 7))
+    assert odd.is_contiguous()
+    for contiguous in (False, True):
+        with pytest.raises(ValueError, match="last dimension"):
+            wsl._require(like(odd), "y", (torch.float32,), contiguous=contiguous)
+        wsl._require(like(torch.zeros(5, 1)), "y", (torch.float32,), contiguous=contiguous)

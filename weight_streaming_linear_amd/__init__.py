@@ -149,10 +149,9 @@ def _require(t, name, dtypes, device=None, contiguous=False, ndim=None):
         raise ValueError(f"{name}: on {t.device}, expected {device}")
     if ndim is not None and t.dim() != ndim:
         raise ValueError(f"{name}: expected {ndim} dimensions, got shape {tuple(t.shape)}")
-    if contiguous:
-        if not t.is_contiguous():
-            raise ValueError(f"{name}: must be contiguous")
-    elif t.dim() > 0 and t.numel() > 1 and t.stride(-1) != 1:
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    if t.dim() > 0 and t.numel() > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name}: last dimension must have stride 1 (got strides {t.stride()})")
 
 
