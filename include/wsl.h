@@ -437,7 +437,8 @@ int kv_cache_read(const wsl_kv_cache *h_cache, const int64_t *d_slots, int64_t c
  * d_status   device uint32 or NULL: WSL_STATUS_INDEX as above.
  * Scores, maxima, sums and products with V are held in fp32.  The matrix instructions take bf16:
  * fp32 queries enter them as three bf16 numbers (24 bits), and so do the weights, but as two (16
- * bits) where queries and result are both bf16.  Deterministic.
+ * bits) where queries and result are both bf16.  The sums over V are divided last: they overflow
+ * where sum_t exp(s_t - max s) |V_t| reaches 2^128.  Deterministic.
  */
 size_t attn_decode_workspace_bytes(int qfmt, int64_t n_seq, int64_t q_len, int64_t n_heads, int64_t n_kv,
                                    int64_t head_dim, int64_t pages_per_seq, int64_t page_size);

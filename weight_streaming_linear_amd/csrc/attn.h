@@ -98,10 +98,14 @@ __device__ __forceinline__ AttnSpan attn_span(const AttnArgs &a, int32_t raw) {
 // for its beginning and end, which a worker spends about as long on as on so many tiles.  Worker w
 // takes `each` successive units from w * each on, with the least `each` for which the workers suffice.
 // Where equal shares of tiles alone end with the items, or are a tile or two, there is nothing to weigh
-// up (cost 0).  (16 sequences of up to 4224 tokens with five queries 32.2 us at cost 0, 31.5, 30.5, 30.9,
-// 30.9 and 31.8 at 1, 2, 3, 4 and 6; 32 of up to 8192 in e4m3 44.9, 44.5, 43.3, 44.0, 44.5 and 45.7.)
+// up (cost 0).  (16 sequences of up to 4224 tokens with five queries 29.6 us at cost 0, 29.1, 27.6, 27.5,
+// 28.1 and 28.8 at 1, 2, 3, 4 and 6, in e4m3 27.9, 27.0, 25.5, 25.4, 25.2 and 26.1; 32 of up to 8192 76.2,
+// 73.4, 73.8, 75.3, 76.3 and 77.3, in e4m3 43.0, 42.7, 42.3, 42.9, 43.2 and 44.7.)
 // A few long items are not cut finer than two tiles where that leaves a worker for most compute units:
-// half as many parts are to be joined (one sequence of 8192 tokens, 8 kv heads: 16.1 -> 15.2 us).
+// half as many parts are to be joined.  That is so over e4m3 alone: over bf16 there are as many workers as
+// compute units, and such items have two tiles each anyway.  (One sequence of 8192 tokens, 8 kv heads, in
+// e4m3 14.0 -> 12.4 us, two of 4096 13.1 -> 12.5, one of 12000 with heads of 64 13.9 -> 13.1, of 6000 13.5 ->
+// 13.9.)
 // The lengths are on the device, so every wave works this out for itself: without LDS or barriers,
 // each lane adds up the units of `per` successive sequences, a scan over the lanes finds the lane whose
 // sequences hold the wanted unit, and its sequences are divided among the lanes again until one is left.

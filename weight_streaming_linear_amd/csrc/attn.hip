@@ -71,9 +71,10 @@ __global__ __launch_bounds__(kJoinMany) void attn_join_kernel(AttnArgs a) {
 }
 
 // Short sequences are not split, which saves the joining launch: a workgroup takes an item from end to
-// end.  (One sequence of 512 tokens, 40 heads on 8 of 128: 9.7 us against 12.9, 16 of up to 512 11.2
-// against 12.8, 64 of them 16.6 against 22; of 1024 tokens 14.1 against 12.8, 17.2 against 14.2 and, with
-// enough items to fill the chip, 26.8 against 29.6.)
+// end.  (One sequence of 512 tokens, 40 heads on 8 of 128: 8.9 us against 12.5, 16 of up to 512 9.6
+// against 13.0, 64 of them 16.0 against 22.0; of 1024 tokens 13.1 against 12.7, 15.1 against 14.5 and, with
+// enough items to fill the chip, 25.8 against 27.5.  What a table has room for decides, not the lengths: one
+// of 512 in a table for 8192 takes 12.7.)
 bool attn_whole(int64_t tiles, int64_t items) {
     return tiles <= (items >= 2 * kAttnCus ? 8 : 4) && items <= (1 << 23);      // (a grid's limit)
 }
@@ -86,11 +87,13 @@ struct AttnShape {
 
 // Two blocks of 16 rows for a workgroup, or one; more rows are as many workgroups over the same tokens.
 // Two where the registers allow beside the head's width (24 rows of 192, 89 sequences of up to 1839
-// tokens, bf16: 59 us against 75 with one, over e4m3 26.0 against 25.8; at 256, with spilled registers,
-// 41.7 against 36.3; fp32 queries, 25 rows of 128, 16 sequences of up to 4224 tokens: 33.6 against 39.2,
-// over e4m3 33.8 against 29.0, at 64 24.9 against 25.4) and there is enough to do for all compute units
-// (25 rows of 128, one sequence of 300 tokens 11.2 against 8.8, of 4000 14.8 against 13.8, of 8192 18.2
-// against 20.0; 16 of up to 500 13.5 against 10.8, 32 of them 13.2 against 17.1).
+// tokens, bf16: 104 us against 138 with one; 25 rows of 128, 16 of up to 4224: 27.6 against 32.6, over e4m3
+// 25.3 against 26.4, with fp32 queries 30.8 against 34.1, over e4m3 31.1 against 28.2).  Left at one where
+// two won in some shapes and lost in others: 192 over e4m3 88 against 96 and 26.0 against 25.8; 256 over
+// bf16, with spilled registers, 63.6 against 66.5 and 41.7 against 36.3; fp32 queries of 64 22.0 against
+// 24.0 and 24.9 against 25.4.  And where there is enough to do for all compute units (25 rows of 128, one
+// sequence of 300 tokens 10.8 against 8.2, of 4000 14.7 against 13.6, of 8192 16.9 against 16.7; 16 of up to
+// 500 12.4 against 10.1, 32 of them 13.0 against 17.1, 64 19.2 against 25.7).
 int blocks_of(int fmt, int qfmt, int64_t rows, int64_t head_dim, bool whole, int64_t shares) {
     if (rows <= 16 || shares <= (whole ? 1 : 2) * kAttnCus / ((rows + 15) / 16)) return 1;
     return attn_two_blocks(fmt, qfmt, head_dim) ? 2 : 1;
@@ -161,9 +164,9 @@ int launch_attn(const wsl_kv_cache *c, const void *q, int qfmt, int64_t n_seq, i
     else launch_attn_fmt<WSL_KV_E4M3>(a, sh.mt, s);
     if (!sh.whole) {
         // A few long sequences leave items in many parts, many sequences leave many items in two or
-        // three.  (One sequence of 8192 tokens, 8 heads of 64 parts: 18.5 us a call with few threads,
-        // 16.1 with many; 16 sequences with five queries: 6.2 us for this kernel with few, 13.5 with
-        // many.)
+        // three.  (One sequence of 8192 tokens, 8 heads of 32 parts: 15.3 us a call with few threads,
+        // 14.6 with many, in e4m3 12.9 and 12.4; 16 of up to 4224 with five queries 27.6 with few, 30.0
+        // with many, in e4m3 25.5 and 28.8; 32 of up to 8192 in e4m3 42.2 and 44.0.)
         const int threads = a.workers >= 16 * n_seq * c->n_kv ? kJoinMany : kJoinFew;
         hipLaunchKernelGGL(attn_join_kernel,
                            dim3(static_cast<unsigned>(a.by_item ? n_seq * c->n_kv : a.workers),

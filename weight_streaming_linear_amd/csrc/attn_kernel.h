@@ -122,8 +122,8 @@ __device__ __forceinline__ void load_keys(const AttnArgs &a, const WaveLds &w, K
 // S^T leaves in this lane) and, of each, the kVec elements that start at (l % 16) * kVec: whole
 // rows are read in order, and the 8 x kVec block is transposed inside the lane.  They are streamed: a
 // line of values is read by one instruction once, where one of keys is read by two.  (Keys and values
-// streamed alike, or neither: 44, 42 against 39 us for 16 sequences of up to 4224 tokens with five
-// queries, 48, 52 against 47 us for 32 of up to 8192 in e4m3.)
+// streamed alike, or neither: 30.4, 29.2 against 27.6 us for 16 sequences of up to 4224 tokens with five
+// queries, 43.6, 48.9 against 42.2 for 32 of up to 8192 in e4m3, 160, 185 against 164 for 8 of 32768.)
 template <int FMT, int DP, bool FULL>
 __device__ __forceinline__ void load_values(const AttnArgs &a, const WaveLds &w, Values<FMT, DP> &v) {
     typedef Values<FMT, DP> V;
@@ -317,9 +317,9 @@ __device__ __forceinline__ void again(const int32_t *table, int32_t seq, int32_t
 // Waves of a SIMD that the registers are shared among (a workgroup is one wave on each): as many as do
 // without scratch memory.  What is in flight has to cover the memory's latency, and a wave has a round's
 // keys and values under way; more waves with spilled registers lost (8 sequences of 8192 tokens in e4m3,
-// heads of 256, fp32 queries: 106 us with two, 73 with one; 16 of up to 4224 with 25 rows of 64 21.5 with
+// heads of 256, fp32 queries: 92 us with two, 52 with one; 16 of up to 4224 with 25 rows of 64 20.4 with
 // three, 20.2 with two), and more without did not help (three instead of two in e4m3 at 128: 32 ragged
-// sequences 44.7 against 42.4).
+// sequences 44.9 against 42.2).
 template <int FMT, int DP, int MT, int QT>
 constexpr int attn_waves() {
     if (DP > 128) return FMT == WSL_KV_BF16 || (DP > 192 && QT == 3) ? 1 : 2;
@@ -346,8 +346,8 @@ constexpr int attn_waves() {
 // them the compiler waits for all.  So a wave without tokens, and the keys after a range's last round, are
 // a row of the cache that nobody uses.
 // Bound: the cached keys and values, read once.  8 sequences of 32768 tokens, 8 kv heads of 128, bf16
-// (1.07 GB): 160 us, 6.7 TB/s, against 7.3 of a plain read.  Short calls are a chain of five trips to
-// memory (lengths, table, keys, values, result): 7 us for one sequence of 37 tokens.
+// (1.07 GB): 159 us, 6.7 TB/s, against 7.3 of a plain read.  Short calls are a chain of five trips to
+// memory (lengths, table, keys, values, result): 6.3 us for one sequence of 37 tokens.
 template <int FMT, int DP, int MT, int QT, int PT, bool FULL>
 __global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void attn_kernel(AttnArgs a) {
     constexpr int kPad = DP + 4;
@@ -642,9 +642,12 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<FMT, DP, MT, QT>())) void
 
 // There is a workgroup for each whole item and row tile; or else, over bf16, one for each compute unit:
 // its four waves' rounds of 16 KB keep the memory busy, and fewer shares have fewer beginnings, ends and
-// parts (two on each: 16 sequences of up to 4224 tokens with five queries 30.1 us against 27.7, 64 of up to
-// 2048 47.9 against 44.5, 8 of 32768 164.9 against 163.9); over e4m3, whose rounds are half as long, as
-// many as the registers allow (one: 32 ragged sequences 45.3 against 42.4).
+// parts (two on each: 16 sequences of up to 4224 tokens with five queries 30.1 us against 27.6, 64 of up to
+// 2048 48.1 against 44.5, 8 of 32768 164.7 against 163.9); over e4m3, whose rounds are half as long, as
+// many as the registers allow.  There many short sequences and fp32 queries gain (two against one: 64 of up
+// to 2048 28.7 against 30.1, the 16 with five queries 25.3 against 25.7, 32 of up to 8192 with fp32 queries
+// 44.6 against 45.3) and few long ones lose (4 of 8192 20.4 against 18.7, 8 of up to 16384 26.5 against 24.9,
+// 32 of up to 8192 42.2 against 41.8).
 // Those of one token range lie `workers` apart, a multiple of 8 where it can be, so that they run at the
 // same time on the same XCD and what one reads the others find in its L2.
 template <int FMT, int DP, int MT, int QT, int PT>

@@ -19,7 +19,7 @@
 // rows at once and one launch does all of it.  Beyond, one launch sums the segments, so that
 // one sequence alone spreads over the chip, and a second, one wave a sequence, finds the segment that
 // holds the target sum and looks through that one.  (fp32, 64 sequences of 8 drafts over 151937 entries:
-// 13.0 us, 6.0 TB/s, and 4.5; one of 4 over 32000 in one launch: 5.8 us.)
+// 14.5 us, 5.4 TB/s, and 4.6; one of 4 over 32000 in one launch: 5.8 us.)
 #include "device_common.h"
 
 namespace wsl {
