@@ -251,3 +251,21 @@ def test_parts_of_more_items_than_workgroups(lens, heads, n_kv, dim, ql, e4m3):
         some = np.isfinite(rl)
         bound = od.lse_bound(extra, dim, length, rl) + 1e-6
         assert (np.abs(glse[b][some] - rl[some]) <= bound[some]).all(), f"lse of sequence {b}"
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("window", [0, 300, 2 ** 31 - 600])
+def test_a_table_with_room_for_more_than_2_to_the_31_tokens(window, e4m3):
+    import torch
+    page, pages, lens = 1 << 16, 1 << 16, [70000, 5, 0]
+    say(f"attn room for 2^32 tokens, window {window}, e4m3={e4m3}")
+    c = CacheCase(97, lens, 1, 16, page, e4m3, "cuda", spare=0)
+    table = torch.full((len(lens), pages), -1, dtype=torch.int32, device="cuda")
+    table[:, :c.table.shape[1]] = c.table
+    q = torch.randn((len(lens), 2, 2, 16), device="cuda", generator=torch.Generator("cuda").manual_seed(9))
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = f32_of(wsl.attn_decode(c.cache, q, table, c.kv_lens, window=window, status=st))
+    assert st.item() == 0
+    for b, n in enumerate(lens):
+        ref, _, extra = od.attn_ref(f32_of(q)[b], c.values[0][b], c.values[1][b], n, 0.25, window)
+        assert (np.abs(got[b] - ref) <= od.attn_bound(extra, 16, n, ref, 2.0 ** -24)).all()
