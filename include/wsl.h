@@ -71,11 +71,12 @@ enum { WSL_W_BF16 = 0, WSL_W_NF4 = 1 };
 enum { WSL_OUT_F32 = 0, WSL_OUT_BF16 = 1 };
 
 /* Bits OR-ed into a call's optional device status word. */
-#define WSL_STATUS_NONFINITE 1u   /* a group (or cache row) held a NaN or an infinity; verify_drafts: no weights to sample */
+#define WSL_STATUS_NONFINITE 1u   /* a group (or cache row) held a NaN or an infinity; verify_drafts, sample_logits: nothing to sample */
 #define WSL_STATUS_OVERFLOW  2u   /* a group's absmax rounds to +inf in fp16 (>= 65520) */
 #define WSL_STATUS_INDEX     4u   /* a row index, cache slot, page, length or draft was out of range */
 #define WSL_STATUS_SWEEP_TIMEOUT 8u   /* linear_gemv_sweep: a stage barrier waited past its bound */
 #define WSL_STATUS_DESCRIPTOR    16u  /* linear_gemv_sweep: a device stage descriptor was invalid (skipped) */
+#define WSL_STATUS_PAGES         32u  /* kv_pages_grow: a sequence needed more pages than were free */
 
 /* Flags of linear_gemv_streamed / linear_gemm_streamed. */
 #define WSL_RING_PACE 1   /* the host keeps the copies at most two matrices ahead of the kernels */
@@ -481,6 +482,156 @@ int verify_drafts(const void *d_p, const void *d_q, int pfmt, int64_t n_seq, int
                   int64_t ld_p, int64_t ld_q, const int32_t *d_drafts, const int32_t *d_n_drafts, const float *d_u,
                   int32_t *d_accepted, int32_t *d_tokens, void *d_ws, size_t ws_bytes, uint32_t *d_status,
                   void *stream);
+
+/*
+ * The pages of a key-value cache kept on the device, described by the caller (host struct, read
+ * before a call returns): which pages each sequence holds, how long it is, and which are free.
+ *   (IPE page, "What is built": a decode step indexes preallocated buffers and never reads device
+ *   values back; deep-fold README, "Метод": a whole greedy step is one graph.)
+ * table      device int32 [n_seq][ld_table]: the block table that attn_decode reads; a sequence of L
+ *            tokens holds the first ceil(L / page_size) entries of its row.
+ * lens       device int32 [n_seq]: the tokens of each sequence (attn_decode's d_kv_lens).
+ * free_pages device int32 [n_pages], a stack: its first *n_free entries are the free pages.
+ * n_free     device int32 [1].
+ * n_seq 0 .. 65535.  pages_per_seq 1 .. ld_table.  n_pages 1 .. 2^31 - 1.  page_size 1 .. 2^30.
+ * A sequence holds at most pages_per_seq * page_size tokens, and 2^31 - 1.
+ */
+typedef struct wsl_kv_pages {
+    int32_t *table, *lens, *free_pages, *n_free;
+    int64_t n_seq, pages_per_seq, ld_table, n_pages, page_size;
+} wsl_kv_pages;
+
+/*
+ * kv_pages_grow -- take in new tokens: the pages they need, their cache slots and positions.
+ * Sequence b grows by d_new[b] tokens (by `each` where d_new is NULL).  The pages it lacks are taken
+ * off the top of the stack, in the order of sequences and of their places; its lens and the stack
+ * are moved on.  A call is made once for a step, before the layers' kv_cache_write.
+ * d_new       device int32 [n_seq] or NULL.      each   >= 0 (d_new NULL; else ignored).
+ * n_tokens    0 .. 2^30: room in d_slots and d_positions.
+ * d_slots     device int64 [n_tokens]: the slots for kv_cache_write; the tokens of sequence b lie at
+ *             starts[b] .. starts[b] + new[b] - 1, starts the running sum of new.  -1 where there
+ *             is no token, or one that is not taken in.
+ * d_positions device int64 [n_tokens] or NULL: the tokens' positions in their sequences, or -1.
+ * d_starts    device int32 [n_seq + 1] or NULL: starts and their end (at most n_tokens each).
+ * A sequence is left as it is, and its tokens get -1, where
+ *   - more pages are needed, by it and those before it, than are free (WSL_STATUS_PAGES): from
+ *     the first one on only sequences that need no page grow;
+ *   - its lens or new is negative, it would grow past its row, or its tokens past n_tokens
+ *     (WSL_STATUS_INDEX).  It then asks for no page.
+ * A token whose page number is outside [0, n_pages) gets -1 (WSL_STATUS_INDEX).  An *n_free outside
+ * [0, n_pages] is clamped to it and reported.
+ * d_ws        device workspace, 16-byte aligned, of kv_pages_grow_workspace_bytes (none where that is
+ *             0).  Its contents on entry do not matter.  Calls that share a workspace, or the same
+ *             pages, must not overlap.
+ * d_status    device uint32 or NULL.
+ */
+size_t kv_pages_grow_workspace_bytes(int64_t n_seq, int64_t n_tokens);
+int kv_pages_grow(const wsl_kv_pages *h_pages, const int32_t *d_new, int64_t each, int64_t n_tokens, int64_t *d_slots,
+                  int64_t *d_positions, int32_t *d_starts, void *d_ws, size_t ws_bytes, uint32_t *d_status,
+                  void *stream);
+
+/*
+ * kv_pages_trim -- shorten sequences to d_lens[b] tokens (fallen drafts; 0 for one that is done) and
+ * give the pages behind them back.  Of R pages given back, the r-th in the order of sequences
+ * and places comes to lie at free_pages[*n_free + R - 1 - r]: growing again by as much takes the same
+ * pages.  Table entries are left as they are.  A length at or above a sequence's own leaves it as
+ * it is.
+ * d_lens     device int32 [n_seq].  A negative one (or a lens outside the row) leaves the sequence as it
+ *            is and ORs WSL_STATUS_INDEX into the status word; pages that the stack has no room for are
+ *            dropped and reported so too.
+ */
+int kv_pages_trim(const wsl_kv_pages *h_pages, const int32_t *d_lens, uint32_t *d_status, void *stream);
+
+/*
+ * rotary_embed -- rotary positions: pairs of a head's elements turned by position * frequency.
+ *   (Between the fused projection of linear_gemm and kv_cache_write / attn_decode.)
+ * For the token at position p and pair i < rot_dim / 2, with the angle p * freqs[i]:
+ *   (a, b) -> amplitude * (a cos - b sin, a sin + b cos),
+ * a and b the elements i and i + rot_dim / 2 of the head (or, with WSL_ROTARY_INTERLEAVED, 2i and
+ * 2i + 1); elements from rot_dim on are copied.  Angles are reduced in 64 bits: cos and sin are right
+ * to 2^-24 where |p * freqs[i]| < 2^40, the products and sums are in fp32.
+ * d_q, d_k     device [count][ld] of xfmt (WSL_OUT_F32 or WSL_OUT_BF16): n_heads (n_kv) * head_dim elements a
+ *              token; 16-byte aligned, ld a multiple of 16 bytes (views of a fused projection serve).
+ *              d_k may be NULL (then d_k_out is ignored).
+ * d_q_out, d_k_out   the same of ofmt; each may be its input itself where ofmt is xfmt (and the lds
+ *              are equal).  Other overlaps are not allowed.
+ * count >= 0 (0 launches nothing).  n_heads, n_kv 1 .. 2^16.  head_dim 16 .. 256, a multiple of 16.
+ * rot_dim      2 .. head_dim, even.
+ * count * (n_heads + n_kv) * head_dim <= 2^40.
+ * d_positions  device int64 [count], any (kv_pages_grow's -1 too).
+ * d_freqs      device float64 [rot_dim / 2], radians a position: scaling for long contexts is in them.
+ * amplitude    finite.      flags   0 or WSL_ROTARY_INTERLEAVED.
+ */
+#define WSL_ROTARY_INTERLEAVED 1
+int rotary_embed(const void *d_q, int64_t n_heads, int64_t ld_q, const void *d_k, int64_t n_kv, int64_t ld_k, int xfmt,
+                 int64_t count, int64_t head_dim, int64_t rot_dim, const int64_t *d_positions, const double *d_freqs,
+                 double amplitude, int flags, void *d_q_out, int64_t ld_q_out, void *d_k_out, int64_t ld_k_out, int ofmt,
+                 void *stream);
+
+/* Settings of sample_logits (host struct): one value for all rows, or (device, [n_rows]) one for each. */
+typedef struct wsl_sampling {
+    const float *d_temperature;      /* device or NULL: temperature for all */
+    const int32_t *d_top_k;
+    const float *d_top_p, *d_min_p;
+    float temperature;
+    int32_t top_k;
+    float top_p, min_p;
+} wsl_sampling;
+
+/*
+ * sample_logits -- tokens from logits and given random numbers, and the distribution they come from.
+ *   (What follows the packed head's GEMM, and, with d_probs, what verify_drafts takes as p and q.)
+ * A row's entries z are ordered by value, equal ones by index.
+ *   K: the first top_k entries (all where top_k <= 0);
+ *   w_j = exp((z_j - max z) / temperature);
+ *   P: the entries of K before which less than top_p * (sum of w over K) lies (all where top_p >= 1);
+ *   Q: those with w_j >= min_p (all where min_p <= 0).
+ * The entries in K, P and Q, always the first one, are kept; the token is the least j with
+ *   sum of the kept w_0 .. w_j > u * (sum of all kept), or the last kept where none is (u >= 1 or NaN),
+ * and probs_j = w_j / (sum of all kept), 0 for the rest.  Where temperature is not above 0 the first
+ * entry alone is kept.  A NaN in top_p or min_p counts as off.  Weights are right to 2^-40, sums and
+ * decisions are in 64 bits.
+ * Entries of -infinity are out.  A row that holds a NaN or +infinity, or nothing but -infinity, gives
+ * token -1, probabilities 0, and WSL_STATUS_NONFINITE.
+ * d_logits   device [n_rows][ld] of zfmt (WSL_OUT_F32 or WSL_OUT_BF16), the first vocab of each row used;
+ *            aligned to its element.
+ * n_rows     0 .. 65535 (0 launches nothing).      vocab 1 .. 2^22.
+ * h_settings NULL: temperature 1, nothing off.
+ * d_u        device fp32 [n_rows]; may be NULL where d_tokens is.
+ * d_tokens   device int32 [n_rows] or NULL.     d_probs  device fp32 [n_rows][ld_probs] or NULL; one of
+ *            them is needed.  Entries of a row past vocab are not written.
+ * d_ws       device workspace, 16-byte aligned, of sample_logits_workspace_bytes (none where that is 0).
+ *            Its contents on entry do not matter.  Calls that share a workspace must not overlap.
+ */
+size_t sample_logits_workspace_bytes(int64_t n_rows, int64_t vocab);
+int sample_logits(const void *d_logits, int zfmt, int64_t n_rows, int64_t vocab, int64_t ld,
+                  const wsl_sampling *h_settings, const float *d_u, int32_t *d_tokens, float *d_probs, int64_t ld_probs,
+                  void *d_ws, size_t ws_bytes, uint32_t *d_status, void *stream);
+
+/*
+ * lora_add -- low-rank adapters of many requests at once, beside a projection they share:
+ *   out[t] = base[t] + scale[a] * B[a] (A[a] x[t]),  a = ids[t]; out[t] = base[t] where ids[t] is -1.
+ *   (base is what linear_gemm gives for the packed matrix, which no adapter changes.)
+ * d_a       device bf16 [n_adapters][rank][k], d_b device bf16 [n_adapters][n_out][rank]: contiguous,
+ *           16-byte aligned.  An adapter of a smaller rank has zeros in its last rows of A (or columns of B).
+ * n_adapters 1 .. 2^20.   rank 8 .. 128, a multiple of 8.   n_out 1 .. 2^22.   k 8 .. 2^22, a multiple of 8.
+ * d_ids     device int32 [m].  One outside [-1, n_adapters) counts as -1 (WSL_STATUS_INDEX).
+ * d_scales  device fp32 [n_adapters], or NULL: 1.
+ * d_x       device bf16 [m][ldx], 16-byte aligned, ldx a multiple of 8.   m 0 .. 2^24 (0 launches nothing).
+ * d_base    device [m][ld_base] of fmt (WSL_OUT_F32 or WSL_OUT_BF16), aligned to its element.
+ * d_out     device [m][ld_out] of fmt; may be d_base itself (with the same ld), no other overlap.
+ * A x is summed in fp32 and scaled there; its product with B too.  (On the matrix cores A x enters as
+ * three bf16 numbers, 24 bits; there an infinity in B gives a NaN.)  The sum with base is rounded once to
+ * fmt.  Rows without an adapter are copied.  An adapter has no part in other tokens' rows, whatever
+ * it holds.  Deterministic.
+ * d_ws      device workspace, 16-byte aligned, of lora_add_workspace_bytes (A x in parts of k).  Its
+ *           contents on entry do not matter.  Calls that share a workspace must not overlap.
+ */
+size_t lora_add_workspace_bytes(int64_t m, int64_t rank, int64_t k);
+int lora_add(const void *d_a, const void *d_b, int64_t n_adapters, int64_t rank, int64_t n_out, int64_t k,
+             const int32_t *d_ids, const float *d_scales, const void *d_x, int64_t m, int64_t ldx, const void *d_base,
+             int64_t ld_base, void *d_out, int64_t ld_out, int fmt, void *d_ws, size_t ws_bytes, uint32_t *d_status,
+             void *stream);
 
 /*
  * wsl_stream_read -- measurement aid, not part of the linear path: a read-only

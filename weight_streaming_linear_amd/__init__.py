@@ -14,6 +14,9 @@ Entry points (same names as the C ABI):
   linear_gemv_sweep_workspace_bytes);
   KVCache (wsl_kv_cache) with kv_cache_write, kv_cache_read, attn_decode and
   attn_decode_workspace_bytes; verify_drafts and verify_drafts_workspace_bytes;
+  KVPages (wsl_kv_pages) with kv_pages_grow, kv_pages_trim and kv_pages_grow_workspace_bytes;
+  rotary_embed (rotary_freqs makes its frequencies); sample_logits and
+  sample_logits_workspace_bytes; lora_add and lora_add_workspace_bytes;
   stream_read (wsl_stream_read); CopyRing.gemv / CopyRing.gemm (linear_gemv_streamed /
   linear_gemm_streamed, weights streamed from page-locked host memory, see to_pinned).
 """
@@ -43,9 +46,13 @@ EXPORTED = [
     "linear_gemv_sweep_workspace_bytes", "linear_gemv_sweep", "linear_gemv_multi",
     "kv_cache_write", "kv_cache_read", "attn_decode_workspace_bytes", "attn_decode",
     "verify_drafts_workspace_bytes", "verify_drafts",
+    "kv_pages_grow_workspace_bytes", "kv_pages_grow", "kv_pages_trim", "rotary_embed",
+    "sample_logits_workspace_bytes", "sample_logits", "lora_add_workspace_bytes", "lora_add",
 ]
 WSL_STATUS_SWEEP_TIMEOUT = 8
 WSL_STATUS_DESCRIPTOR = 16
+WSL_STATUS_PAGES = 32           # kv_pages_grow: a sequence needed more pages than were free
+WSL_ROTARY_INTERLEAVED = 1
 SWEEP_STATUS_OFFSET = 1280      # byte offset of the status word in the sweep workspace
 WSL_E_SCRATCH = 9
 WSL_E_FLAGS = 10
@@ -115,6 +122,23 @@ def lib():
     L.verify_drafts_workspace_bytes.restype = sz
     L.verify_drafts.argtypes = [vp, vp, ci, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp, sz, vp, vp]
     L.verify_drafts.restype = ci
+    L.kv_pages_grow_workspace_bytes.argtypes = [i64, i64]
+    L.kv_pages_grow_workspace_bytes.restype = sz
+    L.kv_pages_grow.argtypes = [vp, vp, i64, i64, vp, vp, vp, vp, sz, vp, vp]
+    L.kv_pages_grow.restype = ci
+    L.kv_pages_trim.argtypes = [vp, vp, vp, vp]
+    L.kv_pages_trim.restype = ci
+    L.rotary_embed.argtypes = [vp, i64, i64, vp, i64, i64, ci, i64, i64, i64, vp, vp, ctypes.c_double, ci, vp, i64, vp,
+                               i64, ci, vp]
+    L.rotary_embed.restype = ci
+    L.sample_logits_workspace_bytes.argtypes = [i64, i64]
+    L.sample_logits_workspace_bytes.restype = sz
+    L.sample_logits.argtypes = [vp, ci, i64, i64, i64, vp, vp, vp, vp, i64, vp, sz, vp, vp]
+    L.sample_logits.restype = ci
+    L.lora_add_workspace_bytes.argtypes = [i64, i64, i64]
+    L.lora_add_workspace_bytes.restype = sz
+    L.lora_add.argtypes = [vp, vp, i64, i64, i64, i64, vp, vp, vp, i64, i64, vp, i64, vp, i64, ci, vp, sz, vp, vp]
+    L.lora_add.restype = ci
     L.wsl_stream_read.argtypes = [vp, sz, vp, vp]
     L.wsl_stream_read.restype = ctypes.c_int
     L.wsl_strerror.argtypes = [ctypes.c_int]
@@ -723,6 +747,359 @@ def verify_drafts(p, q, drafts, u, n_drafts=None, accepted=None, tokens=None, wo
     if rc:
         _check(rc, "verify_drafts")
     return accepted, tokens
+
+
+# ---------------------------------------------------------------- pages, positions, sampling, adapters
+def _here(device):
+    """Refuse tensors of another GPU than the current one, whose streams the launches go to."""
+    if device.index != _device():
+        raise ValueError(f"tensors on {device}, the current device is {_device()}")
+
+
+class WslKvPages(ctypes.Structure):
+    """struct wsl_kv_pages of the C ABI."""
+    _fields_ = [("table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("free_pages", ctypes.c_void_p),
+                ("n_free", ctypes.c_void_p), ("n_seq", ctypes.c_int64), ("pages_per_seq", ctypes.c_int64),
+                ("ld_table", ctypes.c_int64), ("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int64)]
+
+
+class KVPages:
+    """The handle of a cache's pages kept on the device (wsl_kv_pages), over tensors that the caller owns.
+
+    table: int32 [n_seq][pages_per_seq], the block table of attn_decode; lens: int32 [n_seq], the
+    tokens of each sequence; free: int32 [n_pages], a stack whose first n_free (int32 [1]) entries are
+    the free pages.  All layers' caches share them.  The handle keeps the tensors alive."""
+
+    def __init__(self, table, lens, free, n_free, page_size):
+        import torch
+        dtype = (torch.int32,)
+        _require(table, "table", dtype, ndim=2)
+        dev = table.device
+        n_seq, per = table.shape
+        _require(lens, "lens", dtype, device=dev, contiguous=True, ndim=1)
+        _require(free, "free", dtype, device=dev, contiguous=True, ndim=1)
+        _require(n_free, "n_free", dtype, device=dev)
+        if lens.numel() != n_seq or n_free.numel() != 1:
+            raise ValueError(f"lens: {lens.numel()} entries, n_free: {n_free.numel()}, the table has {n_seq} rows")
+        ld = table.stride(0) if n_seq > 1 else per
+        if ld < per:
+            raise ValueError(f"table: rows of {per} entries lie {ld} apart")
+        if int(page_size) < 1 or per < 1 or free.numel() < 1:
+            raise ValueError(f"page_size {page_size}, rows of {per} entries, {free.numel()} pages")
+        self.table, self.lens, self.free, self.n_free = table, lens, free, n_free
+        self.device, self.n_seq, self.page_size = dev, n_seq, int(page_size)
+        self.desc = WslKvPages(table.data_ptr(), lens.data_ptr(), free.data_ptr(), n_free.data_ptr(), n_seq, per, ld,
+                               free.numel(), self.page_size)
+        self.ref = ctypes.byref(self.desc)
+
+    @classmethod
+    def empty(cls, n_seq, pages_per_seq, n_pages, page_size, device="cuda"):
+        """Sequences without tokens, and all pages free (page 0 on top)."""
+        import torch
+        free = torch.arange(int(n_pages) - 1, -1, -1, dtype=torch.int32, device=device)
+        return cls(torch.zeros((int(n_seq), int(pages_per_seq)), dtype=torch.int32, device=device),
+                   torch.zeros(int(n_seq), dtype=torch.int32, device=device), free,
+                   torch.full((1,), int(n_pages), dtype=torch.int32, device=device), page_size)
+
+
+@functools.lru_cache(maxsize=256)
+def kv_pages_grow_workspace_bytes(n_seq, n_tokens):
+    return int(lib().kv_pages_grow_workspace_bytes(int(n_seq), int(n_tokens)))
+
+
+def kv_pages_grow(pages, new, n_tokens=None, slots=None, positions=None, starts=None, workspace=None, status=None,
+                  stream=None):
+    """Take new tokens of every sequence of a KVPages in; returns their (slots, positions), int64
+    [n_tokens] each, -1 where there is none or it has no page.
+
+    new: one number for all sequences, or int32 [n_seq] (then give n_tokens, the room for their sum);
+    starts: int32 [n_seq + 1] to be written with where each sequence's tokens begin."""
+    import torch
+    dev, n_seq = pages.device, pages.n_seq
+    _here(dev)
+    if isinstance(new, int):
+        want, each = None, new
+        if n_tokens is None:
+            n_tokens = n_seq * new if slots is None else slots.numel()
+    else:
+        _plain(new, "new", torch.int32, dev, (n_seq,))
+        want, each = new.data_ptr(), 0
+        if n_tokens is None:
+            if slots is None:
+                raise ValueError("n_tokens: needed where new is a tensor")
+            n_tokens = slots.numel()
+    if n_tokens < 0:
+        raise ValueError(f"{n_tokens} tokens")
+    if slots is None and positions is None:
+        slots, positions = _new((2, n_tokens), torch.int64, dev, stream).unbind(0)
+    else:
+        slots = _new((n_tokens,), torch.int64, dev, stream) if slots is None else slots
+        positions = _new((n_tokens,), torch.int64, dev, stream) if positions is None else positions
+        _plain(slots, "slots", torch.int64, dev, (n_tokens,))
+        _plain(positions, "positions", torch.int64, dev, (n_tokens,))
+    if starts is not None:
+        _plain(starts, "starts", torch.int32, dev, (n_seq + 1,))
+    if status is not None:
+        _status(status, dev)
+    if workspace is None:
+        ws_bytes = kv_pages_grow_workspace_bytes(n_seq, n_tokens)
+        if ws_bytes:
+            workspace = _new(ws_bytes, torch.uint8, dev, stream)
+    else:
+        _require(workspace, "workspace", (workspace.dtype,), device=dev, contiguous=True)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    rc = lib().kv_pages_grow(pages.ref, want, each, n_tokens, slots.data_ptr(), positions.data_ptr(), _ptr(starts),
+                             _ptr(workspace), ws_bytes, _ptr(status), _stream(stream))
+    if rc:
+        _check(rc, "kv_pages_grow")
+    return slots, positions
+
+
+def kv_pages_trim(pages, lens, status=None, stream=None):
+    """Shorten the sequences of a KVPages to lens (int32 [n_seq]; one at or above a sequence's own length
+    leaves it) and give the pages behind them back."""
+    import torch
+    _here(pages.device)
+    _plain(lens, "lens", torch.int32, pages.device, (pages.n_seq,))
+    if status is not None:
+        _status(status, pages.device)
+    rc = lib().kv_pages_trim(pages.ref, lens.data_ptr(), _ptr(status), _stream(stream))
+    if rc:
+        _check(rc, "kv_pages_trim")
+
+
+def rotary_freqs(rot_dim, base=10000.0, scaling=None, factor=1.0, trained=8192, low=1.0, high=4.0, device="cuda"):
+    """The frequencies of rotary_embed, float64 [rot_dim / 2], radians a position: base ** (-2 i / rot_dim).
+
+    scaling, for positions up to `factor` times those trained with: None; "linear" (all frequencies
+    divided by factor); "base" (base times factor ** (rot_dim / (rot_dim - 2)): the slowest pair is
+    divided by factor, the fastest kept); "bands" (a pair that turns at least `high` times over the
+    `trained` positions is kept, one that turns at most `low` times divided, in between by the
+    line from the one to the other)."""
+    import math
+
+    import torch
+    rot_dim = int(rot_dim)
+    if rot_dim < 2 or rot_dim % 2 or not base > 0 or not factor > 0:
+        raise ValueError(f"rot_dim {rot_dim}, base {base}, factor {factor}")
+    if scaling not in (None, "linear", "base", "bands"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    if scaling == "base":
+        if rot_dim == 2:
+            raise ValueError("scaling 'base' needs rot_dim > 2")
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    freqs = [base ** (-2.0 * i / rot_dim) for i in range(rot_dim // 2)]
+    if scaling == "linear":
+        freqs = [f / factor for f in freqs]
+    elif scaling == "bands":
+        if not high > low or not trained > 0:
+            raise ValueError(f"bands from {low} to {high} turns over {trained} positions")
+        for i, f in enumerate(freqs):
+            kept = min(1.0, max(0.0, (trained * f / (2 * math.pi) - low) / (high - low)))
+            freqs[i] = f * (kept + (1.0 - kept) / factor)
+    return torch.tensor(freqs, dtype=torch.float64, device=device)
+
+
+def rotary_embed(q, positions, freqs, k=None, interleaved=False, amplitude=1.0, out=None, k_out=None, ofmt=None,
+                 stream=None):
+    """Turn pairs of elements of q (and k) by their token's position times freqs; returns out, or
+    (out, k_out) with a k.
+
+    q, k: [count][heads][head_dim] or [n_seq][q_len][heads][head_dim] (views of a fused projection
+    serve), fp32 or bf16; positions: int64 [count] or [n_seq][q_len]; freqs: float64 [rot_dim / 2]
+    (rotary_freqs), the rest of a head is copied; interleaved: pairs lie side by side instead of half
+    a rotation apart; amplitude: a factor of the turned elements; out, k_out may be q and k."""
+    import torch
+    dev = q.device
+    shape = tuple(q.shape)
+    if len(shape) not in (3, 4):
+        raise ValueError(f"q: expected 3 or 4 dimensions, got shape {shape}")
+    if not q.is_cuda:
+        raise ValueError(f"q: expected a GPU tensor, got one on {dev}")
+    _here(dev)
+    xfmt = _float_format(q, "q")
+    ld_q = _head_rows(q, "q", dev, shape)
+    count = shape[0] if len(shape) == 3 else shape[0] * shape[1]
+    if positions.numel() != count or positions.dtype is not torch.int64 or positions.device != dev or \
+            not positions.is_contiguous():
+        _require(positions, "positions", (torch.int64,), device=dev, contiguous=True)
+        raise ValueError(f"positions: shape {tuple(positions.shape)}, {count} tokens")
+    if freqs.dtype is not torch.float64 or freqs.device != dev or freqs.dim() != 1 or not freqs.is_contiguous():
+        _require(freqs, "freqs", (torch.float64,), device=dev, contiguous=True, ndim=1)
+    if ofmt is None:
+        ofmt = xfmt if out is None else _float_format(out, "out")
+    dtype = _float_dtype(ofmt)
+    heads, dim = shape[-2:]
+    if out is None:
+        out = _new(shape, dtype, dev, stream)
+        ld_out = heads * dim
+    else:
+        if out.dtype is not dtype:
+            raise ValueError(f"out: dtype {out.dtype}, expected {dtype}")
+        ld_out = _head_rows(out, "out", dev, shape)
+    n_kv = ld_k = ld_ko = 0
+    if k is not None:
+        if k.dtype is not q.dtype:
+            raise ValueError(f"k: dtype {k.dtype}, q has {q.dtype}")
+        if k.dim() != len(shape):
+            raise ValueError(f"k: shape {tuple(k.shape)}, q has {shape}")
+        n_kv = k.shape[-2]
+        k_shape = shape[:-2] + (n_kv, dim)
+        ld_k = _head_rows(k, "k", dev, k_shape)
+        if k_out is None:
+            k_out = _new(k_shape, dtype, dev, stream)
+            ld_ko = n_kv * dim
+        else:
+            if k_out.dtype is not dtype:
+                raise ValueError(f"k_out: dtype {k_out.dtype}, expected {dtype}")
+            ld_ko = _head_rows(k_out, "k_out", dev, k_shape)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    rc = lib().rotary_embed(q.data_ptr(), heads, ld_q, _ptr(k), n_kv, ld_k, xfmt, count, dim, 2 * freqs.numel(),
+                            positions.data_ptr(), freqs.data_ptr(), float(amplitude),
+                            WSL_ROTARY_INTERLEAVED if interleaved else 0, out.data_ptr(), ld_out, _ptr(k_out), ld_ko, ofmt,
+                            _stream(stream))
+    if rc:
+        _check(rc, "rotary_embed")
+    return out if k is None else (out, k_out)
+
+
+class WslSampling(ctypes.Structure):
+    """struct wsl_sampling of the C ABI."""
+    _fields_ = [("d_temperature", ctypes.c_void_p), ("d_top_k", ctypes.c_void_p), ("d_top_p", ctypes.c_void_p),
+                ("d_min_p", ctypes.c_void_p), ("temperature", ctypes.c_float), ("top_k", ctypes.c_int32),
+                ("top_p", ctypes.c_float), ("min_p", ctypes.c_float)]
+
+
+@functools.lru_cache(maxsize=256)
+def sample_logits_workspace_bytes(n_rows, vocab):
+    return int(lib().sample_logits_workspace_bytes(int(n_rows), int(vocab)))
+
+
+def _logit_rows(t, name, n):
+    """The elements from row to row of a [n][vocab] tensor with contiguous rows of their own."""
+    if t.is_contiguous():
+        return t.shape[1]
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: last dimension must have stride 1 (got strides {t.stride()})")
+    ld = t.stride(0) if n > 1 else t.shape[1]
+    if ld < t.shape[1]:
+        raise ValueError(f"{name}: rows of {t.shape[1]} entries lie {ld} apart (a broadcast tensor needs .contiguous())")
+    return ld
+
+
+def sample_logits(logits, u=None, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tokens=None, probs=None,
+                  workspace=None, status=None, stream=None):
+    """A token (int32 [n]) of each row of logits [n][vocab] (fp32 or bf16) from u, fp32 [n] in [0, 1).
+
+    temperature, top_p, min_p: numbers, or fp32 [n]; top_k: a number, or int32 [n]; a temperature of 0 takes
+    the greatest entry, top_k 0, top_p 1 and min_p 0 are off.  probs: fp32 [n][vocab] to be written with
+    the distribution that is sampled (what verify_drafts takes).  Without u nothing is sampled, and probs
+    (a new tensor unless given) is returned."""
+    import torch
+    if logits.dim() != 2 or not logits.is_cuda:
+        raise ValueError(f"logits: expected a GPU tensor of 2 dimensions, got shape {tuple(logits.shape)} on {logits.device}")
+    n, vocab = logits.shape
+    dev = logits.device
+    _here(dev)
+    zfmt = _float_format(logits, "logits")
+    ld, ld_probs = _logit_rows(logits, "logits", n), 0
+    how = WslSampling()
+    for name, value, dtype in (("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
+                               ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
+        if isinstance(value, torch.Tensor):
+            _plain(value, name, dtype, dev, (n,))
+            setattr(how, "d_" + name, value.data_ptr())
+        else:
+            setattr(how, name, value)
+    if u is not None:
+        _plain(u, "u", torch.float32, dev, (n,))
+        if tokens is None:
+            tokens = u.new_empty((n,), dtype=torch.int32) if stream is None else _new((n,), torch.int32, dev, stream)
+        else:
+            _plain(tokens, "tokens", torch.int32, dev, (n,))
+    elif tokens is not None:
+        raise ValueError("tokens without u")
+    elif probs is None:
+        probs = _new((n, vocab), torch.float32, dev, stream)
+    if probs is not None:
+        if probs.dtype is not torch.float32 or probs.device != dev or probs.shape != logits.shape:
+            raise ValueError(f"probs: {probs.dtype} {tuple(probs.shape)} on {probs.device}, expected float32 {tuple(logits.shape)}")
+        ld_probs = _logit_rows(probs, "probs", n)
+    if status is not None:
+        _status(status, dev)
+    if workspace is None:
+        ws_bytes = sample_logits_workspace_bytes(n, vocab)
+        if ws_bytes:
+            workspace = _new(ws_bytes, torch.uint8, dev, stream)
+    else:
+        _require(workspace, "workspace", (workspace.dtype,), device=dev, contiguous=True)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    rc = lib().sample_logits(logits.data_ptr(), zfmt, n, vocab, ld, ctypes.byref(how), _ptr(u), _ptr(tokens), _ptr(probs),
+                             ld_probs, _ptr(workspace), ws_bytes, _ptr(status), _stream(stream))
+    if rc:
+        _check(rc, "sample_logits")
+    return probs if u is None else tokens
+
+
+@functools.lru_cache(maxsize=256)
+def lora_add_workspace_bytes(m, rank, k):
+    return int(lib().lora_add_workspace_bytes(int(m), int(rank), int(k)))
+
+
+def _token_rows(t, name, m, width):
+    """The elements from row to row of a [m][width] tensor with contiguous rows of their own."""
+    if t.shape != (m, width):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(m, width)}")
+    return _logit_rows(t, name, m)
+
+
+def lora_add(base, x, a, b, ids, scales=None, out=None, workspace=None, status=None, stream=None):
+    """base + scales[ids] * b[ids] (a[ids] x), row by row; a row whose id is -1 is base's.
+
+    base: [m][n_out], fp32 or bf16 (a linear layer's output); x: bf16 [m][k] (its input); a: bf16
+    [n_adapters][rank][k]; b: bf16 [n_adapters][n_out][rank]; ids: int32 [m]; scales: fp32 [n_adapters], 1
+    unless given; out: a new tensor unless given, and may be base."""
+    import torch
+    if a.dim() != 3 or x.dim() != 2 or base.dim() != 2:
+        raise ValueError(f"a, x, base: shapes {tuple(a.shape)}, {tuple(x.shape)}, {tuple(base.shape)}")
+    dev = base.device
+    if not base.is_cuda:
+        raise ValueError(f"base: expected a GPU tensor, got one on {dev}")
+    _here(dev)
+    fmt = _float_format(base, "base")
+    n_adapters, rank, k = a.shape
+    m, n_out = base.shape
+    if x.dtype is not torch.bfloat16 or x.device != dev:
+        raise ValueError(f"x: {x.dtype} on {x.device}, expected bfloat16 on {dev}")
+    ld_base, ldx = _token_rows(base, "base", m, n_out), _token_rows(x, "x", m, k)
+    _plain(a, "a", torch.bfloat16, dev, (n_adapters, rank, k))
+    _plain(b, "b", torch.bfloat16, dev, (n_adapters, n_out, rank))
+    _plain(ids, "ids", torch.int32, dev, (m,))
+    if scales is not None:
+        _plain(scales, "scales", torch.float32, dev, (n_adapters,))
+    if out is None:
+        out = base.new_empty((m, n_out)) if stream is None else _new((m, n_out), base.dtype, dev, stream)
+        ld_out = n_out
+    else:
+        if out.dtype is not base.dtype or out.device != dev:
+            raise ValueError(f"out: {out.dtype} on {out.device}, expected {base.dtype} on {dev}")
+        ld_out = _token_rows(out, "out", m, n_out)
+    if status is not None:
+        _status(status, dev)
+    if workspace is None:
+        ws_bytes = lora_add_workspace_bytes(m, rank, k)
+        if ws_bytes:
+            workspace = _new(ws_bytes, torch.uint8, dev, stream)
+    else:
+        _require(workspace, "workspace", (workspace.dtype,), device=dev, contiguous=True)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    rc = lib().lora_add(a.data_ptr(), b.data_ptr(), n_adapters, rank, n_out, k, ids.data_ptr(), _ptr(scales), x.data_ptr(),
+                        m, ldx, base.data_ptr(), ld_base, out.data_ptr(), ld_out, fmt, _ptr(workspace), ws_bytes,
+                        _ptr(status), _stream(stream))
+    if rc:
+        _check(rc, "lora_add")
+    return out
 
 
 def stream_read(buf, sink, stream=None):

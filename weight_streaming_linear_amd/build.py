@@ -15,7 +15,8 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libwsl.so")
 
 HIP_SOURCES = ["api.hip", "pack.hip", "gemv.hip", "gemm.hip", "embed.hip", "ring.hip", "probe.hip", "kvcache.hip",
-               "attn.hip", "attn_bf16.hip", "attn_e4m3.hip", "verify.hip"]
+               "attn.hip", "attn_bf16.hip", "attn_e4m3.hip", "verify.hip", "pages.hip", "rotary.hip", "sample.hip",
+               "lora.hip"]
 CXX_SOURCES = ["validate.cpp"]
 
 HIP_FLAGS = [

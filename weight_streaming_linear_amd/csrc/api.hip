@@ -35,6 +35,22 @@ size_t verify_ws_bytes(int64_t n_seq, int64_t vocab);
 int launch_verify(const void *p, const void *q, int pfmt, int64_t n_seq, int64_t width, int64_t vocab, int64_t ld_p,
                   int64_t ld_q, const int32_t *drafts, const int32_t *n_drafts, const float *u, int32_t *accepted,
                   int32_t *tokens, void *ws, uint32_t *status, hipStream_t s);
+size_t grow_ws_bytes(int64_t n_seq, int64_t n_tokens);
+int launch_grow(const wsl_kv_pages *p, const int32_t *d_new, int64_t each, int64_t n_tokens, int64_t *slots,
+                int64_t *positions, int32_t *starts, void *ws, uint32_t *status, hipStream_t s);
+int launch_trim(const wsl_kv_pages *p, const int32_t *lens, uint32_t *status, hipStream_t s);
+int launch_rotary(const void *q, int64_t n_heads, int64_t ld_q, const void *k, int64_t n_kv, int64_t ld_k, int xfmt,
+                  int64_t count, int64_t head_dim, int64_t rot_dim, const int64_t *positions, const double *freqs,
+                  double amplitude, int flags, void *q_out, int64_t ld_q_out, void *k_out, int64_t ld_k_out, int ofmt,
+                  hipStream_t s);
+size_t sample_ws_bytes(int64_t n_rows, int64_t vocab);
+int launch_sample(const void *logits, int zfmt, int64_t n_rows, int64_t vocab, int64_t ld, const wsl_sampling *how,
+                  const float *u, int32_t *tokens, float *probs, int64_t ld_probs, void *ws, uint32_t *status,
+                  hipStream_t s);
+size_t lora_ws_bytes(int64_t m, int64_t rank, int64_t k);
+int launch_lora(const void *d_a, const void *d_b, int64_t n_adapters, int64_t rank, int64_t n_out, int64_t k,
+                const int32_t *ids, const float *scales, const void *x, int64_t m, int64_t ldx, const void *base,
+                int64_t ld_base, void *out, int64_t ld_out, int fmt, void *ws, uint32_t *status, hipStream_t s);
 int check_pinned(int64_t count, const void *const *h_w);
 int ring_gemv(int wfmt, int64_t count, const void *const *h_w, const int64_t *n_out, const int64_t *k,
               const void *const *x, float *const *y, void *const *slot, hipStream_t copy, hipStream_t compute,
@@ -251,6 +267,75 @@ int verify_drafts(const void *d_p, const void *d_q, int pfmt, int64_t n_seq, int
     if ((rc = wsl::device_ok()) != WSL_OK) return rc;
     return wsl::after_launch(wsl::launch_verify(d_p, d_q, pfmt, n_seq, width, vocab, ld_p, ld_q, d_drafts, d_n_drafts,
                                                 d_u, d_accepted, d_tokens, d_ws, d_status, wsl::as_stream(stream)));
+}
+
+size_t kv_pages_grow_workspace_bytes(int64_t n_seq, int64_t n_tokens) {
+    if (n_seq < 0 || n_seq > 65535 || n_tokens < 0 || n_tokens > wsl::kMaxDim) return 0;
+    return wsl::grow_ws_bytes(n_seq, n_tokens);
+}
+
+int kv_pages_grow(const wsl_kv_pages *h_pages, const int32_t *d_new, int64_t each, int64_t n_tokens, int64_t *d_slots,
+                  int64_t *d_positions, int32_t *d_starts, void *d_ws, size_t ws_bytes, uint32_t *d_status,
+                  void *stream) {
+    int rc = wsl::check_grow(h_pages, d_new, each, n_tokens, d_slots, d_positions, d_starts);
+    if (rc != WSL_OK || (h_pages->n_seq == 0 && n_tokens == 0 && !d_starts)) return rc;
+    if ((rc = wsl::check_workspace(d_ws, ws_bytes, wsl::grow_ws_bytes(h_pages->n_seq, n_tokens), 16)) != WSL_OK) return rc;
+    if ((rc = wsl::device_ok()) != WSL_OK) return rc;
+    return wsl::after_launch(wsl::launch_grow(h_pages, d_new, each, n_tokens, d_slots, d_positions, d_starts, d_ws,
+                                              d_status, wsl::as_stream(stream)));
+}
+
+int kv_pages_trim(const wsl_kv_pages *h_pages, const int32_t *d_lens, uint32_t *d_status, void *stream) {
+    int rc = wsl::check_trim(h_pages, d_lens);
+    if (rc != WSL_OK || h_pages->n_seq == 0) return rc;
+    if ((rc = wsl::device_ok()) != WSL_OK) return rc;
+    return wsl::after_launch(wsl::launch_trim(h_pages, d_lens, d_status, wsl::as_stream(stream)));
+}
+
+int rotary_embed(const void *d_q, int64_t n_heads, int64_t ld_q, const void *d_k, int64_t n_kv, int64_t ld_k, int xfmt,
+                 int64_t count, int64_t head_dim, int64_t rot_dim, const int64_t *d_positions, const double *d_freqs,
+                 double amplitude, int flags, void *d_q_out, int64_t ld_q_out, void *d_k_out, int64_t ld_k_out, int ofmt,
+                 void *stream) {
+    int rc = wsl::check_rotary(d_q, n_heads, ld_q, d_k, n_kv, ld_k, xfmt, count, head_dim, rot_dim, d_positions, d_freqs,
+                               amplitude, flags, d_q_out, ld_q_out, d_k_out, ld_k_out, ofmt);
+    if (rc != WSL_OK || count == 0) return rc;
+    if ((rc = wsl::device_ok()) != WSL_OK) return rc;
+    return wsl::after_launch(wsl::launch_rotary(d_q, n_heads, ld_q, d_k, n_kv, ld_k, xfmt, count, head_dim, rot_dim,
+                                                d_positions, d_freqs, amplitude, flags, d_q_out, ld_q_out, d_k_out,
+                                                ld_k_out, ofmt, wsl::as_stream(stream)));
+}
+
+size_t sample_logits_workspace_bytes(int64_t n_rows, int64_t vocab) {
+    if (n_rows <= 0 || n_rows > 65535 || vocab <= 0 || vocab > wsl::kMaxSampleVocab) return 0;
+    return wsl::sample_ws_bytes(n_rows, vocab);
+}
+
+int sample_logits(const void *d_logits, int zfmt, int64_t n_rows, int64_t vocab, int64_t ld,
+                  const wsl_sampling *h_settings, const float *d_u, int32_t *d_tokens, float *d_probs, int64_t ld_probs,
+                  void *d_ws, size_t ws_bytes, uint32_t *d_status, void *stream) {
+    int rc = wsl::check_sample(d_logits, zfmt, n_rows, vocab, ld, h_settings, d_u, d_tokens, d_probs, ld_probs);
+    if (rc != WSL_OK || n_rows == 0) return rc;
+    if ((rc = wsl::check_workspace(d_ws, ws_bytes, wsl::sample_ws_bytes(n_rows, vocab), 16)) != WSL_OK) return rc;
+    if ((rc = wsl::device_ok()) != WSL_OK) return rc;
+    return wsl::after_launch(wsl::launch_sample(d_logits, zfmt, n_rows, vocab, ld, h_settings, d_u, d_tokens, d_probs,
+                                                ld_probs, d_ws, d_status, wsl::as_stream(stream)));
+}
+
+size_t lora_add_workspace_bytes(int64_t m, int64_t rank, int64_t k) {
+    return m > 0 && wsl::lora_shape_ok(m, rank, k) ? wsl::lora_ws_bytes(m, rank, k) : 0;
+}
+
+int lora_add(const void *d_a, const void *d_b, int64_t n_adapters, int64_t rank, int64_t n_out, int64_t k,
+             const int32_t *d_ids, const float *d_scales, const void *d_x, int64_t m, int64_t ldx, const void *d_base,
+             int64_t ld_base, void *d_out, int64_t ld_out, int fmt, void *d_ws, size_t ws_bytes, uint32_t *d_status,
+             void *stream) {
+    int rc = wsl::check_lora(d_a, d_b, n_adapters, rank, n_out, k, d_ids, d_scales, d_x, m, ldx, d_base, ld_base, d_out,
+                             ld_out, fmt);
+    if (rc != WSL_OK || m == 0) return rc;
+    if ((rc = wsl::check_workspace(d_ws, ws_bytes, wsl::lora_ws_bytes(m, rank, k), 16)) != WSL_OK) return rc;
+    if ((rc = wsl::device_ok()) != WSL_OK) return rc;
+    return wsl::after_launch(wsl::launch_lora(d_a, d_b, n_adapters, rank, n_out, k, d_ids, d_scales, d_x, m, ldx, d_base,
+                                              ld_base, d_out, ld_out, fmt, d_ws, d_status, wsl::as_stream(stream)));
 }
 
 int wsl_stream_read(const void *d_buf, size_t bytes, uint32_t *d_sink, void *stream) {

@@ -266,6 +266,107 @@ int check_verify(const void *p, const void *q, int pfmt, int64_t n_seq, int64_t 
     return WSL_OK;
 }
 
+int check_kv_pages(const void *h_pages) {
+    if (!h_pages) return WSL_E_NULL;
+    const wsl_kv_pages &p = *static_cast<const wsl_kv_pages *>(h_pages);
+    if (p.n_seq < 0 || p.n_seq > 65535) return WSL_E_SHAPE;
+    if (p.pages_per_seq < 1 || p.pages_per_seq > 0x7fffffff || p.ld_table < p.pages_per_seq) return WSL_E_SHAPE;
+    if (p.n_pages < 1 || p.n_pages > 0x7fffffff || p.page_size < 1 || p.page_size > kMaxDim) return WSL_E_SHAPE;
+    int64_t all = 0;
+    if (!mul_ok(p.n_seq, p.ld_table, &all) || all > INT64_MAX / 8) return WSL_E_SHAPE;
+    if (p.n_seq == 0) return WSL_OK;
+    if (!p.table || !p.lens || !p.free_pages || !p.n_free) return WSL_E_NULL;
+    if (!aligned(p.table, 4) || !aligned(p.lens, 4) || !aligned(p.free_pages, 4) || !aligned(p.n_free, 4))
+        return WSL_E_ALIGN;
+    return WSL_OK;
+}
+
+int check_grow(const void *h_pages, const void *d_new, int64_t each, int64_t n_tokens, const void *slots,
+               const void *positions, const void *starts) {
+    const int rc = check_kv_pages(h_pages);
+    if (rc != WSL_OK) return rc;
+    if (n_tokens < 0 || n_tokens > kMaxDim || (!d_new && (each < 0 || each > kMaxDim))) return WSL_E_SHAPE;
+    if (n_tokens > 0 && !slots) return WSL_E_NULL;
+    if (!aligned(d_new, 4) || !aligned(slots, 8) || !aligned(positions, 8) || !aligned(starts, 4)) return WSL_E_ALIGN;
+    return WSL_OK;
+}
+
+int check_trim(const void *h_pages, const void *lens) {
+    const int rc = check_kv_pages(h_pages);
+    if (rc != WSL_OK) return rc;
+    if (static_cast<const wsl_kv_pages *>(h_pages)->n_seq == 0) return WSL_OK;
+    if (!lens) return WSL_E_NULL;
+    return aligned(lens, 4) ? WSL_OK : WSL_E_ALIGN;
+}
+
+int check_rotary(const void *q, int64_t n_heads, int64_t ld_q, const void *k, int64_t n_kv, int64_t ld_k, int xfmt,
+                 int64_t count, int64_t head_dim, int64_t rot_dim, const void *positions, const void *freqs,
+                 double amplitude, int flags, const void *q_out, int64_t ld_q_out, const void *k_out, int64_t ld_k_out,
+                 int ofmt) {
+    if ((xfmt != WSL_OUT_F32 && xfmt != WSL_OUT_BF16) || (ofmt != WSL_OUT_F32 && ofmt != WSL_OUT_BF16))
+        return WSL_E_FORMAT;
+    if ((flags & ~WSL_ROTARY_INTERLEAVED) != 0) return WSL_E_FLAGS;
+    if (count < 0 || n_heads < 1 || n_heads > 65536 || (k && (n_kv < 1 || n_kv > 65536))) return WSL_E_SHAPE;
+    if (head_dim < 16 || head_dim > 256 || head_dim % 16 != 0) return WSL_E_SHAPE;
+    if (rot_dim < 2 || rot_dim > head_dim || rot_dim % 2 != 0 || !(amplitude - amplitude == 0)) return WSL_E_SHAPE;
+    if (count > (int64_t(1) << 40) / ((n_heads + (k ? n_kv : 0)) * head_dim)) return WSL_E_SHAPE;
+    if (count == 0) return WSL_OK;
+    if (!q || !q_out || !positions || !freqs || (k && !k_out)) return WSL_E_NULL;
+    int rc = check_token_rows(xfmt, count, n_heads * head_dim, ld_q);
+    if (rc == WSL_OK) rc = check_token_rows(ofmt, count, n_heads * head_dim, ld_q_out);
+    if (rc == WSL_OK && k) rc = check_token_rows(xfmt, count, n_kv * head_dim, ld_k);
+    if (rc == WSL_OK && k) rc = check_token_rows(ofmt, count, n_kv * head_dim, ld_k_out);
+    if (rc != WSL_OK) return rc;
+    if (!aligned(q, 16) || !aligned(q_out, 16) || !aligned(positions, 8) || !aligned(freqs, 8)) return WSL_E_ALIGN;
+    if (k && (!aligned(k, 16) || !aligned(k_out, 16))) return WSL_E_ALIGN;
+    return WSL_OK;
+}
+
+int check_sample(const void *logits, int zfmt, int64_t n_rows, int64_t vocab, int64_t ld, const void *h_settings,
+                 const void *u, const void *tokens, const void *probs, int64_t ld_probs) {
+    if (zfmt != WSL_OUT_F32 && zfmt != WSL_OUT_BF16) return WSL_E_FORMAT;
+    if (n_rows < 0 || n_rows > 65535 || vocab < 1 || vocab > kMaxSampleVocab) return WSL_E_SHAPE;
+    if (n_rows == 0) return WSL_OK;
+    if (!logits || (!tokens && !probs) || (tokens && !u)) return WSL_E_NULL;
+    int64_t all = 0;
+    if (ld < vocab || !mul_ok(n_rows, ld, &all) || all > INT64_MAX / 8) return WSL_E_SHAPE;
+    if (probs && (ld_probs < vocab || !mul_ok(n_rows, ld_probs, &all) || all > INT64_MAX / 8)) return WSL_E_SHAPE;
+    if (!aligned(logits, zfmt == WSL_OUT_F32 ? 4 : 2) || !aligned(u, 4) || !aligned(tokens, 4) || !aligned(probs, 4))
+        return WSL_E_ALIGN;
+    if (h_settings) {
+        const wsl_sampling &s = *static_cast<const wsl_sampling *>(h_settings);
+        if (!aligned(s.d_temperature, 4) || !aligned(s.d_top_k, 4) || !aligned(s.d_top_p, 4) || !aligned(s.d_min_p, 4))
+            return WSL_E_ALIGN;
+    }
+    return WSL_OK;
+}
+
+bool lora_shape_ok(int64_t m, int64_t rank, int64_t k) {
+    return m >= 0 && m <= (int64_t(1) << 24) && rank >= 8 && rank <= 128 && rank % 8 == 0 && k >= 8 &&
+           k <= kMaxLoraDim && k % 8 == 0;
+}
+
+int check_lora(const void *a, const void *b, int64_t n_adapters, int64_t rank, int64_t n_out, int64_t k, const void *ids,
+               const void *scales, const void *x, int64_t m, int64_t ldx, const void *base, int64_t ld_base,
+               const void *out, int64_t ld_out, int fmt) {
+    if (fmt != WSL_OUT_F32 && fmt != WSL_OUT_BF16) return WSL_E_FORMAT;
+    if (!lora_shape_ok(m, rank, k) || n_adapters < 1 || n_adapters > (int64_t(1) << 20) || n_out < 1 ||
+        n_out > kMaxLoraDim)
+        return WSL_E_SHAPE;
+    if (m == 0) return WSL_OK;
+    if (!a || !b || !ids || !x || !base || !out) return WSL_E_NULL;
+    int64_t all = 0;
+    if (ldx < k || ld_base < n_out || ld_out < n_out) return WSL_E_SHAPE;
+    if (!mul_ok(m, ldx, &all) || all > INT64_MAX / 8 || !mul_ok(m, ld_base, &all) || all > INT64_MAX / 8 ||
+        !mul_ok(m, ld_out, &all) || all > INT64_MAX / 8)
+        return WSL_E_SHAPE;
+    const uintptr_t elem = fmt == WSL_OUT_F32 ? 4 : 2;
+    if (ldx % 8 != 0 || !aligned(a, 16) || !aligned(b, 16) || !aligned(x, 16) || !aligned(ids, 4) || !aligned(scales, 4) ||
+        !aligned(base, elem) || !aligned(out, elem))
+        return WSL_E_ALIGN;
+    return WSL_OK;
+}
+
 int check_workspace(const void *ws, size_t ws_bytes, size_t need, size_t alignment) {
     if (need == 0) return WSL_OK;
     if (!ws) return WSL_E_NULL;

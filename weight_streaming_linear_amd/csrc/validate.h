@@ -52,11 +52,28 @@ int check_attn(const void *h_cache, const void *q, int qfmt, int64_t n_seq, int6
 int check_verify(const void *p, const void *q, int pfmt, int64_t n_seq, int64_t width, int64_t vocab, int64_t ld_p,
                  int64_t ld_q, const void *drafts, const void *n_drafts, const void *u, const void *accepted,
                  const void *tokens);
+// A wsl_kv_pages, then what a call is asked for.
+int check_kv_pages(const void *h_pages);
+int check_grow(const void *h_pages, const void *d_new, int64_t each, int64_t n_tokens, const void *slots,
+               const void *positions, const void *starts);
+int check_trim(const void *h_pages, const void *lens);
+int check_rotary(const void *q, int64_t n_heads, int64_t ld_q, const void *k, int64_t n_kv, int64_t ld_k, int xfmt,
+                 int64_t count, int64_t head_dim, int64_t rot_dim, const void *positions, const void *freqs,
+                 double amplitude, int flags, const void *q_out, int64_t ld_q_out, const void *k_out, int64_t ld_k_out,
+                 int ofmt);
+int check_sample(const void *logits, int zfmt, int64_t n_rows, int64_t vocab, int64_t ld, const void *h_settings,
+                 const void *u, const void *tokens, const void *probs, int64_t ld_probs);
+int check_lora(const void *a, const void *b, int64_t n_adapters, int64_t rank, int64_t n_out, int64_t k, const void *ids,
+               const void *scales, const void *x, int64_t m, int64_t ldx, const void *base, int64_t ld_base,
+               const void *out, int64_t ld_out, int fmt);
+bool lora_shape_ok(int64_t m, int64_t rank, int64_t k);
 // A workspace of ws_bytes at ws where need bytes are needed.
 int check_workspace(const void *ws, size_t ws_bytes, size_t need, size_t alignment);
 
 // Upper bound on any single dimension accepted by the library (keeps every
 // derived index within int64 and every per-row byte offset within int32).
 constexpr int64_t kMaxDim = int64_t(1) << 30;
+constexpr int64_t kMaxSampleVocab = int64_t(1) << 22;
+constexpr int64_t kMaxLoraDim = int64_t(1) << 22;
 
 }  // namespace wsl
