@@ -72,6 +72,21 @@ __device__ __forceinline__ double lanes_before(double v) {
     v = lanes_add<0x142, 0xa>(v);      // rows 1 and 3: the row before's last lane
     return lanes_add<0x143, 0xc>(v);   // rows 2 and 3: lane 31
 }
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t lanes_add(uint32_t v) {
+    return v + static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, ROWS, 0xf, false));
+}
+__device__ __forceinline__ uint32_t lanes_before(uint32_t v) {
+    v = lanes_add<0x111, 0xf>(v);
+    v = lanes_add<0x112, 0xf>(v);
+    v = lanes_add<0x114, 0xf>(v);
+    v = lanes_add<0x118, 0xf>(v);
+    v = lanes_add<0x142, 0xa>(v);
+    return lanes_add<0x143, 0xc>(v);
+}
+__device__ __forceinline__ uint32_t lane_value(uint32_t v, int lane) {
+    return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), lane));
+}
 __device__ __forceinline__ double lane_value(double v, int lane) {
     const uint64_t b = __builtin_bit_cast(uint64_t, v);
     const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(b), lane);

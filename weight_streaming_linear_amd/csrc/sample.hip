@@ -36,8 +36,26 @@ constexpr float kInf = __builtin_huge_valf();
 // What a part of a long row finds.
 struct PartHead {
     float m;                                   // its greatest entry
-    uint32_t tops, first;                      // how many are as great, and the first of them (greedy rows)
+    uint32_t first;                            // the first that is as great (greedy rows)
     uint32_t bad;
+    uint32_t at;                               // where its entries begin in the row's list
+};
+// Which cells' entries are needed one by one, and what is on.
+struct Plan {
+    int32_t k_on, p_on;
+    int32_t one, lo, hi, min;                  // cells: of top-k, from .. to of top-p, of min-p; -1: none
+    uint32_t n;                                // their entries
+    __device__ __forceinline__ bool wants(int c) const { return c == one || (c >= lo && c <= hi) || c == min; }
+};
+// Counts and weights of 256 cells (or ranges).
+struct Bins {
+    double w[kCells];
+    uint32_t count[kCells];
+};
+struct RowPlan {
+    Bins cells;
+    Plan plan;
+    uint32_t pad;
 };
 // What is decided of a long row, for the probabilities.
 struct RowOut {
@@ -60,6 +78,7 @@ struct SampleArgs {
     PartHead *heads;                           // [rows][parts]
     uint64_t *cells;                           // [rows][parts][kCells]: count in the upper 16 bits, sum
     uint64_t *list;                            // [rows][kGathered]
+    RowPlan *plans;                            // [rows]
     RowOut *outs;                              // [rows]
     int32_t parts, part;                       // of a row, and entries of one
 };
@@ -97,21 +116,29 @@ __device__ __forceinline__ double eighths(double n) {
     for (int e = 1; e < 8; ++e) r = (i & 7) == e ? kRoots[e] : r;
     return __builtin_ldexp(r, i >> 3);
 }
-// 2^(f / 8), |f| <= 1/2: the Taylor series of exp(f ln 2 / 8) to the TERMS-th power: 7, right to 2^-50, or
-// 5, to 2^-36 (and 1 for an f that is nearly 0: logits that a high temperature makes equal weigh the same).
-template <int TERMS>
+// 2^(f / 8), |f| <= 1/2: the Taylor series of exp(f ln 2 / 8) to the 7th power, right to 2^-50 (and 1 for an
+// f that is nearly 0: logits that a high temperature makes equal weigh the same).
+constexpr double kEighth = 0.08664339756999316;        // ln 2 / 8
 __device__ __forceinline__ double power(double f) {
-    const double x = f * 0.08664339756999316;
-    double r = 1.0 / 120;
-    if constexpr (TERMS == 7) {
-        r = __builtin_fma(1.0 / 5040, x, 1.0 / 720);
-        r = __builtin_fma(r, x, 1.0 / 120);
-    }
+    const double x = f * kEighth;
+    double r = __builtin_fma(1.0 / 5040, x, 1.0 / 720);
+    r = __builtin_fma(r, x, 1.0 / 120);
     r = __builtin_fma(r, x, 1.0 / 24);
     r = __builtin_fma(r, x, 1.0 / 6);
     r = __builtin_fma(r, x, 0.5);
     r = __builtin_fma(r, x, 1.0);
     return __builtin_fma(r, x, 1.0);
+}
+// The same to the 5th power (2^-36), as a whole number of 2^-32: the last sum is above 2^52, whose fraction
+// ends at 1, so its low bits are the number, rounded once.
+__device__ __forceinline__ uint64_t whole_power(double f) {
+    constexpr double k1 = kEighth * kPartUnit, k2 = kEighth * k1 / 2, k3 = kEighth * k2 / 3, k4 = kEighth * k3 / 4,
+                     k5 = kEighth * k4 / 5;
+    double r = __builtin_fma(k5, f, k4);
+    r = __builtin_fma(r, f, k3);
+    r = __builtin_fma(r, f, k2);
+    r = __builtin_fma(r, f, k1);
+    return __builtin_bit_cast(uint64_t, __builtin_fma(r, f, kPartUnit + 4503599627370496.0)) & 0x3ffffffffull;
 }
 
 __device__ __forceinline__ bool in_row(float z) { return z > -kInf; }
@@ -137,7 +164,7 @@ struct Scale {
     }
     __device__ __forceinline__ double weight(float z) const {
         const double v = c8 * (static_cast<double>(z) - m), n = __builtin_rint(v);
-        return power<7>(v - n) * eighths(n);
+        return power(v - n) * eighths(n);
     }
     // a power of two near the weights of a cell, and a weight as a whole number of 2^-40 of it
     static __device__ __forceinline__ double unit(int cell) { return __builtin_ldexp(1.0, -(cell >> 3)); }
@@ -146,11 +173,7 @@ struct Scale {
     }
 };
 
-// Counts and weights of 256 cells (or ranges), and where a count or a sum is reached.
-struct Bins {
-    double w[kCells];
-    uint32_t count[kCells];
-};
+// Where a count or a sum is reached.
 struct Border {
     int bin;
     uint32_t before, in;           // entries before the bin, and in it
@@ -169,9 +192,9 @@ __device__ __forceinline__ Border border_of(const Bins &b, bool by_count, uint32
         w[i] = b.w[lane * kMine + i];
         cs += c[i], ws += w[i];
     }
-    const double up_w = lanes_before(ws), up_c = lanes_before(static_cast<double>(cs));
+    const double up_w = lanes_before(ws);
     double at_w = up_w - ws;
-    uint32_t at_c = static_cast<uint32_t>(up_c) - cs;
+    uint32_t at_c = lanes_before(cs) - cs;
     int hit = -1, last = -1;
     uint32_t hit_c = 0, hit_in = 0, last_c = 0, last_in = 0;
     double hit_w = 0, last_w = 0;
@@ -198,6 +221,7 @@ struct Shared {
     Bins cells, bins;
     uint64_t sum[kCells];
     uint64_t list[kList], sorted[kList];
+    uint32_t rank[kList];
     uint64_t least[kMostWaves], most[kMostWaves];
     float top[kMostWaves];
     uint32_t n, bad;
@@ -310,12 +334,20 @@ __device__ uint64_t keep_from(const From &row, Shared &s, const Scale &sc, bool 
     });
     __syncthreads();
     const uint32_t n = s.n < kList ? s.n : kList;  // b.in
-    if (tid < n) {
-        const uint64_t mine = s.list[tid];
+    // an entry's place: as many threads as there are for each, a part of the list each
+    const uint32_t shares = blockDim.x / kList, entry = tid % kList, share = tid / kList;
+    if (tid < kList) s.rank[tid] = 0;
+    __syncthreads();
+    if (entry < n) {
+        const uint64_t mine = s.list[entry];
+        const uint32_t i0 = n * share / shares, i1 = n * (share + 1) / shares;
         uint32_t rank = 0;
-        for (uint32_t i = 0; i < n; ++i) rank += s.list[i] > mine ? 1u : 0u;
-        s.sorted[rank] = mine;
+#pragma unroll 8
+        for (uint32_t i = i0; i < i1; ++i) rank += s.list[i] > mine ? 1u : 0u;
+        atomicAdd(&s.rank[entry], rank);
     }
+    __syncthreads();
+    if (tid < n) s.sorted[s.rank[tid]] = s.list[tid];
     __syncthreads();
     // every wave: four successive entries a lane
     constexpr int kMine = kList / 64;
@@ -505,12 +537,13 @@ __global__ __launch_bounds__(kSmallWaves * 64) void sample_short_kernel(SampleAr
 }
 
 // ------------------------------------------------------------------ long rows
-// Cells of one part: blockIdx (part, row), a wave a segment.
+// Cells of one part: blockIdx (part, row), a wave a segment.  Bound by the 64-bit arithmetic, about 16
+// instructions an entry (an exponential in 32 bits would take as many and leave 2^-22 of a weight).
 template <int FMT>
 __global__ __launch_bounds__(kMostWaves * 64) void sample_cells_kernel(SampleArgs a) {
     __shared__ uint64_t cells[kCells];
     __shared__ float top[kMostWaves];
-    __shared__ uint32_t tops, first, bad;
+    __shared__ uint32_t first, bad;
     constexpr int kSize = FMT == WSL_OUT_F32 ? 4 : 2;
     const int64_t r = blockIdx.y;
     const uint32_t tid = threadIdx.x;
@@ -520,7 +553,7 @@ __global__ __launch_bounds__(kMostWaves * 64) void sample_cells_kernel(SampleArg
     float z[kEach];
     load_seg<FMT>(static_cast<const char *>(a.logits) + r * a.ld * kSize, j0, a.vocab, z, -kInf);
     const How h = how_of(a, r);
-    if (tid == 0) tops = 0, first = ~0u, bad = 0;
+    if (tid == 0) first = ~0u, bad = 0;
     if (tid < kCells) cells[tid] = 0;
     float m = -kInf;
     bool mine_bad = false;
@@ -541,41 +574,35 @@ __global__ __launch_bounds__(kMostWaves * 64) void sample_cells_kernel(SampleArg
 #pragma unroll
         for (int e = kEach - 1; e >= 0; --e) at = z[e] == m ? static_cast<uint32_t>(j0) + entry_of<FMT>(lane, e) : at;
         if (at != ~0u) atomicMin(&first, at);
-    } else {
+    } else if (in_row(m)) {
         const double n_m = __builtin_rint(h.c8 * static_cast<double>(m));
-        uint32_t equal = 0;
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
-            equal += static_cast<uint32_t>(__popcll(__ballot(z[e] == m && in_row(m))));
-            if (in_row(z[e])) {
-                const double y = h.c8 * static_cast<double>(z[e]), n = __builtin_rint(y), d = n_m - n;
-                const int c = static_cast<int>(d < kCells - 1 ? d : kCells - 1);
-                // 2^52 + x has x as the low bits of its fraction
-                double w = power<5>(y - n) * kPartUnit;
-                if (c == kCells - 1) w = static_cast<double>(exp2f(static_cast<float>(y - (n_m - (kCells - 1))) * 0.125f)) * kPartUnit;
-                w = z[e] == m ? 0.0 : w;
-                const uint64_t bits = __builtin_bit_cast(uint64_t, w + 4503599627370496.0);
-                atomicAdd(reinterpret_cast<unsigned long long *>(&cells[c]),
-                          static_cast<unsigned long long>((bits & 0xfffffffffffffull) + (1ull << 48)));
+            const double y = h.c8 * static_cast<double>(z[e]), n = __builtin_rint(y), d = n_m - n;
+            uint64_t v = whole_power(y - n) + (1ull << 48);
+            int c = static_cast<int>(d);
+            bool put = d < kCells - 1;
+            if (__ballot(!put)) {              // the last cell's entries count by how far they are behind it
+                if (!put) {
+                    c = kCells - 1, put = in_row(z[e]);
+                    const float w = exp2f(static_cast<float>(y - (n_m - (kCells - 1))) * 0.125f) * 4294967296.f;
+                    v = static_cast<uint64_t>(w) + (1ull << 48);
+                }
             }
+            if (put) atomicAdd(reinterpret_cast<unsigned long long *>(&cells[c]), static_cast<unsigned long long>(v));
         }
-        if (lane == 0 && equal) atomicAdd(&tops, equal);
     }
     __syncthreads();
     const int64_t at = r * a.parts + blockIdx.x;
     if (tid < kCells && !h.greedy) a.cells[at * kCells + tid] = cells[tid];
-    if (tid == 0) a.heads[at] = PartHead{m, tops, first, bad};
+    if (tid == 0) a.heads[at] = PartHead{m, first, bad, 0};
 }
 
 // A long row put together from its parts.
-struct Whole {
-    float m;
-    uint32_t bad, first;
-};
 struct LongShared {
     float m[kMostParts];
-    uint32_t tops[kMostParts];
-    int32_t shift[kMostParts];                     // cells that a part's lie below the row's
+    double below[kMostParts];                      // cells that a part's lie below the row's
+    int32_t shift[kMostParts];                     // the same, 255 at most
     double part_sum[kMostParts];
     uint32_t part_count[kMostParts];
     double w[kMostWaves / 4][kCells];
@@ -584,14 +611,18 @@ struct LongShared {
     uint32_t rest_count[kMostWaves];
     uint32_t bad, first;
 };
+struct Whole {
+    float m;
+    uint32_t bad, first;
+};
 
-__device__ __forceinline__ Whole heads_of(const SampleArgs &a, int64_t r, LongShared &s) {
+__device__ __forceinline__ Whole heads_of(const SampleArgs &a, int64_t r, double c8, LongShared &s) {
     const uint32_t tid = threadIdx.x;
     if (tid == 0) s.bad = 0, s.first = ~0u;
-    PartHead p = {-kInf, 0, ~0u, 0};
+    PartHead p = {-kInf, ~0u, 0, 0};
     if (tid < static_cast<uint32_t>(a.parts)) {
         p = a.heads[r * a.parts + tid];
-        s.m[tid] = p.m, s.tops[tid] = p.tops;
+        s.m[tid] = p.m;
     }
     __syncthreads();
     Whole o;
@@ -599,15 +630,20 @@ __device__ __forceinline__ Whole heads_of(const SampleArgs &a, int64_t r, LongSh
     for (int i = 0; i < a.parts; ++i) o.m = s.m[i] > o.m ? s.m[i] : o.m;
     if (p.bad) atomicOr(&s.bad, 1u);
     if (p.m == o.m && p.first != ~0u) atomicMin(&s.first, p.first);
+    if (tid < static_cast<uint32_t>(a.parts)) {
+        const double d = __builtin_rint(c8 * static_cast<double>(o.m)) - __builtin_rint(c8 * static_cast<double>(p.m));
+        s.below[tid] = d < 100000 ? d : 100000;    // (a part of -infinities, and infinite temperature: NaN)
+        s.shift[tid] = static_cast<int>(d < kCells - 1 ? d : kCells - 1);
+    }
     __syncthreads();
     o.bad = s.bad, o.first = s.first;
     return o;
 }
 
-// The weight of a part's whole number of 2^-32 in its cell c: 2^((rint(y of its greatest) - c - y_m) / 8).
-__device__ __forceinline__ double part_unit(const Scale &sc, float m, int c) {
-    const double n = __builtin_rint(sc.y(m)) - sc.n_m - c;
-    return eighths(n) * power<7>(sc.n_m - sc.y(static_cast<float>(sc.m))) / kPartUnit;
+// The sum of a cell's whole numbers as a weight: by the number of the greatest entry, which weighs 1.
+__device__ __forceinline__ double top_whole(const Scale &sc) {
+    const double y = sc.y(static_cast<float>(sc.m));
+    return static_cast<double>(whole_power(y - sc.n_m));
 }
 
 // The row's cells from its parts': groups of 256 threads take every so many parts, a thread a cell of the
@@ -615,15 +651,12 @@ __device__ __forceinline__ double part_unit(const Scale &sc, float m, int c) {
 __device__ __forceinline__ void put_together(const SampleArgs &a, int64_t r, const Scale &sc, LongShared &s, Bins &cells) {
     const uint32_t tid = threadIdx.x, cell = tid & (kCells - 1), group = tid / kCells, groups = blockDim.x / kCells;
     const int lane = static_cast<int>(tid & 63), wave = static_cast<int>(tid >> 6);
-    if (tid < static_cast<uint32_t>(a.parts)) {
-        const double d = sc.n_m - __builtin_rint(sc.y(s.m[tid]));      // a part of -infinities: infinite
-        s.shift[tid] = static_cast<int>(d < kCells - 1 ? d : kCells - 1);
-    }
-    __syncthreads();
     uint64_t sum = 0;
-    double w = 0, rest = 0;
+    double rest = 0;
     uint32_t count = 0, rest_count = 0;
     const uint64_t *mine = a.cells + r * a.parts * kCells;
+    const double whole = top_whole(sc);
+#pragma unroll 4
     for (int i = group; i < a.parts; i += groups) {
         const int shift = s.shift[i], from = static_cast<int>(cell) - shift;
         const bool here = from >= 0 && cell < kCells - 1, behind = static_cast<int>(cell) + shift >= kCells - 1;
@@ -631,20 +664,21 @@ __device__ __forceinline__ void put_together(const SampleArgs &a, int64_t r, con
         sum += v & 0xffffffffffffull;
         count += static_cast<uint32_t>(v >> 48);
         if (u) {
-            rest += static_cast<double>(u & 0xffffffffffffull) * part_unit(sc, s.m[i], cell);
+            rest += static_cast<double>(u & 0xffffffffffffull) / whole * eighths(-(s.below[i] + cell));
             rest_count += static_cast<uint32_t>(u >> 48);
         }
-        if (s.tops[i] && shift == static_cast<int>(cell)) w += s.tops[i] * sc.weight(s.m[i]);
     }
-    w += static_cast<double>(sum) * part_unit(sc, static_cast<float>(sc.m), cell);
+    const double unit = eighths(-static_cast<double>(cell));
     rest = lanes_total(rest);
-    rest_count = static_cast<uint32_t>(lanes_total(static_cast<double>(rest_count)));
-    s.w[group][cell] = w, s.count[group][cell] = count;
+    rest_count = lane_value(lanes_before(rest_count), 63);
+    s.w[group][cell] = static_cast<double>(sum), s.count[group][cell] = count;
     if (lane == 0) s.rest[wave] = rest, s.rest_count[wave] = rest_count;
     __syncthreads();
     if (tid < kCells) {
-        w = 0, count = 0;
+        double w = 0;
+        count = 0;
         for (uint32_t g = 0; g < groups; ++g) w += s.w[g][cell], count += s.count[g][cell];
+        w = w / whole * unit;
         if (cell == kCells - 1)
             for (uint32_t i = 0; i < groups * 4; ++i) w += s.rest[i], count += s.rest_count[i];
         cells.w[cell] = w, cells.count[cell] = count;
@@ -652,13 +686,6 @@ __device__ __forceinline__ void put_together(const SampleArgs &a, int64_t r, con
     __syncthreads();
 }
 
-// Which cells' entries are needed one by one, and what is on.
-struct Plan {
-    bool k_on, p_on;
-    int one, lo, hi, min;                          // cells: of top-k, from .. to of top-p, of min-p; -1: none
-    uint32_t n;                                    // their entries
-    __device__ __forceinline__ bool wants(int c) const { return c == one || (c >= lo && c <= hi) || c == min; }
-};
 __device__ __forceinline__ Plan plan_of(const Bins &cells, const Scale &sc, const How &h, double least) {
     const Border all = border_of(cells, true, ~0u, 0);
     Plan p;
@@ -668,10 +695,11 @@ __device__ __forceinline__ Plan plan_of(const Bins &cells, const Scale &sc, cons
     if (p.k_on) {
         const Border b = border_of(cells, true, h.k, 0);
         p.one = b.bin;
-        // between the lightest and the heaviest that (k - before) entries of the cell can be
-        const double some = static_cast<double>(h.k - b.before), unit = part_unit(sc, static_cast<float>(sc.m), b.bin) * kPartUnit;
-        least_w = b.w_before + (b.bin < kCells - 1 ? 0.957 * unit * some : 0.0);       // 2^(-1/16), and a little
-        most_w = b.w_before + 1.045 * unit * some;                                     // 2^(1/16)
+        // between the lightest and the heaviest that (k - before) entries of the cell can be: 2^(1/16) either way
+        // of its middle, which is as far from the greatest's, and a little
+        const double some = static_cast<double>(h.k - b.before), unit = eighths(-b.bin);
+        least_w = b.w_before + (b.bin < kCells - 1 ? 0.916 * unit * some : 0.0);
+        most_w = b.w_before + 1.091 * unit * some;
     }
     if (p.p_on) {
         p.lo = border_of(cells, false, 0, static_cast<double>(h.top_p) * least_w * (1 - 1e-6)).bin;
@@ -685,7 +713,7 @@ __device__ __forceinline__ Plan plan_of(const Bins &cells, const Scale &sc, cons
         else if (c <= (p.p_on ? p.hi : first)) p.min = c;
     }
     for (int i = static_cast<int>(threadIdx.x & 63); i < kCells; i += 64) p.n += p.wants(i) ? cells.count[i] : 0u;
-    p.n = static_cast<uint32_t>(lanes_total(static_cast<double>(p.n)));
+    p.n = lane_value(lanes_before(p.n), 63);
     return p;
 }
 
@@ -700,10 +728,15 @@ __device__ __forceinline__ void count_parts(const SampleArgs &a, int64_t r, cons
             const int c = e + lane + s.shift[i];
             if (p.wants(c < kCells - 1 ? c : kCells - 1)) n += static_cast<uint32_t>(a.cells[(r * a.parts + i) * kCells + e + lane] >> 48);
         }
-        n = static_cast<uint32_t>(lanes_total(static_cast<double>(n)));
+        n = lane_value(lanes_before(n), 63);
         if (lane == 0) s.part_count[i] = n;
     }
     __syncthreads();
+}
+
+// Whether a row's settings leave entries out (else its cells are all that is needed of it).
+__device__ __forceinline__ bool filters(const SampleArgs &a, const How &h) {
+    return h.k < a.vocab || h.top_p < 1 || h.log_min_p > -__builtin_huge_val();
 }
 
 // The entries of the border's cells, in an order that is the same on every run: blockIdx (part, row).
@@ -716,24 +749,47 @@ __global__ __launch_bounds__(kMostWaves * 64) void sample_border_kernel(SampleAr
     const int64_t r = blockIdx.y;
     const int lane = static_cast<int>(threadIdx.x & 63), wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
     const How h = how_of(a, r);
-    if (h.greedy || (h.k >= a.vocab && h.top_p >= 1 && h.log_min_p == -__builtin_huge_val())) return;
-    const Whole all = heads_of(a, r, s);
+    if (h.greedy || !filters(a, h)) return;
+    const Whole all = heads_of(a, r, h.c8, s);
     if (all.bad || !in_row(all.m)) return;
     const Scale sc(h.c8, all.m);
     put_together(a, r, sc, s, cells);
     const Plan p = plan_of(cells, sc, h, sc.y(all.m) + h.log_min_p);
-    if (p.n == 0 || p.n > kGathered) return;
-    count_parts(a, r, p, s);
-    if (s.part_count[blockIdx.x] == 0) return;
+    const bool fits = p.n > 0 && p.n <= kGathered;
+    if (fits) count_parts(a, r, p, s);
+    if (blockIdx.x == 0) {                         // for the next launch
+        RowPlan &out = a.plans[r];
+        for (uint32_t i = threadIdx.x; i < kCells; i += blockDim.x) out.cells.w[i] = cells.w[i], out.cells.count[i] = cells.count[i];
+        if (threadIdx.x == 0) out.plan = p;
+        if (fits && threadIdx.x < static_cast<uint32_t>(a.parts)) {
+            uint32_t at = 0;
+            for (uint32_t i = 0; i < threadIdx.x; ++i) at += s.part_count[i];
+            a.heads[r * a.parts + threadIdx.x].at = at;
+        }
+    }
+    if (!fits || s.part_count[blockIdx.x] == 0) return;
     const int64_t j0 = static_cast<int64_t>(blockIdx.x) * a.part + wave * kSeg;
     float z[kEach];
     load_seg<FMT>(static_cast<const char *>(a.logits) + r * a.ld * kSize, j0, a.vocab, z, -kInf);
+    // nearly all entries are outside of what the wanted cells span: looked at in 32 bits, with a margin
+    float low = -kInf, high = kInf;
+    if (h.c8 > 0) {
+        int c0 = p.min >= 0 ? p.min : kCells, c1 = p.min;
+        if (p.one >= 0) c0 = p.one < c0 ? p.one : c0, c1 = p.one > c1 ? p.one : c1;
+        if (p.hi >= 0) c0 = p.lo < c0 ? p.lo : c0, c1 = p.hi > c1 ? p.hi : c1;
+        const double to = (sc.n_m - c0 + 0.51) / h.c8, from = (sc.n_m - c1 - 0.51) / h.c8;
+        high = static_cast<float>(to + __builtin_fabs(to) * 1e-6);
+        if (c1 < kCells - 1) low = static_cast<float>(from - __builtin_fabs(from) * 1e-6);
+    }
     uint32_t mine = 0, n = 0;
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
-        const bool w = in_row(z[e]) && p.wants(sc.cell(sc.y(z[e])));
-        mine |= w ? 1u << e : 0u;
-        n += static_cast<uint32_t>(__popcll(__ballot(w)));
+        bool w = z[e] >= low && z[e] <= high;
+        if (__ballot(w)) {
+            w = w && in_row(z[e]) && p.wants(sc.cell(sc.y(z[e])));
+            mine |= w ? 1u << e : 0u;
+            n += static_cast<uint32_t>(__popcll(__ballot(w)));
+        }
     }
     if (lane == 0) found[wave] = n;
     __syncthreads();
@@ -746,9 +802,11 @@ __global__ __launch_bounds__(kMostWaves * 64) void sample_border_kernel(SampleAr
     for (int e = 0; e < kEach; ++e) {
         const bool w = mine >> e & 1u;
         const uint64_t who = __ballot(w);
-        const uint32_t to = at + static_cast<uint32_t>(__popcll(who & ((1ull << lane) - 1)));
-        if (w && to < kGathered) list[to] = order_of(z[e], static_cast<uint32_t>(j0) + entry_of<FMT>(lane, e));
-        at += static_cast<uint32_t>(__popcll(who));
+        if (who) {
+            const uint32_t to = at + static_cast<uint32_t>(__popcll(who & ((1ull << lane) - 1)));
+            if (w && to < kGathered) list[to] = order_of(z[e], static_cast<uint32_t>(j0) + entry_of<FMT>(lane, e));
+            at += static_cast<uint32_t>(__popcll(who));
+        }
     }
 }
 
@@ -763,8 +821,14 @@ __global__ __launch_bounds__(kMostWaves * 64) void sample_pick_kernel(SampleArgs
     const uint32_t tid = threadIdx.x;
     const int lane = static_cast<int>(tid & 63), wave = __builtin_amdgcn_readfirstlane(static_cast<int>(tid >> 6));
     const How h = how_of(a, r);
-    const Whole all = heads_of(a, r, s);
     const char *p_row = static_cast<const char *>(a.logits) + r * a.ld * kSize;
+    const bool some = !h.greedy && filters(a, h);
+    Plan p = {0, 0, -1, -1, -2, -1, 0};
+    if (some) {                                    // (read before it is known that there is anything to sample)
+        p = a.plans[r].plan;
+        if (tid < kCells) t.cells.w[tid] = a.plans[r].cells.w[tid], t.cells.count[tid] = a.plans[r].cells.count[tid];
+    }
+    const Whole all = heads_of(a, r, h.c8, s);
     if (all.bad || !in_row(all.m) || h.greedy) {
         const bool fine = !all.bad && in_row(all.m);
         if (tid == 0) {
@@ -775,13 +839,11 @@ __global__ __launch_bounds__(kMostWaves * 64) void sample_pick_kernel(SampleArgs
         return;
     }
     const Scale sc(h.c8, all.m);
-    put_together(a, r, sc, s, t.cells);
     const double least = sc.y(all.m) + h.log_min_p;
-    const Plan p = plan_of(t.cells, sc, h, least);
     const bool listed = p.n <= kGathered;
     uint64_t from = 0;
     int border = kCells;                           // the cell that is kept in part; those before it are whole
-    if (p.n) {
+    if (p.n && (p.k_on || p.p_on)) {
         Gathered g;
         const LongRow<FMT> row = {p_row, a.vocab};
 #pragma unroll
@@ -798,28 +860,26 @@ __global__ __launch_bounds__(kMostWaves * 64) void sample_pick_kernel(SampleArgs
         };
         double w_kept = 0, w_top;
         if (p.k_on) keep(true, 0, w_kept);
-        else if (p.p_on) w_kept = border_of(t.cells, true, ~0u, 0).w_all;
+        else w_kept = border_of(t.cells, true, ~0u, 0).w_all;
         if (p.p_on) keep(false, static_cast<double>(h.top_p) * w_kept, w_top);
-        count_parts(a, r, p, s);
     }
     if (p.min >= 0 && p.min < border) border = p.min;      // (which may hold nothing)
     const auto weight = [&](float z, uint64_t o) { return in_row(z) && o >= from && sc.y(z) >= least ? sc.weight(z) : 0.0; };
     // the kept weight of each part; a wave a part: whole cells, and entries of the border's
+    const double whole = top_whole(sc);
     for (int i = wave; i < a.parts; i += kMostWaves) {
         double w = 0;
 #pragma unroll
         for (int e = 0; e < kCells; e += 64) {
             const int c = e + lane, to = c + s.shift[i];
             if ((to < kCells - 1 ? to : kCells - 1) < border)
-                w += static_cast<double>(a.cells[(r * a.parts + i) * kCells + c] & 0xffffffffffffull) * part_unit(sc, s.m[i], c);
+                w += static_cast<double>(a.cells[(r * a.parts + i) * kCells + c] & 0xffffffffffffull) / whole * eighths(-(s.below[i] + c));
         }
-        if (lane == 0 && s.shift[i] < border && s.tops[i]) w += s.tops[i] * sc.weight(s.m[i]);
         if (border < kCells && p.n) {
             if (listed) {
-                uint32_t at = 0;
-                for (int q = 0; q < i; ++q) at += s.part_count[q];
-                for (uint32_t e = lane; e < s.part_count[i]; e += 64) {
-                    const uint64_t o = a.list[r * kGathered + at + e];
+                const uint32_t end = i + 1 < a.parts ? a.heads[r * a.parts + i + 1].at : p.n;
+                for (uint32_t at = a.heads[r * a.parts + i].at + lane; at < end; at += 64) {
+                    const uint64_t o = a.list[r * kGathered + at];
                     const float z = logit_of(o);
                     if (sc.cell(sc.y(z)) == border) w += weight(z, o);
                 }
@@ -915,7 +975,7 @@ Sizes sizes_of(int64_t vocab) {
     Sizes z;
     z.part = static_cast<int64_t>(waves_of(vocab)) * kSeg;
     z.parts = (vocab + z.part - 1) / z.part;
-    z.row = sizeof(RowOut) + static_cast<size_t>(z.parts) * (sizeof(PartHead) + kCells * sizeof(uint64_t)) + kGathered * sizeof(uint64_t);
+    z.row = sizeof(RowOut) + sizeof(RowPlan) + static_cast<size_t>(z.parts) * (sizeof(PartHead) + kCells * sizeof(uint64_t)) + kGathered * sizeof(uint64_t);
     return z;
 }
 
@@ -936,7 +996,8 @@ int launch_sample(const void *logits, int zfmt, int64_t n_rows, int64_t vocab, i
     a.parts = static_cast<int32_t>(z.parts), a.part = static_cast<int32_t>(z.part);
     a.cells = static_cast<uint64_t *>(ws);
     a.list = a.cells + n_rows * z.parts * kCells;
-    a.heads = reinterpret_cast<PartHead *>(a.list + n_rows * kGathered);
+    a.plans = reinterpret_cast<RowPlan *>(a.list + n_rows * kGathered);
+    a.heads = reinterpret_cast<PartHead *>(a.plans + n_rows);
     a.outs = reinterpret_cast<RowOut *>(a.heads + n_rows * z.parts);
     if (zfmt == WSL_OUT_F32) go<WSL_OUT_F32>(a, n_rows, s);
     else go<WSL_OUT_BF16>(a, n_rows, s);
