@@ -96,12 +96,12 @@ def test_sampling_refusals():
     for name in ("d_temperature", "d_top_k", "d_top_p", "d_min_p"):
         assert call(how=ctypes.byref(wsl.WslSampling(**{name: 4098}))) == ALIGN
     f = wsl.sample_logits_workspace_bytes
-    assert f(3, 32768) == 0 == f(0, 151937) == f(3, 0) == f(3, 1 << 23)
+    assert f(3, 8192) == 0 == f(0, 151937) == f(3, 0) == f(3, 1 << 23)
     need = f(3, 151937)
-    if need:
-        assert call(n=3, vocab=151937, ld=151937, ws=None) == NULL
-        assert call(n=3, vocab=151937, ld=151937, nb=need - 1) == RANGE
-        assert call(n=3, vocab=151937, ld=151937, ws=4104) == ALIGN
+    assert need > 0
+    assert call(n=3, vocab=151937, ld=151937, ws=None) == NULL
+    assert call(n=3, vocab=151937, ld=151937, nb=need - 1) == RANGE
+    assert call(n=3, vocab=151937, ld=151937, ws=4104) == ALIGN
 
 
 def test_lora_refusals():

@@ -522,10 +522,9 @@ def _new(shape, dtype, device, stream):
 
 
 def _like(t, dtype, stream):
-    """A new contiguous tensor of t's shape: half the time of torch.empty."""
-    import torch
+    """A new contiguous tensor of t's shape."""
     if stream is None:
-        return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
+        return _torch.empty_like(t, dtype=dtype, memory_format=_torch.contiguous_format)
     return _new(t.shape, dtype, t.device, stream)
 
 
@@ -758,10 +757,62 @@ def verify_drafts(p, q, drafts, u, n_drafts=None, accepted=None, tokens=None, wo
 
 
 # ---------------------------------------------------------------- pages, positions, sampling, adapters
-def _here(device):
-    """Refuse tensors of another GPU than the current one, whose streams the launches go to."""
-    if device.index != _device():
-        raise ValueError(f"tensors on {device}, the current device is {_device()}")
+# The checks below take what they need of a tensor once: its attributes cost a tenth to a quarter of a microsecond
+# each, and a launch three.  torch and its types are looked up at the first call (the module loads without torch).
+_torch = _bf16 = _f32 = _i32 = _i64 = None
+
+
+def _load_torch():
+    global _torch, _bf16, _f32, _i32, _i64
+    import torch
+    _bf16, _f32, _i32, _i64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+    _torch = torch
+    return torch
+
+
+def _here(t, name):
+    """The index of a tensor's GPU, which has to be the current one: its streams are where the launches go."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name}: expected a GPU tensor, got one on {t.device}")
+    if index != _device():
+        raise ValueError(f"{name}: on {t.device}, the current device is {_device()}")
+    return index
+
+
+def _exactly(t, name, dtype, index, shape):
+    """Check a contiguous tensor of one type and shape on one GPU."""
+    if t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous():
+        return
+    if t.get_device() != index:
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{index}")
+    _plain(t, name, dtype, t.device, shape)
+
+
+def _format_of(t, name):
+    """WSL_OUT_F32 or WSL_OUT_BF16 of a tensor."""
+    dtype = t.dtype
+    if dtype is _bf16:
+        return WSL_OUT_BF16
+    if dtype is _f32:
+        return WSL_OUT_F32
+    raise ValueError(f"{name}: dtype {dtype} is neither float32 nor bfloat16")
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _space(workspace, ws_bytes, index, like, stream):
+    """The (address, size) of a workspace, and the tensor that keeps it: a new one of ws_bytes unless given."""
+    if workspace is not None:
+        _require(workspace, "workspace", (workspace.dtype,), device=like.device, contiguous=True)
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    if not ws_bytes:
+        return None, 0, None
+    workspace = _torch.empty(ws_bytes, dtype=_torch.uint8, device=index) if stream is None else \
+        _new(ws_bytes, _torch.uint8, like.device, stream)
+    return workspace.data_ptr(), ws_bytes, workspace
 
 
 class WslKvPages(ctypes.Structure):
@@ -795,7 +846,7 @@ class KVPages:
         if int(page_size) < 1 or per < 1 or free.numel() < 1:
             raise ValueError(f"page_size {page_size}, rows of {per} entries, {free.numel()} pages")
         self.table, self.lens, self.free, self.n_free = table, lens, free, n_free
-        self.device, self.n_seq, self.page_size = dev, n_seq, int(page_size)
+        self.device, self.index, self.n_seq, self.page_size = dev, dev.index, n_seq, int(page_size)
         self.desc = WslKvPages(table.data_ptr(), lens.data_ptr(), free.data_ptr(), n_free.data_ptr(), n_seq, per, ld,
                                free.numel(), self.page_size)
         self.ref = ctypes.byref(self.desc)
@@ -822,15 +873,16 @@ def kv_pages_grow(pages, new, n_tokens=None, slots=None, positions=None, starts=
 
     new: one number for all sequences, or int32 [n_seq] (then give n_tokens, the room for their sum);
     starts: int32 [n_seq + 1] to be written with where each sequence's tokens begin."""
-    import torch
-    dev, n_seq = pages.device, pages.n_seq
-    _here(dev)
+    torch = _torch or _load_torch()
+    index, n_seq = pages.index, pages.n_seq
+    if index != _device():
+        _here(pages.lens, "pages")
     if isinstance(new, int):
         want, each = None, new
         if n_tokens is None:
             n_tokens = n_seq * new if slots is None else slots.numel()
     else:
-        _plain(new, "new", torch.int32, dev, (n_seq,))
+        _exactly(new, "new", _i32, index, (n_seq,))
         want, each = new.data_ptr(), 0
         if n_tokens is None:
             if slots is None:
@@ -838,30 +890,23 @@ def kv_pages_grow(pages, new, n_tokens=None, slots=None, positions=None, starts=
             n_tokens = slots.numel()
     if n_tokens < 0:
         raise ValueError(f"{n_tokens} tokens")
-    if slots is None and positions is None:
-        if stream is None:
-            slots = torch.empty(n_tokens, dtype=torch.int64, device=dev)
-            positions = torch.empty_like(slots)
-        else:
-            slots, positions = (_new(n_tokens, torch.int64, dev, stream) for _ in range(2))
+    if slots is None:
+        slots = torch.empty(n_tokens, dtype=_i64, device=index) if stream is None else \
+            _new(n_tokens, _i64, pages.device, stream)
     else:
-        slots = _new((n_tokens,), torch.int64, dev, stream) if slots is None else slots
-        positions = _new((n_tokens,), torch.int64, dev, stream) if positions is None else positions
-        _plain(slots, "slots", torch.int64, dev, (n_tokens,))
-        _plain(positions, "positions", torch.int64, dev, (n_tokens,))
+        _exactly(slots, "slots", _i64, index, (n_tokens,))
+    if positions is None:
+        positions = _like(slots, _i64, stream)
+    else:
+        _exactly(positions, "positions", _i64, index, (n_tokens,))
     if starts is not None:
-        _plain(starts, "starts", torch.int32, dev, (n_seq + 1,))
+        _exactly(starts, "starts", _i32, index, (n_seq + 1,))
     if status is not None:
-        _status(status, dev)
-    if workspace is None:
-        ws_bytes = kv_pages_grow_workspace_bytes(n_seq, n_tokens)
-        if ws_bytes:
-            workspace = _new(ws_bytes, torch.uint8, dev, stream)
-    else:
-        _require(workspace, "workspace", (workspace.dtype,), device=dev, contiguous=True)
-        ws_bytes = workspace.numel() * workspace.element_size()
-    rc = lib().kv_pages_grow(pages.ref, want, each, n_tokens, slots.data_ptr(), positions.data_ptr(), _ptr(starts),
-                             _ptr(workspace), ws_bytes, _ptr(status), _stream(stream))
+        _status(status, pages.device)
+    ws, ws_bytes, workspace = _space(workspace, kv_pages_grow_workspace_bytes(n_seq, n_tokens) if workspace is None else 0,
+                                     index, pages.lens, stream)
+    rc = lib().kv_pages_grow(pages.ref, want, each, n_tokens, slots.data_ptr(), positions.data_ptr(), _at(starts), ws,
+                             ws_bytes, _at(status), _stream(stream))
     if rc:
         _check(rc, "kv_pages_grow")
     return slots, positions
@@ -870,12 +915,15 @@ def kv_pages_grow(pages, new, n_tokens=None, slots=None, positions=None, starts=
 def kv_pages_trim(pages, lens, status=None, stream=None):
     """Shorten the sequences of a KVPages to lens (int32 [n_seq]; one at or above a sequence's own length
     leaves it) and give the pages behind them back."""
-    import torch
-    _here(pages.device)
-    _plain(lens, "lens", torch.int32, pages.device, (pages.n_seq,))
+    if _torch is None:
+        _load_torch()
+    index = pages.index
+    if index != _device():
+        _here(pages.lens, "pages")
+    _exactly(lens, "lens", _i32, index, (pages.n_seq,))
     if status is not None:
         _status(status, pages.device)
-    rc = lib().kv_pages_trim(pages.ref, lens.data_ptr(), _ptr(status), _stream(stream))
+    rc = lib().kv_pages_trim(pages.ref, lens.data_ptr(), _at(status), _stream(stream))
     if rc:
         _check(rc, "kv_pages_trim")
 
@@ -921,56 +969,56 @@ def rotary_embed(q, positions, freqs, k=None, interleaved=False, amplitude=1.0, 
     serve), fp32 or bf16; positions: int64 [count] or [n_seq][q_len]; freqs: float64 [rot_dim / 2]
     (rotary_freqs), the rest of a head is copied; interleaved: pairs lie side by side instead of half
     a rotation apart; amplitude: a factor of the turned elements; out, k_out may be q and k."""
-    import torch
-    dev = q.device
-    shape = tuple(q.shape)
-    if len(shape) not in (3, 4):
-        raise ValueError(f"q: expected 3 or 4 dimensions, got shape {shape}")
-    if not q.is_cuda:
-        raise ValueError(f"q: expected a GPU tensor, got one on {dev}")
-    _here(dev)
-    xfmt = _float_format(q, "q")
-    ld_q = _head_rows(q, "q", dev, shape)
-    count = shape[0] if len(shape) == 3 else shape[0] * shape[1]
-    if positions.numel() != count or positions.dtype is not torch.int64 or positions.device != dev or \
+    if _torch is None:
+        _load_torch()
+    index, shape = _here(q, "q"), q.shape
+    if len(shape) == 3:
+        count, heads, dim = shape
+    elif len(shape) == 4:
+        count, heads, dim = shape[0] * shape[1], shape[2], shape[3]
+    else:
+        raise ValueError(f"q: expected 3 or 4 dimensions, got shape {tuple(shape)}")
+    xfmt = _format_of(q, "q")
+    ld_q = heads * dim if q.is_contiguous() else _head_rows(q, "q", q.device, tuple(shape))
+    if positions.dtype is not _i64 or positions.get_device() != index or positions.numel() != count or \
             not positions.is_contiguous():
-        _require(positions, "positions", (torch.int64,), device=dev, contiguous=True)
+        _require(positions, "positions", (_i64,), device=q.device, contiguous=True)
         raise ValueError(f"positions: shape {tuple(positions.shape)}, {count} tokens")
-    if freqs.dtype is not torch.float64 or freqs.device != dev or freqs.dim() != 1 or not freqs.is_contiguous():
-        _require(freqs, "freqs", (torch.float64,), device=dev, contiguous=True, ndim=1)
+    if freqs.dtype is not _torch.float64 or freqs.get_device() != index or freqs.dim() != 1 or not freqs.is_contiguous():
+        _require(freqs, "freqs", (_torch.float64,), device=q.device, contiguous=True, ndim=1)
     if ofmt is None:
-        ofmt = xfmt if out is None else _float_format(out, "out")
-    dtype = _float_dtype(ofmt)
-    heads, dim = shape[-2:]
+        ofmt = xfmt if out is None else _format_of(out, "out")
+    elif ofmt != WSL_OUT_BF16 and ofmt != WSL_OUT_F32:
+        raise ValueError(f"unknown element format {ofmt}")
+    dtype = _bf16 if ofmt == WSL_OUT_BF16 else _f32
     if out is None:
-        out = _like(q, dtype, stream)
-        ld_out = heads * dim
+        out, ld_out = _like(q, dtype, stream), heads * dim
     else:
         if out.dtype is not dtype:
             raise ValueError(f"out: dtype {out.dtype}, expected {dtype}")
-        ld_out = _head_rows(out, "out", dev, shape)
+        ld_out = _head_rows(out, "out", q.device, tuple(shape))
     n_kv = ld_k = ld_ko = 0
     if k is not None:
+        k_shape = k.shape
+        n_kv = k_shape[-2]
         if k.dtype is not q.dtype:
             raise ValueError(f"k: dtype {k.dtype}, q has {q.dtype}")
-        if k.dim() != len(shape):
-            raise ValueError(f"k: shape {tuple(k.shape)}, q has {shape}")
-        n_kv = k.shape[-2]
-        k_shape = shape[:-2] + (n_kv, dim)
-        ld_k = _head_rows(k, "k", dev, k_shape)
+        if k.get_device() == index and k.is_contiguous() and len(k_shape) == len(shape) and k_shape[-1] == dim and \
+                k_shape[0] == shape[0] and (len(shape) == 3 or k_shape[1] == shape[1]):
+            ld_k = n_kv * dim
+        else:
+            ld_k = _head_rows(k, "k", q.device, (*shape[:-2], n_kv, dim))
         if k_out is None:
-            k_out = _like(k, dtype, stream)
-            ld_ko = n_kv * dim
+            k_out, ld_ko = _like(k, dtype, stream), n_kv * dim
         else:
             if k_out.dtype is not dtype:
                 raise ValueError(f"k_out: dtype {k_out.dtype}, expected {dtype}")
-            ld_ko = _head_rows(k_out, "k_out", dev, k_shape)
+            ld_ko = _head_rows(k_out, "k_out", q.device, tuple(k_shape))
     elif k_out is not None:
         raise ValueError("k_out without k")
-    rc = lib().rotary_embed(q.data_ptr(), heads, ld_q, _ptr(k), n_kv, ld_k, xfmt, count, dim, 2 * freqs.numel(),
-                            positions.data_ptr(), freqs.data_ptr(), float(amplitude),
-                            WSL_ROTARY_INTERLEAVED if interleaved else 0, out.data_ptr(), ld_out, _ptr(k_out), ld_ko, ofmt,
-                            _stream(stream))
+    rc = lib().rotary_embed(q.data_ptr(), heads, ld_q, _at(k), n_kv, ld_k, xfmt, count, dim, 2 * freqs.numel(),
+                            positions.data_ptr(), freqs.data_ptr(), amplitude, 1 if interleaved else 0, out.data_ptr(), ld_out,
+                            _at(k_out), ld_ko, ofmt, _stream(stream))
     if rc:
         _check(rc, "rotary_embed")
     return out if k is None else (out, k_out)
@@ -1008,47 +1056,55 @@ def sample_logits(logits, u=None, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0
     the greatest entry, top_k 0, top_p 1 and min_p 0 are off.  probs: fp32 [n][vocab] to be written with
     the distribution that is sampled (what verify_drafts takes).  Without u nothing is sampled, and probs
     (a new tensor unless given) is returned."""
-    import torch
-    if logits.dim() != 2 or not logits.is_cuda:
-        raise ValueError(f"logits: expected a GPU tensor of 2 dimensions, got shape {tuple(logits.shape)} on {logits.device}")
-    n, vocab = logits.shape
-    dev = logits.device
-    _here(dev)
-    zfmt = _float_format(logits, "logits")
-    ld, ld_probs = _logit_rows(logits, "logits", n), 0
+    torch = _torch or _load_torch()
+    index = _here(logits, "logits")
+    shape = logits.shape
+    if len(shape) != 2:
+        raise ValueError(f"logits: expected 2 dimensions, got shape {tuple(shape)}")
+    n, vocab = shape
+    zfmt = _format_of(logits, "logits")
+    ld, ld_probs = vocab if logits.is_contiguous() else _logit_rows(logits, "logits", n), 0
     how = WslSampling()
-    for name, value, dtype in (("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
-                               ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
-        if isinstance(value, torch.Tensor):
-            _plain(value, name, dtype, dev, (n,))
-            setattr(how, "d_" + name, value.data_ptr())
-        else:
-            setattr(how, name, value)
+    if isinstance(temperature, torch.Tensor):
+        _exactly(temperature, "temperature", _f32, index, (n,))
+        how.d_temperature = temperature.data_ptr()
+    else:
+        how.temperature = temperature
+    if isinstance(top_k, torch.Tensor):
+        _exactly(top_k, "top_k", _i32, index, (n,))
+        how.d_top_k = top_k.data_ptr()
+    else:
+        how.top_k = min(max(int(top_k), 0), 0x7fffffff)
+    if isinstance(top_p, torch.Tensor):
+        _exactly(top_p, "top_p", _f32, index, (n,))
+        how.d_top_p = top_p.data_ptr()
+    else:
+        how.top_p = top_p
+    if isinstance(min_p, torch.Tensor):
+        _exactly(min_p, "min_p", _f32, index, (n,))
+        how.d_min_p = min_p.data_ptr()
+    else:
+        how.min_p = min_p
     if u is not None:
-        _plain(u, "u", torch.float32, dev, (n,))
+        _exactly(u, "u", _f32, index, (n,))
         if tokens is None:
-            tokens = _like(u, torch.int32, stream)
+            tokens = _like(u, _i32, stream)
         else:
-            _plain(tokens, "tokens", torch.int32, dev, (n,))
+            _exactly(tokens, "tokens", _i32, index, (n,))
     elif tokens is not None:
         raise ValueError("tokens without u")
     elif probs is None:
-        probs = _new((n, vocab), torch.float32, dev, stream)
+        probs = _like(logits, _f32, stream)
     if probs is not None:
-        if probs.dtype is not torch.float32 or probs.device != dev or probs.shape != logits.shape:
-            raise ValueError(f"probs: {probs.dtype} {tuple(probs.shape)} on {probs.device}, expected float32 {tuple(logits.shape)}")
+        if probs.dtype is not _f32 or probs.get_device() != index or probs.shape != shape:
+            raise ValueError(f"probs: {probs.dtype} {tuple(probs.shape)} on {probs.device}, expected float32 {tuple(shape)}")
         ld_probs = _logit_rows(probs, "probs", n)
     if status is not None:
-        _status(status, dev)
-    if workspace is None:
-        ws_bytes = sample_logits_workspace_bytes(n, vocab)
-        if ws_bytes:
-            workspace = _new(ws_bytes, torch.uint8, dev, stream)
-    else:
-        _require(workspace, "workspace", (workspace.dtype,), device=dev, contiguous=True)
-        ws_bytes = workspace.numel() * workspace.element_size()
-    rc = lib().sample_logits(logits.data_ptr(), zfmt, n, vocab, ld, ctypes.byref(how), _ptr(u), _ptr(tokens), _ptr(probs),
-                             ld_probs, _ptr(workspace), ws_bytes, _ptr(status), _stream(stream))
+        _status(status, logits.device)
+    ws, ws_bytes, workspace = _space(workspace, sample_logits_workspace_bytes(n, vocab) if workspace is None else 0, index,
+                                     logits, stream)
+    rc = lib().sample_logits(logits.data_ptr(), zfmt, n, vocab, ld, ctypes.byref(how), _at(u), _at(tokens), _at(probs),
+                             ld_probs, ws, ws_bytes, _at(status), _stream(stream))
     if rc:
         _check(rc, "sample_logits")
     return probs if u is None else tokens
@@ -1072,43 +1128,36 @@ def lora_add(base, x, a, b, ids, scales=None, out=None, workspace=None, status=N
     base: [m][n_out], fp32 or bf16 (a linear layer's output); x: bf16 [m][k] (its input); a: bf16
     [n_adapters][rank][k]; b: bf16 [n_adapters][n_out][rank]; ids: int32 [m]; scales: fp32 [n_adapters], 1
     unless given; out: a new tensor unless given, and may be base."""
-    import torch
-    if a.dim() != 3 or x.dim() != 2 or base.dim() != 2:
-        raise ValueError(f"a, x, base: shapes {tuple(a.shape)}, {tuple(x.shape)}, {tuple(base.shape)}")
-    dev = base.device
-    if not base.is_cuda:
-        raise ValueError(f"base: expected a GPU tensor, got one on {dev}")
-    _here(dev)
-    fmt = _float_format(base, "base")
-    n_adapters, rank, k = a.shape
-    m, n_out = base.shape
-    if x.dtype is not torch.bfloat16 or x.device != dev:
-        raise ValueError(f"x: {x.dtype} on {x.device}, expected bfloat16 on {dev}")
-    ld_base, ldx = _token_rows(base, "base", m, n_out), _token_rows(x, "x", m, k)
-    _plain(a, "a", torch.bfloat16, dev, (n_adapters, rank, k))
-    _plain(b, "b", torch.bfloat16, dev, (n_adapters, n_out, rank))
-    _plain(ids, "ids", torch.int32, dev, (m,))
+    if _torch is None:
+        _load_torch()
+    index, shape, pool = _here(base, "base"), base.shape, a.shape
+    if len(pool) != 3 or len(shape) != 2:
+        raise ValueError(f"base, a: shapes {tuple(shape)}, {tuple(pool)}")
+    m, n_out = shape
+    n_adapters, rank, k = pool
+    fmt = _format_of(base, "base")
+    if x.dtype is not _bf16 or x.get_device() != index:
+        raise ValueError(f"x: {x.dtype} on {x.device}, expected bfloat16 on cuda:{index}")
+    ld_base = n_out if base.is_contiguous() else _token_rows(base, "base", m, n_out)
+    ldx = _token_rows(x, "x", m, k)
+    _exactly(a, "a", _bf16, index, pool)
+    _exactly(b, "b", _bf16, index, (n_adapters, n_out, rank))
+    _exactly(ids, "ids", _i32, index, (m,))
     if scales is not None:
-        _plain(scales, "scales", torch.float32, dev, (n_adapters,))
+        _exactly(scales, "scales", _f32, index, (n_adapters,))
     if out is None:
-        out = _like(base, base.dtype, stream)
-        ld_out = n_out
+        out, ld_out = _like(base, base.dtype, stream), n_out
     else:
-        if out.dtype is not base.dtype or out.device != dev:
-            raise ValueError(f"out: {out.dtype} on {out.device}, expected {base.dtype} on {dev}")
+        if out.dtype is not base.dtype or out.get_device() != index:
+            raise ValueError(f"out: {out.dtype} on {out.device}, expected {base.dtype} on cuda:{index}")
         ld_out = _token_rows(out, "out", m, n_out)
     if status is not None:
-        _status(status, dev)
-    if workspace is None:
-        ws_bytes = lora_add_workspace_bytes(m, rank, k)
-        if ws_bytes:
-            workspace = _new(ws_bytes, torch.uint8, dev, stream)
-    else:
-        _require(workspace, "workspace", (workspace.dtype,), device=dev, contiguous=True)
-        ws_bytes = workspace.numel() * workspace.element_size()
-    rc = lib().lora_add(a.data_ptr(), b.data_ptr(), n_adapters, rank, n_out, k, ids.data_ptr(), _ptr(scales), x.data_ptr(),
-                        m, ldx, base.data_ptr(), ld_base, out.data_ptr(), ld_out, fmt, _ptr(workspace), ws_bytes,
-                        _ptr(status), _stream(stream))
+        _status(status, base.device)
+    ws, ws_bytes, workspace = _space(workspace, lora_add_workspace_bytes(m, rank, k) if workspace is None else 0, index, base,
+                                     stream)
+    rc = lib().lora_add(a.data_ptr(), b.data_ptr(), n_adapters, rank, n_out, k, ids.data_ptr(), _at(scales), x.data_ptr(),
+                        m, ldx, base.data_ptr(), ld_base, out.data_ptr(), ld_out, fmt, ws, ws_bytes, _at(status),
+                        _stream(stream))
     if rc:
         _check(rc, "lora_add")
     return out
