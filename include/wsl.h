@@ -617,7 +617,7 @@ int sample_logits(const void *d_logits, int zfmt, int64_t n_rows, int64_t vocab,
  * n_adapters 1 .. 2^20.   rank 8 .. 128, a multiple of 8.   n_out 1 .. 2^22.   k 8 .. 2^22, a multiple of 8.
  * d_ids     device int32 [m].  One outside [-1, n_adapters) counts as -1 (WSL_STATUS_INDEX).
  * d_scales  device fp32 [n_adapters], or NULL: 1.
- * d_x       device bf16 [m][ldx], 16-byte aligned, ldx a multiple of 8.   m 0 .. 2^24 (0 launches nothing).
+ * d_x       device bf16 [m][ldx], 16-byte aligned, ldx a multiple of 8.   m 0 .. 2^20 (0 launches nothing).
  * d_base    device [m][ld_base] of fmt (WSL_OUT_F32 or WSL_OUT_BF16), aligned to its element.
  * d_out     device [m][ld_out] of fmt; may be d_base itself (with the same ld), no other overlap.
  * A x is summed in fp32 and scaled there; its product with B too.  (On the matrix cores A x enters as

@@ -38,7 +38,9 @@ def _check(base, x, a, b, ids, scales, out):
 @pytest.mark.parametrize("m,k,n_out,rank,count,pad", [
     (1, 8, 1, 8, 1, 0), (1, 512, 640, 16, 3, 0), (5, 520, 333, 24, 2, 1), (48, 1024, 257, 32, 40, 0), (3, 4096, 100, 64, 2, 3),
     (64, 136, 700, 128, 5, 0), (65, 136, 700, 128, 5, 0), (17, 2000, 515, 40, 3, 1), (66, 1000, 333, 8, 70, 1),
-    (130, 512, 1040, 16, 3, 0), (200, 2056, 64, 56, 4, 0), (300, 768, 130, 32, 1, 2), (100, 1536, 515, 104, 9, 0)])
+    (130, 512, 1040, 16, 3, 0), (200, 2056, 64, 56, 4, 0), (300, 768, 130, 32, 1, 2), (100, 1536, 515, 104, 9, 0),
+    (1100, 264, 130, 8, 3, 0), (520, 512, 1040, 16, 3, 0), (530, 2056, 70, 16, 70, 1), (700, 1544, 129, 24, 4, 0),
+    (130, 640, 200, 64, 3, 0), (70, 1160, 333, 128, 2, 4)])
 def test_against_the_formula(m, k, n_out, rank, count, pad, dtype):
     say(f"lora m={m} k={k} n_out={n_out} rank={rank} count={count} pad={pad} {dtype}")
     base, x, a, b, ids, scales = _case(m + k, m, k, n_out, rank, count, dtype, pad)
@@ -51,7 +53,7 @@ def test_against_the_formula(m, k, n_out, rank, count, pad, dtype):
     assert same is base and base.equal(out)
 
 
-@pytest.mark.parametrize("m", [4, 64, 65, 200])
+@pytest.mark.parametrize("m", [4, 64, 65, 200, 1100])
 @pytest.mark.parametrize("rank,n_out", [(8, 80), (16, 128), (40, 129), (128, 64)])
 def test_whole_numbers_are_exact(m, rank, n_out):
     """Small whole numbers: every sum is one that fp32 holds, so the result is equal.  A x runs up to
@@ -72,7 +74,7 @@ def test_whole_numbers_are_exact(m, rank, n_out):
     assert (f32_of(out) == want).all()
 
 
-@pytest.mark.parametrize("m", [9, 70, 200])
+@pytest.mark.parametrize("m", [9, 70, 200, 600])
 def test_an_adapter_has_no_part_in_other_rows(m):
     """Adapters full of NaN and infinities, rows of x too: rows of other adapters and of none are as
     if they were not there."""
@@ -94,7 +96,7 @@ def test_an_adapter_has_no_part_in_other_rows(m):
     assert out[none].view(torch.int32).equal(base[none].view(torch.int32))
 
 
-@pytest.mark.parametrize("m", [5, 90])
+@pytest.mark.parametrize("m", [5, 90, 1100])
 def test_bad_ids_are_reported_and_left_out(m):
     import torch
     base, x, a, b, ids, scales = _case(7, m, 256, 96, 8, 3, "bfloat16")
@@ -109,7 +111,7 @@ def test_bad_ids_are_reported_and_left_out(m):
         _check(base, x, a, b, ids, scales, out)
 
 
-@pytest.mark.parametrize("m", [12, 150])
+@pytest.mark.parametrize("m", [12, 150, 600])
 def test_beside_a_packed_projection(m):
     """linear_gemm's output and its adapters in place, as a layer runs them, replayed from a graph with a
     poisoned workspace."""

@@ -113,7 +113,7 @@ def test_lora_refusals():
 
     assert call(m=0, a=None, x=None, out=None) == OK
     assert call(fmt=2) == FORMAT
-    for bad in (dict(m=-1), dict(m=(1 << 24) + 1), dict(rank=0), dict(rank=12), dict(rank=136), dict(k=0), dict(k=60), dict(k=1 << 23, ldx=1 << 23),
+    for bad in (dict(m=-1), dict(m=(1 << 20) + 1), dict(rank=0), dict(rank=12), dict(rank=136), dict(k=0), dict(k=60), dict(k=1 << 23, ldx=1 << 23),
                 dict(n_out=0), dict(n_out=(1 << 22) + 1, ld_b=1 << 23, ld_o=1 << 23), dict(count=0), dict(count=(1 << 20) + 1),
                 dict(ldx=56), dict(ld_b=99), dict(ld_o=99), dict(ldx=1 << 62), dict(ld_b=1 << 62), dict(ld_o=1 << 62)):
         assert call(**bad) == SHAPE, bad

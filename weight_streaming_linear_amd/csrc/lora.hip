@@ -14,9 +14,15 @@
 namespace wsl {
 namespace {
 
-constexpr int64_t kFewTokens = 64;
+// Tokens one by one up to here.  That costs the same whatever their adapters; tiles of 16 cost by the adapters among
+// them.  5120 to 5120, one against the other, in us: tokens with adapters of their own, rank 16: 14 and 61 for 128, 28 and
+// 63 for 512, 45 and 83 for 1024; requests of 200 tokens: 11 and 13, 24 and 17, 43 and 26.  Rank 64: 32 and 72 for 128, 46 and
+// 70 for 256; requests: 26 and 23, 42 and 29.
+constexpr int64_t kFewRows = 8192;         // m * rank
+bool few(int64_t m, int64_t rank) { return m * rank <= kFewRows; }
 constexpr int kPart = 512;                 // least elements of k in a part
 constexpr int64_t kMostParts = 16;
+constexpr int64_t kGroups = 512;           // workgroups of 16 tokens that keep the chip busy
 
 struct LoraArgs {
     const uint16_t *a, *b, *x;
@@ -133,43 +139,100 @@ __global__ __launch_bounds__(256) void expand_few_kernel(LoraArgs a) {
 // ------------------------------------------------------------------ more tokens
 __device__ __forceinline__ bf16x8 frag(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
 
-// blockIdx: (64 tokens, part of k); a wave's 16 tokens are the rows, 16 rows of A the columns.
-template <int BLOCKS>
-__global__ __launch_bounds__(256) void shrink_many_kernel(LoraArgs a) {
+// blockIdx: (16 tokens, part of k).  The tokens are the rows, 16 rows of A the columns; the waves take 128
+// elements of k in turn, all of their loads made before the first product, and are added up in LDS, so that x is
+// read in long pieces and one part is enough where tokens are many.
+template <int BLOCKS, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void shrink_many_kernel(LoraArgs a) {
+    __shared__ f32x4 sums[WAVES][BLOCKS][64];
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
-    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * 64 + wave * 16;
-    if (t0 >= a.m) return;
-    const int64_t mine = t0 + col < a.m ? t0 + col : a.m - 1;
-    const int32_t id = t0 + col < a.m ? adapter_of(a, mine, blockIdx.y == 0 && g == 0) : -1;
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * 16;
+    const bool there = t0 + col < a.m;
+    const int64_t mine = there ? t0 + col : a.m - 1;
+    const int32_t id = there ? adapter_of(a, mine, blockIdx.y == 0 && tid < 16) : -1;
     const int64_t k0 = blockIdx.y * a.part, k1 = k0 + a.part < a.k ? k0 + a.part : a.k;
-    const uint16_t *x = a.x + mine * a.ldx;
+    const uint16_t *x = a.x + mine * a.ldx + g * 8;
     uint32_t todo = static_cast<uint32_t>(__ballot(id >= 0)) & 0xffffu;
     while (todo) {
-        const int32_t which = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
-        const uint32_t same = static_cast<uint32_t>(__ballot(id == which)) & 0xffffu;
-        todo &= ~same;
-        const uint16_t *w = a.a + static_cast<int64_t>(which) * a.rank * a.k;
-        f32x4 acc[BLOCKS];
+        // two adapters at a time: most tiles where requests meet have two
+        int32_t which[2];
+        uint32_t same[2] = {0, 0};
 #pragma unroll
-        for (int b = 0; b < BLOCKS; ++b) acc[b] = f32x4{0, 0, 0, 0};
-#pragma unroll 4
-        for (int64_t kk = k0; kk < k1; kk += 32) {
-            const int64_t at = kk + g * 8;
-            u32x4 xv = {0, 0, 0, 0};
-            if (at < k1) xv = *reinterpret_cast<const u32x4 *>(x + at);
-#pragma unroll
-            for (int b = 0; b < BLOCKS; ++b) {
-                u32x4 wv = {0, 0, 0, 0};
-                if (at < k1 && 16 * b + col < a.rank) wv = *reinterpret_cast<const u32x4 *>(w + (16 * b + col) * a.k + at);
-                acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(xv), frag(wv), acc[b], 0, 0, 0);
+        for (int p = 0; p < 2; ++p) {
+            which[p] = p ? which[0] : -1;
+            if (todo) {
+                which[p] = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
+                same[p] = static_cast<uint32_t>(__ballot(id == which[p])) & 0xffffu;
+                todo &= ~same[p];
             }
         }
+        // rows behind the rank are read again and not kept
+        const uint16_t *w[2][BLOCKS];
 #pragma unroll
-        for (int b = 0; b < BLOCKS; ++b)
+        for (int p = 0; p < 2; ++p)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if ((same >> (4 * g + i) & 1u) && 16 * b + col < a.rank)
-                    a.h[(blockIdx.y * a.m + t0 + 4 * g + i) * a.rank + 16 * b + col] = acc[b][i];
+            for (int b = 0; b < BLOCKS; ++b)
+                w[p][b] = a.a + (static_cast<int64_t>(which[p]) * a.rank + (16 * b + col < a.rank ? 16 * b + col : 0)) * a.k + g * 8;
+        f32x4 acc[2][BLOCKS];
+#pragma unroll
+        for (int b = 0; b < BLOCKS; ++b) acc[0][b] = acc[1][b] = f32x4{0, 0, 0, 0};
+        int64_t kk = k0 + wave * 128;
+        for (; kk + 128 <= k1; kk += 128 * WAVES) {
+            u32x4 xv[4], wv[BLOCKS][4];
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                xv[s] = *reinterpret_cast<const u32x4 *>(x + kk + 32 * s);
+#pragma unroll
+                for (int b = 0; b < BLOCKS; ++b) wv[b][s] = *reinterpret_cast<const u32x4 *>(w[0][b] + kk + 32 * s);
+            }
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int b = 0; b < BLOCKS; ++b)
+                    acc[0][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(xv[s]), frag(wv[b][s]), acc[0][b], 0, 0, 0);
+            if (same[1]) {
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+#pragma unroll
+                    for (int b = 0; b < BLOCKS; ++b)
+                        acc[1][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            frag(xv[s]), frag(*reinterpret_cast<const u32x4 *>(w[1][b] + kk + 32 * s)), acc[1][b], 0, 0, 0);
+            }
+        }
+        for (; kk < k1; kk += 32) {                // fewer than 128 left: this wave's alone
+            u32x4 xv = {0, 0, 0, 0};
+            const bool in = kk + g * 8 < k1;
+            if (in) xv = *reinterpret_cast<const u32x4 *>(x + kk);
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int b = 0; b < BLOCKS; ++b) {
+                    u32x4 wv = {0, 0, 0, 0};
+                    if (in) wv = *reinterpret_cast<const u32x4 *>(w[p][b] + kk);
+                    acc[p][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(xv), frag(wv), acc[p][b], 0, 0, 0);
+                }
+        }
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            if (!same[p]) continue;
+#pragma unroll
+            for (int b = 0; b < BLOCKS; ++b) sums[wave][b][lane] = acc[p][b];
+            __syncthreads();
+            for (int b = wave; b < BLOCKS; b += WAVES) {
+                f32x4 v = sums[0][b][lane];
+#pragma unroll
+                for (int q = 1; q < WAVES; ++q) {
+                    const f32x4 u = sums[q][b][lane];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] += u[i];
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if ((same[p] >> (4 * g + i) & 1u) && 16 * b + col < a.rank)
+                        a.h[(blockIdx.y * a.m + t0 + 4 * g + i) * a.rank + 16 * b + col] = v[i];
+            }
+            __syncthreads();
+        }
     }
 }
 
@@ -182,16 +245,39 @@ __device__ __forceinline__ float third(float x, int p) {
     return p == 1 ? mid : rest - mid;
 }
 
-// blockIdx: (64 tokens, outputs).  The products run over (part of h, rank), 32 at a time.  Rows: 16
-// outputs, columns: a wave's 16 tokens; the outputs of four products are shuffled so that a lane ends
-// up with 16 successive ones of its token.
-template <int FMT, int STEPS>
-__global__ __launch_bounds__(256) void expand_many_kernel(LoraArgs a, int64_t each) {
+// blockIdx: (outputs, 64 tokens): what runs together covers whole rows of base and out.  The products run over
+// (part of h, rank), 32 at a time.  Rows: 16 outputs, columns: a wave's 16 tokens; the outputs of four products are
+// shuffled so that a lane ends up with 16 successive bytes of its token's row for each access, the four lanes of a token
+// with 64.  A wave has kTiles * 64 outputs, whose base it
+// asks for before it knows its adapters: waiting for those, and for h, would otherwise take as long as the rest.  (B asked
+// for as early takes registers for it, and half the waves: 54 -> 56 us for 4224 tokens, rank 16, 6144 outputs.)  The rows
+// of B that go with the three parts of h are the same: PERIOD of them are different (STEPS where the rank neither divides
+// 32 nor is a multiple of it).
+constexpr int kTiles = 2;
+// The output of row i of product q: four successive rows make 16 bytes of fp32, those of two products 16 bytes of bf16.
+template <int FMT>
+__device__ __forceinline__ int output_of(int q, int i) {
+    if constexpr (FMT == WSL_OUT_F32) return 16 * q + i;
+    return (q >> 1) * 32 + (i >> 2) * 8 + (q & 1) * 4 + (i & 3);
+}
+template <int FMT, int STEPS, int PERIOD>
+__global__ __launch_bounds__(256) void expand_many_kernel(LoraArgs a) {
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
-    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * 64 + wave * 16;
+    const int64_t t0 = static_cast<int64_t>(blockIdx.y) * 64 + wave * 16;
     if (t0 >= a.m) return;
+    constexpr int kWide = FMT == WSL_OUT_F32 ? 4 : 2, kSize = FMT == WSL_OUT_F32 ? 4 : 2;
     const bool there = t0 + col < a.m;
-    const int64_t t = there ? t0 + col : a.m - 1;
+    const int64_t t = there ? t0 + col : a.m - 1, n0 = static_cast<int64_t>(blockIdx.x) * (kTiles * 64);
+    u32x4 v[kTiles][kWide];
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) {
+        const int64_t n = n0 + 64 * i;
+        if (a.wide && n + 64 <= a.n_out) {
+            const u32x4 *in = reinterpret_cast<const u32x4 *>(static_cast<const char *>(a.base) + (t * a.ld_base + n) * kSize) + g;
+#pragma unroll
+            for (int q = 0; q < kWide; ++q) v[i][q] = in[4 * q];
+        }
+    }
     const int32_t id = there ? adapter_of(a, t, false) : -1;
     const uint32_t some = static_cast<uint32_t>(__ballot(id >= 0)) & 0xffffu;
     if (!some && a.base == a.out) return;
@@ -200,20 +286,23 @@ __global__ __launch_bounds__(256) void expand_many_kernel(LoraArgs a, int64_t ea
     const float scale = id >= 0 && a.scales ? a.scales[id] : 1.f;
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
-        const int slot = 32 * s + 8 * g, p = slot / a.rank, r = slot - p * a.rank;
-        at[s] = p < 3 ? r : 0;
-        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        const int slot = 32 * s + 8 * g, p = slot / a.rank;
+        at[s] = p < 3 || PERIOD < STEPS ? slot - p * a.rank : 0;
+        float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         if (id >= 0 && p < 3)
             for (int c = 0; c < a.parts; ++c) {
-                const float *from = a.h + (c * a.m + t) * a.rank + r;
+                const f32x4 *from = reinterpret_cast<const f32x4 *>(a.h + (c * a.m + t) * a.rank + at[s]);
+                const f32x4 lo = from[0], hi = from[1];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] += from[e];
+                for (int e = 0; e < 4; ++e) x[e] += lo[e], x[4 + e] += hi[e];
             }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) h[s][e] = pack_bf16x2(third(scale * v[2 * e], p), third(scale * v[2 * e + 1], p));
+        for (int e = 0; e < 4; ++e) h[s][e] = pack_bf16x2(third(scale * x[2 * e], p), third(scale * x[2 * e + 1], p));
     }
-    const int64_t n0 = blockIdx.y * each, n1 = n0 + each < a.n_out ? n0 + each : a.n_out;
-    for (int64_t n = n0; n < n1; n += 64) {
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) {
+        const int64_t n = n0 + 64 * i;
+        if (n >= a.n_out) break;
         f32x4 acc[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) acc[q] = f32x4{0, 0, 0, 0};
@@ -223,85 +312,84 @@ __global__ __launch_bounds__(256) void expand_many_kernel(LoraArgs a, int64_t ea
             todo &= ~static_cast<uint32_t>(__ballot(id == which));
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const int64_t row = n + (col >> 2) * 16 + q * 4 + (col & 3);
+                const int64_t row = n + output_of<FMT>(q, col);
                 const uint16_t *w = a.b + (which * a.n_out + (row < a.n_out ? row : a.n_out - 1)) * a.rank;
+                u32x4 b[PERIOD];
+#pragma unroll
+                for (int s = 0; s < PERIOD; ++s) b[s] = *reinterpret_cast<const u32x4 *>(w + at[s]);
                 f32x4 d = {0, 0, 0, 0};
 #pragma unroll
                 for (int s = 0; s < STEPS; ++s)
-                    d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(*reinterpret_cast<const u32x4 *>(w + at[s])),
-                                                                frag(h[s]), d, 0, 0, 0);
+                    d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(b[s % PERIOD]), frag(h[s]), d, 0, 0, 0);
                 if (id == which) acc[q] = d;           // whatever this adapter makes of other tokens is left
             }
         }
-        if (!there) continue;
-        const int64_t mine = n + g * 16;
-        const int64_t from = t * a.ld_base + mine, to = t * a.ld_out + mine;
-        if (a.wide && mine + 16 <= a.n_out) {
-            constexpr int kWide = FMT == WSL_OUT_F32 ? 4 : 2, kSize = FMT == WSL_OUT_F32 ? 4 : 2;
-            const u32x4 *in = reinterpret_cast<const u32x4 *>(static_cast<const char *>(a.base) + from * kSize);
-            u32x4 *out = reinterpret_cast<u32x4 *>(static_cast<char *>(a.out) + to * kSize), v[kWide];
-#pragma unroll
-            for (int q = 0; q < kWide; ++q) v[q] = in[q];
+        if (there && a.wide && n + 64 <= a.n_out) {
+            u32x4 *out = reinterpret_cast<u32x4 *>(static_cast<char *>(a.out) + (t * a.ld_out + n) * kSize) + g;
             if (id >= 0) {
 #pragma unroll
                 for (int q = 0; q < kWide; ++q)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const uint32_t w = v[q][e];
+                        const uint32_t w = v[i][q][e];
                         if constexpr (FMT == WSL_OUT_F32)
-                            v[q][e] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, w) + acc[q][e]);
+                            v[i][q][e] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, w) + acc[q][e]);
                         else
-                            v[q][e] = pack_bf16x2(bf16_lo(w) + acc[2 * q + e / 2][2 * (e % 2)],
-                                                  bf16_hi(w) + acc[2 * q + e / 2][2 * (e % 2) + 1]);
+                            v[i][q][e] = pack_bf16x2(bf16_lo(w) + acc[2 * q + e / 2][2 * (e % 2)],
+                                                     bf16_hi(w) + acc[2 * q + e / 2][2 * (e % 2) + 1]);
                     }
             }
 #pragma unroll
-            for (int q = 0; q < kWide; ++q) out[q] = v[q];
-        } else {
+            for (int q = 0; q < kWide; ++q) out[4 * q] = v[i][q];
+        } else if (there) {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (mine + 4 * q + i < a.n_out) {
-                        if (id >= 0) put<FMT>(a.out, to + 4 * q + i, get<FMT>(a.base, from + 4 * q + i) + acc[q][i]);
-                        else copy1<FMT>(a.out, to + 4 * q + i, a.base, from + 4 * q + i);
+                for (int e = 0; e < 4; ++e)
+                    if (const int64_t row = n + output_of<FMT>(q, 4 * g + e); row < a.n_out) {
+                        if (id >= 0) put<FMT>(a.out, t * a.ld_out + row, get<FMT>(a.base, t * a.ld_base + row) + acc[q][e]);
+                        else copy1<FMT>(a.out, t * a.ld_out + row, a.base, t * a.ld_base + row);
                     }
         }
     }
 }
 
 // Parts of k: few tokens, as many as there are kPart elements; more, until there are enough workgroups.
-int64_t parts_of(int64_t m, int64_t k) {
-    int64_t most = kMostParts;
-    if (m > kFewTokens) {
-        const int64_t tiles = (m + 63) / 64;
-        most = (512 + tiles - 1) / tiles;
+int64_t parts_of(int64_t m, int64_t rank, int64_t k) {
+    int64_t most = kMostParts, least = kPart;
+    if (!few(m, rank)) {
+        const int64_t tiles = (m + 15) / 16;
+        most = (kGroups + tiles - 1) / tiles;
         if (most > kMostParts) most = kMostParts;
+        least = 1024;                              // at least eight waves have something to do
     }
-    const int64_t parts = (k + kPart - 1) / kPart;
+    const int64_t parts = (k + least - 1) / least;
     return parts < most ? parts : most;
 }
 
 template <int FMT>
 void go_expand(const LoraArgs &a, hipStream_t s) {
-    if (a.m <= kFewTokens) {
+    if (few(a.m, a.rank)) {
         hipLaunchKernelGGL(expand_few_kernel<FMT>, dim3(static_cast<unsigned>(a.m), static_cast<unsigned>((a.n_out + 255) / 256)),
                            dim3(256), 0, s, a);
         return;
     }
-    const int64_t each = 512;
-    const dim3 grid(static_cast<unsigned>((a.m + 63) / 64), static_cast<unsigned>((a.n_out + each - 1) / each));
-    const int steps = (3 * a.rank + 31) / 32;
-    if (steps <= 2) hipLaunchKernelGGL((expand_many_kernel<FMT, 2>), grid, dim3(256), 0, s, a, each);
-    else if (steps <= 3) hipLaunchKernelGGL((expand_many_kernel<FMT, 3>), grid, dim3(256), 0, s, a, each);
-    else if (steps <= 6) hipLaunchKernelGGL((expand_many_kernel<FMT, 6>), grid, dim3(256), 0, s, a, each);
-    else hipLaunchKernelGGL((expand_many_kernel<FMT, 12>), grid, dim3(256), 0, s, a, each);
+    const dim3 grid(static_cast<unsigned>((a.n_out + kTiles * 64 - 1) / (kTiles * 64)), static_cast<unsigned>((a.m + 63) / 64));
+    const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, a); };
+    const int rank = a.rank, steps = (3 * rank + 31) / 32;
+    if (rank <= 8) go(expand_many_kernel<FMT, 1, 1>);
+    else if (rank == 16) go(expand_many_kernel<FMT, 2, 1>);
+    else if (rank == 32) go(expand_many_kernel<FMT, 3, 1>);
+    else if (rank == 64) go(expand_many_kernel<FMT, 6, 2>);
+    else if (rank == 128) go(expand_many_kernel<FMT, 12, 4>);
+    else if (steps <= 6) go(expand_many_kernel<FMT, 6, 6>);
+    else go(expand_many_kernel<FMT, 12, 12>);
 }
 
 }  // namespace
 
 size_t lora_ws_bytes(int64_t m, int64_t rank, int64_t k) {
-    return static_cast<size_t>(parts_of(m, k)) * static_cast<size_t>(m) * static_cast<size_t>(rank) * sizeof(float);
+    return static_cast<size_t>(parts_of(m, rank, k)) * static_cast<size_t>(m) * static_cast<size_t>(rank) * sizeof(float);
 }
 
 int launch_lora(const void *d_a, const void *d_b, int64_t n_adapters, int64_t rank, int64_t n_out, int64_t k,
@@ -313,13 +401,14 @@ int launch_lora(const void *d_a, const void *d_b, int64_t n_adapters, int64_t ra
     a.ids = ids, a.scales = scales, a.base = base, a.out = out, a.h = static_cast<float *>(ws), a.status = status;
     a.n_adapters = n_adapters, a.n_out = n_out, a.k = k, a.m = m, a.ldx = ldx, a.ld_base = ld_base, a.ld_out = ld_out;
     a.rank = static_cast<int32_t>(rank);
-    const int64_t parts = parts_of(m, k);
-    a.part = ((k + parts - 1) / parts + kPart - 1) / kPart * kPart;
+    const int64_t parts = parts_of(m, rank, k);
+    const int64_t step = few(m, rank) ? kPart : 1024;
+    a.part = ((k + parts - 1) / parts + step - 1) / step * step;
     a.parts = static_cast<int32_t>((k + a.part - 1) / a.part);
-    const int64_t step = fmt == WSL_OUT_F32 ? 4 : 8;
-    a.wide = ld_base % step == 0 && ld_out % step == 0 && reinterpret_cast<uintptr_t>(base) % 16 == 0 &&
+    const int64_t vec = fmt == WSL_OUT_F32 ? 4 : 8;
+    a.wide = ld_base % vec == 0 && ld_out % vec == 0 && reinterpret_cast<uintptr_t>(base) % 16 == 0 &&
              reinterpret_cast<uintptr_t>(out) % 16 == 0;
-    if (m <= kFewTokens) {
+    if (few(m, rank)) {
         const dim3 grid(static_cast<unsigned>(m), static_cast<unsigned>(a.parts));
         if (rank <= 8) hipLaunchKernelGGL(shrink_few_kernel<2>, grid, dim3(256), 0, s, a);
         else if (rank <= 16) hipLaunchKernelGGL(shrink_few_kernel<4>, grid, dim3(256), 0, s, a);
@@ -327,11 +416,11 @@ int launch_lora(const void *d_a, const void *d_b, int64_t n_adapters, int64_t ra
         else if (rank <= 64) hipLaunchKernelGGL(shrink_few_kernel<16>, grid, dim3(256), 0, s, a);
         else hipLaunchKernelGGL(shrink_few_kernel<32>, grid, dim3(256), 0, s, a);
     } else {
-        const dim3 grid(static_cast<unsigned>((m + 63) / 64), static_cast<unsigned>(a.parts));
-        if (rank <= 16) hipLaunchKernelGGL(shrink_many_kernel<1>, grid, dim3(256), 0, s, a);
-        else if (rank <= 32) hipLaunchKernelGGL(shrink_many_kernel<2>, grid, dim3(256), 0, s, a);
-        else if (rank <= 64) hipLaunchKernelGGL(shrink_many_kernel<4>, grid, dim3(256), 0, s, a);
-        else hipLaunchKernelGGL(shrink_many_kernel<8>, grid, dim3(256), 0, s, a);
+        const dim3 grid(static_cast<unsigned>((m + 15) / 16), static_cast<unsigned>(a.parts));
+        if (rank <= 16) hipLaunchKernelGGL((shrink_many_kernel<1, 8>), grid, dim3(512), 0, s, a);
+        else if (rank <= 32) hipLaunchKernelGGL((shrink_many_kernel<2, 8>), grid, dim3(512), 0, s, a);
+        else if (rank <= 64) hipLaunchKernelGGL((shrink_many_kernel<4, 8>), grid, dim3(512), 0, s, a);
+        else hipLaunchKernelGGL((shrink_many_kernel<8, 8>), grid, dim3(512), 0, s, a);
     }
     if (fmt == WSL_OUT_F32) go_expand<WSL_OUT_F32>(a, s);
     else go_expand<WSL_OUT_BF16>(a, s);

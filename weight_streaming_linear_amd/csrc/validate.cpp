@@ -342,7 +342,7 @@ int check_sample(const void *logits, int zfmt, int64_t n_rows, int64_t vocab, in
 }
 
 bool lora_shape_ok(int64_t m, int64_t rank, int64_t k) {
-    return m >= 0 && m <= (int64_t(1) << 24) && rank >= 8 && rank <= 128 && rank % 8 == 0 && k >= 8 &&
+    return m >= 0 && m <= (int64_t(1) << 20) && rank >= 8 && rank <= 128 && rank % 8 == 0 && k >= 8 &&
            k <= kMaxLoraDim && k % 8 == 0;
 }
 
