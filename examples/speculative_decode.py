@@ -1,13 +1,15 @@
 #!/usr/bin/env python3
 """Drafting and verifying with the library's decode-side calls, on random weights.
 
-A small decoder (NF4 linear layers, grouped-query attention, rotary positions) continues a few
-sequences.  A shallower one drafts ``width`` tokens for each, one at a time; the target scores all
-of them and the token before them in one sweep over its weights and its cache, and
-``verify_drafts`` keeps what agrees with the target and samples the next token.  Lengths, drafts
-and tokens stay on the device: nothing is read back until the end.
+A small decoder (NF4 linear layers, grouped-query attention, rotary positions, and adapters of the
+sequences' own) continues a few sequences.  A shallower one drafts ``width`` tokens for each, one at a
+time; the target scores all of them and the token before them in one sweep over its weights and its
+cache, and ``verify_drafts`` keeps what agrees with the target and samples the next token, both from
+distributions cut by temperature, top-k and top-p.  Pages, lengths, drafts and tokens stay on the
+device: nothing is read back until the end.
 
-    python examples/speculative_decode.py [--e4m3] [--seqs 4] [--width 4] [--tokens 64]
+    python examples/speculative_decode.py [--e4m3] [--seqs 4] [--width 4] [--tokens 64] [--adapters 3]
+                                          [--temperature 0.8] [--top-k 50] [--top-p 0.9]
 """
 
 import argparse
@@ -23,10 +25,12 @@ NF4, F32 = wsl.WSL_W_NF4, wsl.WSL_OUT_F32
 
 
 class Decoder:
-    """`layers` layers of random NF4 weights, each with a paged key-value cache for n_seq sequences."""
+    """`layers` layers of random NF4 weights, each with a paged key-value cache for n_seq sequences, and `adapters`
+    low-rank adapters of the attention's projections: sequence i uses i % (adapters + 1), the last of which is
+    none.  `sampling`: what sample_logits makes its distributions by."""
 
     def __init__(self, n_seq, layers, hidden=1024, heads=16, n_kv=4, ffn=2816, vocab=8000, capacity=1024, page=16,
-                 fmt=wsl.WSL_KV_BF16, seed=0):
+                 fmt=wsl.WSL_KV_BF16, seed=0, adapters=0, rank=16, sampling=None):
         self.hidden, self.heads, self.n_kv, self.ffn, self.vocab, self.page = hidden, heads, n_kv, ffn, vocab, page
         self.dim = hidden // heads
         gen = torch.Generator(device="cuda").manual_seed(seed)
@@ -40,47 +44,53 @@ class Decoder:
                             up=packed(2 * ffn, hidden), down=packed(hidden, ffn)) for _ in range(layers)]
         self.head = packed(vocab, hidden)
         pages = -(-capacity // page)
-        self.table = torch.randperm(n_seq * pages, generator=gen, device="cuda").view(n_seq, pages).to(torch.int32)
+        self.pages = wsl.KVPages.empty(n_seq, pages, n_seq * pages, page)
+        self.table = self.pages.table
+        self.freqs = wsl.rotary_freqs(self.dim)
+        self.sampling = dict(sampling or {})
+        self.ids = None
+        if adapters:
+            ids = torch.arange(n_seq, device="cuda") % (adapters + 1)
+            self.ids = torch.where(ids == adapters, -1, ids).to(torch.int32)
+            for layer in self.layers:
+                for name in ("qkv", "o"):
+                    _, n, k = layer[name]
+                    a = torch.randn((adapters, rank, k), generator=gen, device="cuda").mul_(k ** -0.5)
+                    b = torch.randn((adapters, n, rank), generator=gen, device="cuda").mul_(0.3 * rank ** -0.5)
+                    layer[name + "_lora"] = a.to(torch.bfloat16), b.to(torch.bfloat16)
         self.caches = [wsl.KVCache.empty(n_seq * pages, n_kv, page, self.dim, fmt) for _ in range(layers)]
 
-    def linear(self, w, x):
+    def linear(self, w, x, lora=None):
         packed, n, k = w
-        return wsl.linear_gemm(packed, x, wfmt=NF4, n_out=n, k=k, ofmt=F32)
+        y = wsl.linear_gemm(packed, x, wfmt=NF4, n_out=n, k=k, ofmt=F32)
+        if lora is not None:
+            wsl.lora_add(y, x, *lora, self.ids.repeat_interleave(len(x) // len(self.ids)), out=y)
+        return y
 
     @staticmethod
     def norm(x):
         return (x * torch.rsqrt(x.square().mean(-1, keepdim=True) + 1e-5)).to(torch.bfloat16)
 
-    def rotate(self, x, at):
-        """Rotary positions of x [n_seq, q_len, heads, dim] at the positions `at` [n_seq, q_len]."""
-        half = self.dim // 2
-        freq = 10000.0 ** (-torch.arange(half, device="cuda", dtype=torch.float64) / half)
-        angle = at.double()[..., None, None] * freq
-        c, s = angle.cos().float(), angle.sin().float()
-        a, b = x[..., :half], x[..., half:]
-        return torch.cat((a * c - b * s, b * c + a * s), -1)
-
     def step(self, tokens, lens):
-        """Takes in tokens [n_seq, q_len] behind the `lens` [n_seq] that the cache holds of each sequence
-        (on the device: that lens + q_len is within the capacity is for the caller to see to); returns the
-        probabilities [n_seq, q_len, vocab] of what follows each."""
+        """Takes in tokens [n_seq, q_len] behind the first `lens` [n_seq] of each sequence (on the device: that
+        lens + q_len is within the capacity is for the caller to see to), giving back the pages of any tokens
+        that were taken in beyond; returns the probabilities [n_seq, q_len, vocab] of what follows each."""
         n_seq, q_len = tokens.shape
-        at = lens[:, None] + torch.arange(q_len, device="cuda")
-        slots = (self.table.gather(1, at // self.page).long() * self.page + at % self.page).view(-1)
-        kv_lens = (lens + q_len).to(torch.int32)
+        wsl.kv_pages_trim(self.pages, lens.to(torch.int32))
+        slots, at = wsl.kv_pages_grow(self.pages, q_len)
         q_heads, kv = self.heads * self.dim, self.n_kv * self.dim
         h = wsl.nf4_embed_rows(self.embed, self.vocab, self.hidden, tokens.reshape(-1).long(), ofmt=F32)
         for layer, cache in zip(self.layers, self.caches):
-            x = self.linear(layer["qkv"], self.norm(h)).view(n_seq, q_len, -1)
-            q = self.rotate(x[..., :q_heads].unflatten(-1, (self.heads, self.dim)), at)
-            k = self.rotate(x[..., q_heads:q_heads + kv].unflatten(-1, (self.n_kv, self.dim)), at)
-            v = x.view(n_seq * q_len, -1)[:, q_heads + kv:].unflatten(-1, (self.n_kv, self.dim))
-            wsl.kv_cache_write(cache, k.flatten(0, 1), v, slots)
-            out = wsl.attn_decode(cache, q.to(torch.bfloat16), self.table, kv_lens)
-            h = h + self.linear(layer["o"], out.view(-1, self.hidden))
+            x = self.linear(layer["qkv"], self.norm(h), layer.get("qkv_lora"))
+            q, k, v = (y.unflatten(-1, (-1, self.dim)) for y in x.split((q_heads, kv, kv), 1))
+            q = wsl.rotary_embed(q, at, self.freqs, ofmt=wsl.WSL_OUT_BF16)
+            k = wsl.rotary_embed(k, at, self.freqs, out=k)
+            wsl.kv_cache_write(cache, k, v, slots)
+            out = wsl.attn_decode(cache, q.view(n_seq, q_len, self.heads, self.dim), self.table, self.pages.lens)
+            h = h + self.linear(layer["o"], out.view(-1, self.hidden), layer.get("o_lora"))
             gate, up = self.linear(layer["up"], self.norm(h)).chunk(2, -1)
             h = h + self.linear(layer["down"], (torch.nn.functional.silu(gate) * up).to(torch.bfloat16))
-        return torch.softmax(self.linear(self.head, self.norm(h)), -1).view(n_seq, q_len, -1)
+        return wsl.sample_logits(self.linear(self.head, self.norm(h)), **self.sampling).view(n_seq, q_len, -1)
 
 
 def pick(p, u):
@@ -138,10 +148,15 @@ def main():
     ap.add_argument("--tokens", type=int, default=64)
     ap.add_argument("--layers", type=int, default=4)
     ap.add_argument("--e4m3", action="store_true", help="an 8-bit cache")
+    ap.add_argument("--adapters", type=int, default=0)
+    ap.add_argument("--temperature", type=float, default=1.0)
+    ap.add_argument("--top-k", type=int, default=0)
+    ap.add_argument("--top-p", type=float, default=1.0)
     a = ap.parse_args()
     fmt = wsl.WSL_KV_E4M3 if a.e4m3 else wsl.WSL_KV_BF16
     length, rounds = 100, -(-a.tokens // (a.width + 1))
-    kw = dict(fmt=fmt, capacity=max(1024, most_tokens(length, a.width, rounds)))
+    kw = dict(fmt=fmt, capacity=max(1024, most_tokens(length, a.width, rounds)), adapters=a.adapters,
+              sampling=dict(temperature=a.temperature, top_k=a.top_k, top_p=a.top_p))
     target = Decoder(a.seqs, a.layers, **kw)
     drafter = Decoder(a.seqs, max(1, a.layers // 2), **kw)      # its weights only in the first layers: some drafts stand
     gen = torch.Generator(device="cuda").manual_seed(1)
