@@ -494,7 +494,8 @@ int verify_drafts(const void *d_p, const void *d_q, int pfmt, int64_t n_seq, int
  * free_pages device int32 [n_pages], a stack: its first *n_free entries are the free pages.
  * n_free     device int32 [1].
  * n_seq 0 .. 65535.  pages_per_seq 1 .. ld_table.  n_pages 1 .. 2^31 - 1.  page_size 1 .. 2^30.
- * A sequence holds at most pages_per_seq * page_size tokens, and 2^31 - 1.
+ * A sequence holds at most pages_per_seq * page_size tokens, and 2^31 - 1.  A page is held by one sequence, or free:
+ * one that two rows name is given back twice.
  */
 typedef struct wsl_kv_pages {
     int32_t *table, *lens, *free_pages, *n_free;

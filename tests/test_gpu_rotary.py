@@ -93,6 +93,18 @@ def test_turning_back_and_by_differences():
     assert ((near - far).abs() <= 4 * 4 * 2 ** -24 * 2 ** 0.5 * size).all()
 
 
+def test_more_tokens_than_workgroups():
+    """Past 2^20 tokens each workgroup goes on with further ones."""
+    import torch
+    n = (1 << 20) + 3
+    x = torch.randn((n, 1, 16), generator=torch.Generator(device="cuda").manual_seed(4), device="cuda").to(torch.bfloat16)
+    at, freqs = torch.arange(n, device="cuda"), wsl.rotary_freqs(16)
+    out = wsl.rotary_embed(x, at, freqs)
+    some = torch.cat((torch.arange(5), torch.arange(n - 5, n))).cuda()
+    _check(out[some], x[some], at[some], freqs, False, 1.0)
+    assert out[: 1 << 19].equal(wsl.rotary_embed(x[: 1 << 19], at[: 1 << 19], freqs))
+
+
 def test_empty_and_infinite():
     import torch
     freqs = wsl.rotary_freqs(32)

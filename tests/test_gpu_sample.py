@@ -67,6 +67,32 @@ def test_settings_against_the_definition(n, vocab, pad, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("n,vocab,pad", [(2, 4096, 1), (2, 8193, 0), (2, 16385, 0), (1, 131072, 0), (2, 131073, 3), (1, 262144, 0),
+                                         (2, 262145, 1), (1, 400000, 0)])
+def test_where_parts_begin_and_end(n, vocab, pad, dtype):
+    """Rows at the ends of what one workgroup, a part, and a table of parts hold."""
+    for seed, how in enumerate([dict(top_k=300, top_p=0.9, temperature=0.9), dict(top_p=0.97), dict(min_p=0.001, temperature=0.8), {}]):
+        z, u = _logits(vocab + seed, n, vocab, dtype, pad=pad, peaks=seed % 2)
+        z[0, vocab - 1] = z[0].max() + 1        # the last entry is the greatest
+        _check(z, u, probs_too=seed < 2, **how)
+
+
+def test_settings_where_few_are_kept_far_apart():
+    """Borders in cells that are empty, or hold one entry, over parts whose greatest entries differ by far."""
+    import torch
+    vocab = 60000
+    z = torch.full((3, vocab), -400.0, device="cuda")
+    z[:, 5], z[:, 20000], z[:, 59999] = 10.0, 9.0, -30.0
+    z[1, 30000:34000] = torch.linspace(-60, 5, 4000, device="cuda")
+    z[2, 100::7] = float("-inf")
+    u = torch.tensor([0.2, 0.9, 0.99999], device="cuda")
+    for how in (dict(top_k=2), dict(top_k=3), dict(top_k=50), dict(top_p=0.99), dict(top_p=1 - 2.0 ** -24), dict(min_p=0.3), dict(min_p=0.4),
+                dict(min_p=1e-30), dict(top_k=30000, top_p=0.9999999), dict(top_k=4, min_p=1e-38, temperature=3.0),
+                dict(temperature=40.0, top_k=59000), dict(temperature=200.0, top_p=0.9)):
+        _check(z, u, **how)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 @pytest.mark.parametrize("vocab", [777, 40001])
 def test_settings_of_each_row(vocab, dtype):
     import torch

@@ -877,10 +877,10 @@ def kv_pages_grow(pages, new, n_tokens=None, slots=None, positions=None, starts=
     index, n_seq = pages.index, pages.n_seq
     if index != _device():
         _here(pages.lens, "pages")
-    if isinstance(new, int):
-        want, each = None, new
+    if not isinstance(new, torch.Tensor):
+        want, each = None, int(new)
         if n_tokens is None:
-            n_tokens = n_seq * new if slots is None else slots.numel()
+            n_tokens = n_seq * each if slots is None else slots.numel()
     else:
         _exactly(new, "new", _i32, index, (n_seq,))
         want, each = new.data_ptr(), 0
@@ -1017,7 +1017,7 @@ def rotary_embed(q, positions, freqs, k=None, interleaved=False, amplitude=1.0, 
     elif k_out is not None:
         raise ValueError("k_out without k")
     rc = lib().rotary_embed(q.data_ptr(), heads, ld_q, _at(k), n_kv, ld_k, xfmt, count, dim, 2 * freqs.numel(),
-                            positions.data_ptr(), freqs.data_ptr(), amplitude, 1 if interleaved else 0, out.data_ptr(), ld_out,
+                            positions.data_ptr(), freqs.data_ptr(), float(amplitude), 1 if interleaved else 0, out.data_ptr(), ld_out,
                             _at(k_out), ld_ko, ofmt, _stream(stream))
     if rc:
         _check(rc, "rotary_embed")
@@ -1069,7 +1069,7 @@ def sample_logits(logits, u=None, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0
         _exactly(temperature, "temperature", _f32, index, (n,))
         how.d_temperature = temperature.data_ptr()
     else:
-        how.temperature = temperature
+        how.temperature = float(temperature)
     if isinstance(top_k, torch.Tensor):
         _exactly(top_k, "top_k", _i32, index, (n,))
         how.d_top_k = top_k.data_ptr()
@@ -1079,12 +1079,12 @@ def sample_logits(logits, u=None, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0
         _exactly(top_p, "top_p", _f32, index, (n,))
         how.d_top_p = top_p.data_ptr()
     else:
-        how.top_p = top_p
+        how.top_p = float(top_p)
     if isinstance(min_p, torch.Tensor):
         _exactly(min_p, "min_p", _f32, index, (n,))
         how.d_min_p = min_p.data_ptr()
     else:
-        how.min_p = min_p
+        how.min_p = float(min_p)
     if u is not None:
         _exactly(u, "u", _f32, index, (n,))
         if tokens is None:
