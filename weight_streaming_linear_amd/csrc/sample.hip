@@ -184,7 +184,7 @@ struct Scale {
 };
 
 // The first bin up to which there are `count` entries (by_count), or a sum of `sum`; where rounding lets
-// none, the last that holds any.  Every wave comes to the same.
+// none, the last that holds any.  By one wave: the others wait, for what all of them did would take as many times as long.
 __device__ __forceinline__ Border border_of(const Bins &b, bool by_count, uint32_t count, double sum) {
     const int lane = static_cast<int>(threadIdx.x & 63);
     constexpr int kMine = kCells / 64;
@@ -221,12 +221,25 @@ __device__ __forceinline__ Border border_of(const Bins &b, bool by_count, uint32
     return o;
 }
 
+// What one wave found, for all: the same in every lane.
+__device__ __forceinline__ uint32_t same(uint32_t v) { return static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(v))); }
+__device__ __forceinline__ double same(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(double, static_cast<uint64_t>(same(static_cast<uint32_t>(b >> 32))) << 32 | same(static_cast<uint32_t>(b)));
+}
+__device__ __forceinline__ Border same(const Border &b) {
+    return Border{static_cast<int32_t>(same(static_cast<uint32_t>(b.bin))), same(b.before), same(b.in), same(b.all), same(b.w_before), same(b.w_all)};
+}
+
 struct Shared {
     uint64_t held[kHeld];                          // orders; 0: none
     Bins cells, bins;
     uint64_t sum[kCells];
     uint64_t list[kList], sorted[kList];
     uint32_t rank[kList];
+    Border border;
+    uint64_t from;
+    double w_kept;
     uint64_t least[kWaves], most[kWaves];
     float top[kWaves];
     uint32_t n, bad;
@@ -320,7 +333,12 @@ __device__ __forceinline__ uint64_t keep_from(const Entries<FMT> &row, Shared &s
         __syncthreads();
         if (tid < kCells) s.bins.w[tid] = sc.weight_of(static_cast<double>(s.sum[tid]), cell);
         __syncthreads();
-        b = border_of(s.bins, by_count, count, sum);
+        if (wave == 0) {
+            b = border_of(s.bins, by_count, count, sum);
+            if (lane == 0) s.border = b;
+        }
+        __syncthreads();
+        b = same(s.border);
         count -= b.before, sum -= b.w_before;
         w_kept += b.w_before;
         hi -= static_cast<uint64_t>(b.bin) << shift;
@@ -338,69 +356,72 @@ __device__ __forceinline__ uint64_t keep_from(const Entries<FMT> &row, Shared &s
     });
     __syncthreads();
     const uint32_t n = s.n < kList ? s.n : kList;                      // b.in
-    if (n <= 64) {                                 // every wave by itself: a lane an entry, brought into their order
-        const uint64_t mine = static_cast<uint32_t>(lane) < n ? s.list[lane] : 0;
-        uint32_t place = 0;
-        for (uint32_t i = 0; i < n; ++i) {
-            const uint64_t o = static_cast<uint64_t>(lane_value(static_cast<uint32_t>(mine >> 32), i)) << 32 |
-                               lane_value(static_cast<uint32_t>(mine), i);
-            place += o > mine ? 1u : 0u;
-        }
-        const int to = static_cast<int>(static_cast<uint32_t>(lane) < n ? place : lane) * 4;
-        const auto push = [&](uint64_t v) {
-            const uint32_t l = static_cast<uint32_t>(__builtin_amdgcn_ds_permute(to, static_cast<int>(v)));
-            const uint32_t h = static_cast<uint32_t>(__builtin_amdgcn_ds_permute(to, static_cast<int>(v >> 32)));
-            return static_cast<uint64_t>(h) << 32 | l;
-        };
-        const uint64_t sorted = push(mine);
-        const double at = lanes_before(static_cast<uint32_t>(lane) < n ? sc.weight(logit_of(sorted)) : 0.0);
-        const uint64_t hits = __ballot(static_cast<uint32_t>(lane) < n && (by_count ? static_cast<uint32_t>(lane) + 1 >= count : at >= sum));
-        __syncthreads();                           // the list and the bins may be used again
-        if (n == 0) return ~0ull;                  // (a border lies in a cell that holds something)
-        const int l = hits ? __builtin_ctzll(hits) : static_cast<int>(n) - 1;
-        w_kept += lane_value(at, l);
-        return static_cast<uint64_t>(lane_value(static_cast<uint32_t>(sorted >> 32), l)) << 32 | lane_value(static_cast<uint32_t>(sorted), l);
-    }
-    // an entry's place: as many threads as there are for each, a part of the list each
-    const uint32_t shares = blockDim.x / kList, entry = tid % kList, share = tid / kList;
-    if (entry < n) {
-        const uint64_t mine = s.list[entry];
-        uint32_t rank = 0;
+    if (n > 64) {
+        // an entry's place: as many threads as there are for each, a part of the list each
+        const uint32_t shares = blockDim.x / kList, entry = tid % kList, share = tid / kList;
+        if (entry < n) {
+            const uint64_t mine = s.list[entry];
+            uint32_t rank = 0;
 #pragma unroll 4
-        for (uint32_t i = n * share / shares; i < n * (share + 1) / shares; ++i) rank += s.list[i] > mine ? 1u : 0u;
-        atomicAdd(&s.rank[entry], rank);
-    }
-    __syncthreads();
-    if (tid < n) s.sorted[s.rank[tid]] = s.list[tid];
-    __syncthreads();
-    // every wave: successive entries of a lane
-    constexpr int kMine = kList / 64;
-    double w[kMine], ws = 0;
-#pragma unroll 1
-    for (uint32_t i = 0; i < kMine; ++i) {
-        const uint32_t at = lane * kMine + i;
-        const double v = at < n ? sc.weight(logit_of(s.sorted[at])) : 0;
-        w[0] = i == 0 ? v : w[0], w[1] = i == 1 ? v : w[1], w[2] = i == 2 ? v : w[2], w[3] = i == 3 ? v : w[3];
-        ws += v;
-    }
-    double at = lanes_before(ws) - ws;
-    int hit = -1, last = -1;
-    double hit_w = 0, last_w = 0;
-#pragma unroll
-    for (int i = 0; i < kMine; ++i) {
-        at += w[i];
-        const uint32_t place = lane * kMine + i;
-        if (place < n) {
-            last = i, last_w = at;
-            if (hit < 0 && (by_count ? place + 1 >= count : at >= sum)) hit = i, hit_w = at;
+            for (uint32_t i = n * share / shares; i < n * (share + 1) / shares; ++i) rank += s.list[i] > mine ? 1u : 0u;
+            atomicAdd(&s.rank[entry], rank);
         }
+        __syncthreads();
+        if (tid < n) s.sorted[s.rank[tid]] = s.list[tid];
+        __syncthreads();
     }
-    const uint64_t hits = __ballot(hit >= 0);
-    const int l = hits ? __builtin_ctzll(hits) : static_cast<int>(n - 1) / kMine;
-    w_kept += lane_value(hits ? hit_w : last_w, l);
-    const uint64_t from = s.sorted[l * kMine + __builtin_amdgcn_readlane(hits ? hit : last, l)];
+    if (wave == 0) {
+        uint64_t from = ~0ull;                     // (a border lies in a cell that holds something)
+        double w = 0;
+        if (n <= 64) {                             // a lane an entry, brought into their order
+            const bool in = static_cast<uint32_t>(lane) < n;
+            const uint64_t mine = in ? s.list[lane] : 0;
+            uint32_t place = 0;
+#pragma unroll 4
+            for (uint32_t i = 0; i < n; ++i) place += s.list[i] > mine ? 1u : 0u;
+            const int to = static_cast<int>(in ? place : lane) * 4;
+            const auto push = [&](uint64_t v) {
+                const uint32_t l = static_cast<uint32_t>(__builtin_amdgcn_ds_permute(to, static_cast<int>(v)));
+                const uint32_t h = static_cast<uint32_t>(__builtin_amdgcn_ds_permute(to, static_cast<int>(v >> 32)));
+                return static_cast<uint64_t>(h) << 32 | l;
+            };
+            const uint64_t sorted = push(mine);
+            const double at = lanes_before(in ? sc.weight(logit_of(sorted)) : 0.0);
+            const uint64_t hits = __ballot(in && (by_count ? static_cast<uint32_t>(lane) + 1 >= count : at >= sum));
+            if (n) {
+                const int l = hits ? __builtin_ctzll(hits) : static_cast<int>(n) - 1;
+                w = lane_value(at, l);
+                from = static_cast<uint64_t>(lane_value(static_cast<uint32_t>(sorted >> 32), l)) << 32 |
+                       lane_value(static_cast<uint32_t>(sorted), l);
+            }
+        } else {                                   // successive entries of a lane
+            constexpr uint32_t kMine = kList / 64;
+            double ws = 0;
+#pragma unroll 1
+            for (uint32_t i = 0; i < kMine; ++i) {
+                const uint32_t at = lane * kMine + i;
+                ws += at < n ? sc.weight(logit_of(s.sorted[at])) : 0;
+            }
+            // the lane, then which of its entries
+            const double up = lanes_before(ws);
+            const uint32_t end = (lane + 1) * kMine < n ? (lane + 1) * kMine : n;
+            const uint64_t hits = __ballot(lane * kMine < n && (by_count ? end >= count : up >= sum));
+            const uint32_t l = hits ? static_cast<uint32_t>(__builtin_ctzll(hits)) : (n - 1) / kMine;
+            w = lane_value(up, l) - lane_value(ws, l);
+            uint32_t at = l * kMine;
+#pragma unroll 1
+            for (;; ++at) {
+                w += sc.weight(logit_of(s.sorted[at]));
+                if (at + 1 >= n || at + 1 >= (l + 1) * kMine || (by_count ? at + 1 >= count : w >= sum)) break;
+            }
+            from = s.sorted[at];
+        }
+        if (lane == 0) s.from = from, s.w_kept = w;
+    }
     __syncthreads();                               // the list and the bins may be used again
-    return from;
+    w_kept += same(s.w_kept);
+    const uint64_t from = s.from;
+    return static_cast<uint64_t>(same(static_cast<uint32_t>(from >> 32))) << 32 | same(static_cast<uint32_t>(from));
 }
 
 // In the order of n sums (LDS): the first that passes u times their total (share; else u itself), or the last
@@ -538,13 +559,22 @@ __global__ __launch_bounds__(kWaves * 64) void sample_short_kernel(SampleArgs a)
         __syncthreads();
         for (uint32_t i = tid; i < kCells; i += blockDim.x) s.cells.w[i] = sc.weight_of(static_cast<double>(s.sum[i]), i);
         __syncthreads();
-        const Border all = border_of(s.cells, true, h.k, 0);
-        double w_kept = all.w_all;
         // top-k, then top-p of what it leaves
+        double w_kept = 0;
 #pragma unroll 1
-        for (int by_count = h.k < all.all; by_count >= (h.top_p < 1 ? 0 : 1); --by_count) {
+        for (int by_count = 1; by_count >= (h.top_p < 1 ? 0 : 1); --by_count) {
             const double sum = by_count ? 0 : static_cast<double>(h.top_p) * w_kept;
-            const Border b = by_count ? all : border_of(s.cells, false, 0, sum);
+            if (wave == 0) {
+                const Border found = border_of(s.cells, by_count != 0, h.k, sum);
+                if (lane == 0) s.border = found;
+            }
+            __syncthreads();
+            const Border b = same(s.border);
+            if (by_count) w_kept = b.w_all;
+            if (by_count && h.k >= b.all) {
+                __syncthreads();                   // all have read it
+                continue;
+            }
             const uint64_t o = keep_from(row, s, sc, b, by_count != 0, h.k, sum, w_kept);
             from = o > from ? o : from;
         }
@@ -616,24 +646,28 @@ __global__ __launch_bounds__(kWaves * 64) void sample_cells_kernel(SampleArgs a)
         if (at != ~0u) atomicMin(&first, at);
     } else if (in_row(m)) {
         const double n_m = __builtin_rint(h.c8 * static_cast<double>(m));
+        // the last cell's entries count by how far they are behind it: weights of less than 2^-31, for which an
+        // exponential of 32 bits does (2^-23 of them; of 2^22 entries together 2^-33), added up in 64 by their lane
+        double behind = 0;
+        uint32_t n_behind = 0;
 #pragma unroll
         for (int i = 0; i < SEGS; ++i)
 #pragma unroll
             for (int e = 0; e < kEach; ++e) {
                 const double y = h.c8 * static_cast<double>(z[i][e]), n = __builtin_rint(y), d = n_m - n;
-                uint64_t v = whole_power(y - n) + (1ull << 48);
-                int c = static_cast<int>(d);
-                const bool near = d < kCells - 1;
-                bool put = near;
-                if (__ballot(!near)) {             // the last cell's entries count by how far they are behind it
-                    if (!near) {
-                        c = kCells - 1, put = in_row(z[i][e]);
-                        const float w = exp2f(static_cast<float>(y - (n_m - (kCells - 1))) * 0.125f) * 4294967296.f;
-                        v = static_cast<uint64_t>(w) + (1ull << 48);
-                    }
+                if (d < kCells - 1) {
+                    const uint64_t v = whole_power(y - n) + (1ull << 48);
+                    atomicAdd(reinterpret_cast<unsigned long long *>(&cells[static_cast<int>(d)]), static_cast<unsigned long long>(v));
+                } else if (in_row(z[i][e])) {
+                    behind += static_cast<double>(__builtin_amdgcn_exp2f(static_cast<float>(y - (n_m - (kCells - 1))) * 0.125f));
+                    ++n_behind;
                 }
-                if (put) atomicAdd(reinterpret_cast<unsigned long long *>(&cells[c]), static_cast<unsigned long long>(v));
             }
+        const double sum = lanes_total(behind);
+        n_behind = lane_value(lanes_before(n_behind), 63);
+        if (lane == 0 && n_behind)
+            atomicAdd(reinterpret_cast<unsigned long long *>(&cells[kCells - 1]),
+                      static_cast<unsigned long long>(static_cast<uint64_t>(sum * kPartUnit) + (static_cast<uint64_t>(n_behind) << 48)));
     }
     __syncthreads();
     const int64_t at = r * a.parts + blockIdx.x;
@@ -724,7 +758,7 @@ __device__ __forceinline__ void put_together(int parts, const uint64_t *mine, co
     uint64_t sum = 0;
     double rest = 0;
     uint32_t count = 0, rest_count = 0;
-    const double top = sc.top();
+    const double top = sc.top(), one = 1 / top;
     for (int i = group; i < parts; i += groups) {
         const int shift = s.shift[i], from = static_cast<int>(cell) - shift;
         const bool here = from >= 0 && cell < kCells - 1, behind = static_cast<int>(cell) + shift >= kCells - 1;
@@ -732,7 +766,7 @@ __device__ __forceinline__ void put_together(int parts, const uint64_t *mine, co
         sum += v & 0xffffffffffffull;
         count += static_cast<uint32_t>(v >> 48);
         if (__ballot(u != 0)) {
-            rest += static_cast<double>(u & 0xffffffffffffull) / top * power(-(s.below[i] + cell));
+            rest += static_cast<double>(u & 0xffffffffffffull) * one * power(-(s.below[i] + cell));
             rest_count += static_cast<uint32_t>(u >> 48);
         }
     }
@@ -755,24 +789,36 @@ __device__ __forceinline__ void put_together(int parts, const uint64_t *mine, co
 
 __device__ __forceinline__ Plan plan_of(const Bins &cells, const Scale &sc, const How &h, double least) {
     Plan p;
-    p.k = border_of(cells, true, h.k, 0);
-    p.p = p.k;
-    p.k_on = h.k < p.k.all, p.p_on = h.top_p < 1;
+    p.p_on = h.top_p < 1;
     p.one = p.min = p.lo = -1, p.hi = -2, p.n = 0, p.pad = 0;
-    double least_w = p.k.w_all, most_w = p.k.w_all;
-    if (p.k_on) {
-        p.one = p.k.bin;
-        // between the lightest and the heaviest that (k - before) entries of the cell can be: 2^(1/16) either way
-        // of its middle, which is as far from the greatest's, and a little
-        const double some = static_cast<double>(h.k - p.k.before), unit = power(-p.one);
-        least_w = p.k.w_before + (p.one < kCells - 1 ? 0.916 * unit * some : 0.0);
-        most_w = p.k.w_before + 1.091 * unit * some;
-    }
-    if (p.p_on) {
-        p.p = border_of(cells, false, 0, static_cast<double>(h.top_p) * least_w * (1 - 1e-6));
-        p.lo = p.hi = p.p.bin;
-        const double most = static_cast<double>(h.top_p) * most_w * (1 + 1e-6);
-        if (!(most < p.p.w_before + cells.w[p.lo])) p.hi = border_of(cells, false, 0, most).bin;
+    // the border of top-k, and of the least and the most that top-p may keep
+    double sum = 0, most = 0;
+#pragma unroll 1
+    for (int step = 0; step < 3; ++step) {
+        const Border b = border_of(cells, step == 0, h.k, sum);
+        if (step == 0) {
+            p.k = p.p = b;
+            p.k_on = h.k < b.all;
+            double least_w = b.w_all, most_w = b.w_all;
+            if (p.k_on) {
+                p.one = b.bin;
+                // between the lightest and the heaviest that (k - before) entries of the cell can be: 2^(1/16) either
+                // way of its middle, which is as far from the greatest's, and a little
+                const double some = static_cast<double>(h.k - b.before), unit = power(-p.one);
+                least_w = b.w_before + (p.one < kCells - 1 ? 0.916 * unit * some : 0.0);
+                most_w = b.w_before + 1.091 * unit * some;
+            }
+            if (!p.p_on) break;
+            sum = static_cast<double>(h.top_p) * least_w * (1 - 1e-6);
+            most = static_cast<double>(h.top_p) * most_w * (1 + 1e-6);
+        } else if (step == 1) {
+            p.p = b;
+            p.lo = p.hi = b.bin;
+            if (most < b.w_before + cells.w[b.bin]) break;
+            sum = most;
+        } else {
+            p.hi = b.bin;
+        }
     }
     if (least > -__builtin_huge_val()) {
         const double d = sc.n_m - __builtin_rint(least);
@@ -825,19 +871,32 @@ __global__ __launch_bounds__(kWaves * 64) void sample_border_kernel(SampleArgs a
     raw.take(a.cells + r * a.parts * kCells, a.parts);
     const How h = how_of(a, r);
     if (h.greedy || !filters(a, h)) return;
+    const int64_t j0 = static_cast<int64_t>(blockIdx.x) * a.part + wave * SEGS * kSeg;
+    float z[SEGS][kEach];
+#pragma unroll
+    for (int i = 0; i < SEGS; ++i) load_seg<FMT>(static_cast<const char *>(a.logits) + r * a.ld * kSize, j0 + i * kSeg, a.vocab, z[i], -kInf);
     raw.put(held, a.parts);
     const Whole all = heads_of(a, head, h.c8, s);
     if (all.bad || !in_row(all.m)) return;
     const Scale sc(h.c8, all.m);
     const uint64_t *mine_cells = PartCells<FEW>::of(a.cells + r * a.parts * kCells, held);
     put_together(a.parts, mine_cells, sc, s, cells);
-    const Plan p = plan_of(cells, sc, h, sc.y(all.m) + h.log_min_p);
+    __shared__ Plan plan;
+    if (wave == 0) {
+        const Plan o = plan_of(cells, sc, h, sc.y(all.m) + h.log_min_p);
+        if (lane == 0) plan = o;
+    }
+    __syncthreads();
+    Plan p = plan;
+    p.one = static_cast<int32_t>(same(static_cast<uint32_t>(p.one))), p.lo = static_cast<int32_t>(same(static_cast<uint32_t>(p.lo)));
+    p.hi = static_cast<int32_t>(same(static_cast<uint32_t>(p.hi))), p.min = static_cast<int32_t>(same(static_cast<uint32_t>(p.min)));
+    p.n = same(p.n);
     const bool fits = p.n > 0 && p.n <= kHeld;
     if (fits) count_parts(a.parts, mine_cells, p, s);
     if (blockIdx.x == 0) {                         // for the next launch
         RowPlan &out = a.plans[r];
         for (uint32_t i = threadIdx.x; i < kCells; i += blockDim.x) out.cells.w[i] = cells.w[i], out.cells.count[i] = cells.count[i];
-        if (threadIdx.x == 0) out.plan = p;
+        if (threadIdx.x == 0) out.plan = plan;
         if (fits && threadIdx.x < static_cast<uint32_t>(a.parts)) {
             uint32_t at = 0;
             for (uint32_t i = 0; i < threadIdx.x; ++i) at += s.part_count[i];
@@ -845,10 +904,6 @@ __global__ __launch_bounds__(kWaves * 64) void sample_border_kernel(SampleArgs a
         }
     }
     if (!fits || s.part_count[blockIdx.x] == 0) return;
-    const int64_t j0 = static_cast<int64_t>(blockIdx.x) * a.part + wave * SEGS * kSeg;
-    float z[SEGS][kEach];
-#pragma unroll
-    for (int i = 0; i < SEGS; ++i) load_seg<FMT>(static_cast<const char *>(a.logits) + r * a.ld * kSize, j0 + i * kSeg, a.vocab, z[i], -kInf);
     // nearly all entries are outside of what the wanted cells span: looked at in 32 bits, with a margin
     float low = -kInf, high = kInf;
     if (h.c8 > 0) {
@@ -944,7 +999,14 @@ __global__ __launch_bounds__(kWaves * 64) void sample_pick_kernel(SampleArgs a) 
         for (int by_count = p.k_on; by_count >= (p.p_on ? 0 : 1); --by_count) {
             const double sum = by_count ? 0 : static_cast<double>(h.top_p) * w_kept;
             Border b = by_count ? p.k : p.p;
-            if (!by_count && p.lo != p.hi) b = border_of(t.cells, false, 0, sum);
+            if (!by_count && p.lo != p.hi) {
+                if (wave == 0) {
+                    b = border_of(t.cells, false, 0, sum);
+                    if (lane == 0) t.border = b;
+                }
+                __syncthreads();
+                b = same(t.border);
+            }
             const uint64_t o = keep_from(g, t, sc, b, by_count != 0, h.k, sum, w_kept);
             from = o > from ? o : from;
             border = b.bin < border ? b.bin : border;
