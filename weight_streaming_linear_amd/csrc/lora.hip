@@ -20,9 +20,14 @@ namespace {
 // 70 for 256; requests: 26 and 23, 42 and 29.
 constexpr int64_t kFewRows = 8192;         // m * rank
 bool few(int64_t m, int64_t rank) { return m * rank <= kFewRows; }
-constexpr int kPart = 512;                 // least elements of k in a part
+// Least elements of k in a part; more only add partial sums to write and read.  512 against 1024, in us: 48 tokens, 7168 to
+// 5120, rank 16: 9.0 and 7.6; 128 tokens of 5120: 15.1 and 13.5; 256 tokens, rank 64: 37.7 and 33.0.
+constexpr int kPart = 1024;
+// Parts at most: 8, 16 and 32 are as good (one token, 14336 to 5120, rank 64: 13.3, 12.6 and 14.4).
 constexpr int64_t kMostParts = 16;
-constexpr int64_t kGroups = 512;           // workgroups of 16 tokens that keep the chip busy
+// Workgroups of 16 tokens that keep the chip busy: one a CU.  128, 256 and 512: 600 tokens, 5120 to 5120, rank 16: 19.4, 17.8 and
+// 17.8; 2048: 36.4, 32.9 and 34.0; 1024 of 14336, rank 64: 82, 69 and 81.
+constexpr int64_t kGroups = 256;
 
 struct LoraArgs {
     const uint16_t *a, *b, *x;
@@ -354,16 +359,15 @@ __global__ __launch_bounds__(256) void expand_many_kernel(LoraArgs a) {
     }
 }
 
-// Parts of k: few tokens, as many as there are kPart elements; more, until there are enough workgroups.
+// Parts of k: as many as there are kPart elements, of more tokens only until there are enough workgroups.
 int64_t parts_of(int64_t m, int64_t rank, int64_t k) {
-    int64_t most = kMostParts, least = kPart;
+    int64_t most = kMostParts;
     if (!few(m, rank)) {
         const int64_t tiles = (m + 15) / 16;
         most = (kGroups + tiles - 1) / tiles;
         if (most > kMostParts) most = kMostParts;
-        least = 1024;                              // at least eight waves have something to do
     }
-    const int64_t parts = (k + least - 1) / least;
+    const int64_t parts = (k + kPart - 1) / kPart;
     return parts < most ? parts : most;
 }
 
@@ -402,8 +406,7 @@ int launch_lora(const void *d_a, const void *d_b, int64_t n_adapters, int64_t ra
     a.n_adapters = n_adapters, a.n_out = n_out, a.k = k, a.m = m, a.ldx = ldx, a.ld_base = ld_base, a.ld_out = ld_out;
     a.rank = static_cast<int32_t>(rank);
     const int64_t parts = parts_of(m, rank, k);
-    const int64_t step = few(m, rank) ? kPart : 1024;
-    a.part = ((k + parts - 1) / parts + step - 1) / step * step;
+    a.part = ((k + parts - 1) / parts + kPart - 1) / kPart * kPart;
     a.parts = static_cast<int32_t>((k + a.part - 1) / a.part);
     const int64_t vec = fmt == WSL_OUT_F32 ? 4 : 8;
     a.wide = ld_base % vec == 0 && ld_out % vec == 0 && reinterpret_cast<uintptr_t>(base) % 16 == 0 &&

@@ -30,7 +30,16 @@ constexpr int kCells = 256, kList = 256;
 constexpr int kWaves = 8, kPartSegs = 16;      // waves of a workgroup, and segments of a part, at most
 constexpr int kMostParts = 256, kFewParts = 16;
 constexpr int kHeld = 8192;                    // orders that a workgroup holds: a short row, or a long one's list
+// Entries of a short row, at most.  Against long rows' launches, in us (top-k 50 and top-p 0.9, as all figures here): 8192
+// entries, 1, 64 and 512 rows: 20, 22 and 44, the others 24, 26 and 51.
 constexpr int kChunk = kHeld;
+// Short rows of up to 4096 entries beyond which four waves take one instead of eight, so that all have room.  Eight and four,
+// 4000 entries: 15 and 18 for 1 row, 16.6 and 19.2 for 256, 31 and 22 for 512, 58 and 42 for 1024.
+constexpr int64_t kManyRows = 256;
+// Parts of all rows up to which a part is 8 segments and not 16.  8 and 16: 32000 entries, 1, 64, 128 and 256 rows (1024 parts):
+// 25.5 and 30.6, 28 and 33, 32.6 and 35.4, 49 and 45; 65536, 64 rows (512) and 128: 33.5 and 34.7, 50 and 44; 131072, 1, 32
+// (512) and 64: 28 and 31, 35.9 and 36.5, 54 and 45.7.
+constexpr int64_t kFill = 512;
 constexpr double kPartUnit = 4294967296.0;     // 2^32: whole numbers to a cell's unit; 2^14 entries of it fit 48 bits
 constexpr float kInf = __builtin_huge_valf();
 
@@ -1114,12 +1123,16 @@ __global__ __launch_bounds__(256) void sample_probs_kernel(SampleArgs a) {
     }
 }
 
-// Segments of a part: eight parts a row and more, of up to 16384 entries.
-int64_t part_of(int64_t vocab) { return vocab <= 65536 ? 4 * kSeg : (vocab <= 131072 ? 8 * kSeg : 16 * kSeg); }
+// Entries of a part, a segment or two of them to each of eight waves.
+int64_t parts_of(int64_t vocab, int64_t segs) { return (vocab + segs * kSeg - 1) / (segs * kSeg); }
+int64_t segs_of(int64_t n_rows, int64_t vocab) {
+    const int64_t parts = parts_of(vocab, kWaves);
+    return parts <= kFewParts && n_rows * parts <= kFill ? kWaves : kPartSegs;
+}
 
 template <int FMT, int SEGS, bool FEW>
 void go_long(const SampleArgs &a, unsigned rows, hipStream_t s) {
-    const dim3 grid(static_cast<unsigned>(a.parts), rows), block(static_cast<unsigned>(a.part / (SEGS * kSeg) * 64));
+    const dim3 grid(static_cast<unsigned>(a.parts), rows), block(kWaves * 64);
     hipLaunchKernelGGL((sample_cells_kernel<FMT, SEGS>), grid, block, 0, s, a);
     const bool some = a.how.d_top_k || a.how.d_top_p || a.how.d_min_p || a.how.top_k > 0 || a.how.top_p < 1 || a.how.min_p > 0;
     if (some) hipLaunchKernelGGL((sample_border_kernel<FMT, SEGS, FEW>), grid, block, 0, s, a);
@@ -1131,28 +1144,20 @@ void go_long(const SampleArgs &a, unsigned rows, hipStream_t s) {
 template <int FMT>
 void go(const SampleArgs &a, int64_t n_rows, hipStream_t s) {
     const unsigned rows = static_cast<unsigned>(n_rows);
-    if (a.vocab <= kChunk) hipLaunchKernelGGL(sample_short_kernel<FMT>, dim3(rows), dim3(static_cast<unsigned>(a.vocab <= 4 * kSeg ? 4 : kWaves) * 64), 0, s, a);
-    else if (a.part <= kWaves * kSeg) go_long<FMT, 1, true>(a, rows, s);
+    if (a.vocab <= kChunk) hipLaunchKernelGGL(sample_short_kernel<FMT>, dim3(rows), dim3(static_cast<unsigned>(a.vocab <= 4 * kSeg && n_rows > kManyRows ? 4 : kWaves) * 64), 0, s, a);
+    else if (a.part == kWaves * kSeg) go_long<FMT, 1, true>(a, rows, s);
     else if (a.parts <= kFewParts) go_long<FMT, 2, true>(a, rows, s);
     else go_long<FMT, 2, false>(a, rows, s);
-}
-
-struct Sizes {
-    int64_t parts, part;
-    size_t row;                                    // bytes of workspace
-};
-Sizes sizes_of(int64_t vocab) {
-    Sizes z;
-    z.part = part_of(vocab);
-    z.parts = (vocab + z.part - 1) / z.part;
-    z.row = sizeof(RowOut) + sizeof(RowPlan) + static_cast<size_t>(z.parts) * (sizeof(PartHead) + kCells * sizeof(uint64_t)) + kHeld * sizeof(uint64_t);
-    return z;
 }
 
 }  // namespace
 
 size_t sample_ws_bytes(int64_t n_rows, int64_t vocab) {
-    return vocab <= kChunk ? 0 : static_cast<size_t>(n_rows) * sizes_of(vocab).row;
+    if (vocab <= kChunk) return 0;
+    // (what the shorter parts take: more rows never take less)
+    const size_t parts = static_cast<size_t>(parts_of(vocab, parts_of(vocab, kWaves) <= kFewParts ? kWaves : kPartSegs));
+    return static_cast<size_t>(n_rows) * (sizeof(RowOut) + sizeof(RowPlan) + parts * (sizeof(PartHead) + kCells * sizeof(uint64_t)) +
+                                          kHeld * sizeof(uint64_t));
 }
 
 int launch_sample(const void *logits, int zfmt, int64_t n_rows, int64_t vocab, int64_t ld, const wsl_sampling *how,
@@ -1162,13 +1167,13 @@ int launch_sample(const void *logits, int zfmt, int64_t n_rows, int64_t vocab, i
     a.vocab = vocab, a.ld = ld, a.ld_probs = ld_probs;
     if (how) a.how = *how;
     else a.how = {nullptr, nullptr, nullptr, nullptr, 1.f, 0, 1.f, 0.f};
-    const Sizes z = sizes_of(vocab);
-    a.parts = static_cast<int32_t>(z.parts), a.part = static_cast<int32_t>(z.part);
+    const int64_t segs = segs_of(n_rows, vocab), parts = parts_of(vocab, segs);
+    a.parts = static_cast<int32_t>(parts), a.part = static_cast<int32_t>(segs * kSeg);
     a.cells = static_cast<uint64_t *>(ws);
-    a.list = a.cells + n_rows * z.parts * kCells;
+    a.list = a.cells + n_rows * parts * kCells;
     a.plans = reinterpret_cast<RowPlan *>(a.list + n_rows * kHeld);
     a.heads = reinterpret_cast<PartHead *>(a.plans + n_rows);
-    a.outs = reinterpret_cast<RowOut *>(a.heads + n_rows * z.parts);
+    a.outs = reinterpret_cast<RowOut *>(a.heads + n_rows * parts);
     if (zfmt == WSL_OUT_F32) go<WSL_OUT_F32>(a, n_rows, s);
     else go<WSL_OUT_BF16>(a, n_rows, s);
     return WSL_OK;
