@@ -28,6 +28,7 @@ constexpr int64_t kMostParts = 16;
 // Workgroups of 16 tokens that keep the chip busy: one a CU.  128, 256 and 512: 600 tokens, 5120 to 5120, rank 16: 19.4, 17.8 and
 // 17.8; 2048: 36.4, 32.9 and 34.0; 1024 of 14336, rank 64: 82, 69 and 81.
 constexpr int64_t kGroups = 256;
+constexpr int kXcds = 8;
 
 struct LoraArgs {
     const uint16_t *a, *b, *x;
@@ -151,11 +152,14 @@ template <int BLOCKS, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void shrink_many_kernel(LoraArgs a) {
     __shared__ f32x4 sums[WAVES][BLOCKS][64];
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
-    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * 16;
+    const uint32_t at = (blockIdx.x % kXcds) * (gridDim.x / kXcds) + blockIdx.x / kXcds;
+    const uint32_t tiles = static_cast<uint32_t>((a.m + 15) / 16), part = at / tiles;
+    if (part >= static_cast<uint32_t>(a.parts)) return;
+    const int64_t t0 = static_cast<int64_t>(at - part * tiles) * 16;
     const bool there = t0 + col < a.m;
     const int64_t mine = there ? t0 + col : a.m - 1;
-    const int32_t id = there ? adapter_of(a, mine, blockIdx.y == 0 && tid < 16) : -1;
-    const int64_t k0 = blockIdx.y * a.part, k1 = k0 + a.part < a.k ? k0 + a.part : a.k;
+    const int32_t id = there ? adapter_of(a, mine, part == 0 && tid < 16) : -1;
+    const int64_t k0 = part * a.part, k1 = k0 + a.part < a.k ? k0 + a.part : a.k;
     const uint16_t *x = a.x + mine * a.ldx + g * 8;
     uint32_t todo = static_cast<uint32_t>(__ballot(id >= 0)) & 0xffffu;
     while (todo) {
@@ -234,7 +238,7 @@ __global__ __launch_bounds__(WAVES * 64) void shrink_many_kernel(LoraArgs a) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if ((same[p] >> (4 * g + i) & 1u) && 16 * b + col < a.rank)
-                        a.h[(blockIdx.y * a.m + t0 + 4 * g + i) * a.rank + 16 * b + col] = v[i];
+                        a.h[(part * a.m + t0 + 4 * g + i) * a.rank + 16 * b + col] = v[i];
             }
             __syncthreads();
         }
@@ -268,11 +272,11 @@ __device__ __forceinline__ int output_of(int q, int i) {
 template <int FMT, int STEPS, int PERIOD>
 __global__ __launch_bounds__(256) void expand_many_kernel(LoraArgs a) {
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
-    const int64_t t0 = static_cast<int64_t>(blockIdx.y) * 64 + wave * 16;
-    if (t0 >= a.m) return;
+    const int64_t t0 = static_cast<int64_t>(blockIdx.y) * 16;
+    __shared__ u32x4 shared[STEPS][64];
     constexpr int kWide = FMT == WSL_OUT_F32 ? 4 : 2, kSize = FMT == WSL_OUT_F32 ? 4 : 2;
     const bool there = t0 + col < a.m;
-    const int64_t t = there ? t0 + col : a.m - 1, n0 = static_cast<int64_t>(blockIdx.x) * (kTiles * 64);
+    const int64_t t = there ? t0 + col : a.m - 1, n0 = (static_cast<int64_t>(blockIdx.x) * 4 + wave) * (kTiles * 64);
     u32x4 v[kTiles][kWide];
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) {
@@ -286,23 +290,30 @@ __global__ __launch_bounds__(256) void expand_many_kernel(LoraArgs a) {
     const int32_t id = there ? adapter_of(a, t, false) : -1;
     const uint32_t some = static_cast<uint32_t>(__ballot(id >= 0)) & 0xffffu;
     if (!some && a.base == a.out) return;
-    u32x4 h[STEPS];
-    int at[STEPS];
     const float scale = id >= 0 && a.scales ? a.scales[id] : 1.f;
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
+    for (int s = wave; s < STEPS; s += 4) {
         const int slot = 32 * s + 8 * g, p = slot / a.rank;
-        at[s] = p < 3 || PERIOD < STEPS ? slot - p * a.rank : 0;
         float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         if (id >= 0 && p < 3)
             for (int c = 0; c < a.parts; ++c) {
-                const f32x4 *from = reinterpret_cast<const f32x4 *>(a.h + (c * a.m + t) * a.rank + at[s]);
+                const f32x4 *from = reinterpret_cast<const f32x4 *>(a.h + (c * a.m + t) * a.rank + slot - p * a.rank);
                 const f32x4 lo = from[0], hi = from[1];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[e] += lo[e], x[4 + e] += hi[e];
             }
+        u32x4 w;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) h[s][e] = pack_bf16x2(third(scale * x[2 * e], p), third(scale * x[2 * e + 1], p));
+        for (int e = 0; e < 4; ++e) w[e] = pack_bf16x2(third(scale * x[2 * e], p), third(scale * x[2 * e + 1], p));
+        shared[s][lane] = w;
+    }
+    __syncthreads();
+    u32x4 h[STEPS];
+    int at[STEPS];
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+        const int slot = 32 * s + 8 * g, p = slot / a.rank;
+        at[s] = p < 3 || PERIOD < STEPS ? slot - p * a.rank : 0;
+        h[s] = shared[s][lane];
     }
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) {
@@ -378,7 +389,7 @@ void go_expand(const LoraArgs &a, hipStream_t s) {
                            dim3(256), 0, s, a);
         return;
     }
-    const dim3 grid(static_cast<unsigned>((a.n_out + kTiles * 64 - 1) / (kTiles * 64)), static_cast<unsigned>((a.m + 63) / 64));
+    const dim3 grid(static_cast<unsigned>((a.n_out + kTiles * 256 - 1) / (kTiles * 256)), static_cast<unsigned>((a.m + 15) / 16));
     const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, a); };
     const int rank = a.rank, steps = (3 * rank + 31) / 32;
     if (rank <= 8) go(expand_many_kernel<FMT, 1, 1>);
@@ -419,7 +430,7 @@ int launch_lora(const void *d_a, const void *d_b, int64_t n_adapters, int64_t ra
         else if (rank <= 64) hipLaunchKernelGGL(shrink_few_kernel<16>, grid, dim3(256), 0, s, a);
         else hipLaunchKernelGGL(shrink_few_kernel<32>, grid, dim3(256), 0, s, a);
     } else {
-        const dim3 grid(static_cast<unsigned>((m + 15) / 16), static_cast<unsigned>(a.parts));
+        const dim3 grid(static_cast<unsigned>(((m + 15) / 16 * a.parts + kXcds - 1) / kXcds * kXcds));
         if (rank <= 16) hipLaunchKernelGGL((shrink_many_kernel<1, 8>), grid, dim3(512), 0, s, a);
         else if (rank <= 32) hipLaunchKernelGGL((shrink_many_kernel<2, 8>), grid, dim3(512), 0, s, a);
         else if (rank <= 64) hipLaunchKernelGGL((shrink_many_kernel<4, 8>), grid, dim3(512), 0, s, a);
