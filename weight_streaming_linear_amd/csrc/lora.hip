@@ -145,22 +145,52 @@ __global__ __launch_bounds__(256) void expand_few_kernel(LoraArgs a) {
 // ------------------------------------------------------------------ more tokens
 __device__ __forceinline__ bf16x8 frag(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
 
-// blockIdx: (16 tokens, part of k).  The tokens are the rows, 16 rows of A the columns; the waves take 128
-// elements of k in turn, all of their loads made before the first product, and are added up in LDS, so that x is
-// read in long pieces and one part is enough where tokens are many.
+// 16 rows of C * 8 elements, by one wave: from C lanes a row, as they are loaded, to the operands of C / 4 products (a row
+// to 16 lanes; as loads those would be 64 pieces of 16 bytes, which take four times as long to ask for).
+template <int C>
+struct Turn {
+    static constexpr int kLoads = C / 4, kRows = 64 / C;       // rows of a load
+    u32x4 at[16 * (C + 1)];                        // a row and 16 bytes: no two rows in the same banks
+    static __device__ __forceinline__ int row(int load) { return load * kRows + static_cast<int>(threadIdx.x & 63) / C; }
+    static __device__ __forceinline__ int element() { return static_cast<int>(threadIdx.x) % C * 8; }
+    __device__ __forceinline__ void operator()(u32x4 (&v)[kLoads]) {
+        const int lane = static_cast<int>(threadIdx.x & 63), col = lane & 15, g = lane >> 4;
+        // (the wave's own, in order: what was read before is out before this comes in)
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) at[row(i) * (C + 1) + lane % C] = v[i];
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+        for (int s = 0; s < kLoads; ++s) v[s] = at[col * (C + 1) + 4 * s + g];
+    }
+};
+
+// A workgroup: 16 tokens and a part of k, those of an XCD in turn so that its L2 holds what they have of A.  The tokens
+// are the rows, 16 rows of A the columns; the waves take 128 elements of k in turn, all of their loads made
+// before the first product, and are added up in LDS, so that one part is enough where tokens are many.
 template <int BLOCKS, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void shrink_many_kernel(LoraArgs a) {
-    __shared__ f32x4 sums[WAVES][BLOCKS][64];
-    const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
+    __shared__ union {
+        Turn<16> turn[WAVES];
+        f32x4 sums[WAVES][BLOCKS][64];
+    } lds;
+    const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, col = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t at = (blockIdx.x % kXcds) * (gridDim.x / kXcds) + blockIdx.x / kXcds;
     const uint32_t tiles = static_cast<uint32_t>((a.m + 15) / 16), part = at / tiles;
     if (part >= static_cast<uint32_t>(a.parts)) return;
     const int64_t t0 = static_cast<int64_t>(at - part * tiles) * 16;
     const bool there = t0 + col < a.m;
-    const int64_t mine = there ? t0 + col : a.m - 1;
-    const int32_t id = there ? adapter_of(a, mine, part == 0 && tid < 16) : -1;
+    const int32_t id = there ? adapter_of(a, t0 + col, part == 0 && tid < 16) : -1;
     const int64_t k0 = part * a.part, k1 = k0 + a.part < a.k ? k0 + a.part : a.k;
-    const uint16_t *x = a.x + mine * a.ldx + g * 8;
+    const auto token = [&](int row) { return t0 + row < a.m ? t0 + row : a.m - 1; };
+    const uint16_t *x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = a.x + token(4 * i + g) * a.ldx + col * 8;
+    const uint32_t lane_at = static_cast<uint32_t>(g * a.k + col * 8) * 2;     // k < 2^22
     uint32_t todo = static_cast<uint32_t>(__ballot(id >= 0)) & 0xffffu;
     while (todo) {
         // two adapters at a time: most tiles where requests meet have two
@@ -175,63 +205,67 @@ __global__ __launch_bounds__(WAVES * 64) void shrink_many_kernel(LoraArgs a) {
                 todo &= ~same[p];
             }
         }
-        // rows behind the rank are read again and not kept
-        const uint16_t *w[2][BLOCKS];
-#pragma unroll
-        for (int p = 0; p < 2; ++p)
-#pragma unroll
-            for (int b = 0; b < BLOCKS; ++b)
-                w[p][b] = a.a + (static_cast<int64_t>(which[p]) * a.rank + (16 * b + col < a.rank ? 16 * b + col : 0)) * a.k + g * 8;
         f32x4 acc[2][BLOCKS];
 #pragma unroll
         for (int b = 0; b < BLOCKS; ++b) acc[0][b] = acc[1][b] = f32x4{0, 0, 0, 0};
         int64_t kk = k0 + wave * 128;
         for (; kk + 128 <= k1; kk += 128 * WAVES) {
-            u32x4 xv[4], wv[BLOCKS][4];
+            constexpr int kOnce = BLOCKS < 2 ? BLOCKS : 2;     // (more have no room in the registers)
+            u32x4 xv[4], wv[kOnce][4];
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                xv[s] = *reinterpret_cast<const u32x4 *>(x + kk + 32 * s);
+            for (int i = 0; i < 4; ++i) xv[i] = *reinterpret_cast<const u32x4 *>(x[i] + kk);
 #pragma unroll
-                for (int b = 0; b < BLOCKS; ++b) wv[b][s] = *reinterpret_cast<const u32x4 *>(w[0][b] + kk + 32 * s);
-            }
+            for (int p = 0; p < 2; ++p) {
+                if (!same[p]) continue;
+                // rows behind the rank (8 of 16, or blocks of them) are read again and not kept
+                const char *w = reinterpret_cast<const char *>(a.a + static_cast<int64_t>(which[p]) * a.rank * a.k + kk);
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
+                for (int b0 = 0; b0 < BLOCKS; b0 += kOnce) {
 #pragma unroll
-                for (int b = 0; b < BLOCKS; ++b)
-                    acc[0][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(xv[s]), frag(wv[b][s]), acc[0][b], 0, 0, 0);
-            if (same[1]) {
+                    for (int b = 0; b < kOnce; ++b)
 #pragma unroll
-                for (int s = 0; s < 4; ++s)
+                        for (int i = 0; i < 4; ++i) {
+                            const int row = 16 * (b0 + b) + 4 * i;
+                            wv[b][i] = *reinterpret_cast<const u32x4 *>(w + (row < a.rank ? row : 0) * a.k * 2 + lane_at);
+                        }
+                    if (p == 0 && b0 == 0) lds.turn[wave](xv);
 #pragma unroll
-                    for (int b = 0; b < BLOCKS; ++b)
-                        acc[1][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            frag(xv[s]), frag(*reinterpret_cast<const u32x4 *>(w[1][b] + kk + 32 * s)), acc[1][b], 0, 0, 0);
+                    for (int b = 0; b < kOnce; ++b) {
+                        lds.turn[wave](wv[b]);
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)
+                            acc[p][b0 + b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(xv[s]), frag(wv[b][s]), acc[p][b0 + b], 0, 0, 0);
+                    }
+                }
             }
         }
-        for (; kk < k1; kk += 32) {                // fewer than 128 left: this wave's alone
-            u32x4 xv = {0, 0, 0, 0};
+        for (; kk < k1; kk += 32) {                // fewer than 128 left: this wave's alone, and read as it is needed
             const bool in = kk + g * 8 < k1;
-            if (in) xv = *reinterpret_cast<const u32x4 *>(x + kk);
+            u32x4 xv = {0, 0, 0, 0};
+            if (in) xv = *reinterpret_cast<const u32x4 *>(a.x + token(col) * a.ldx + kk + g * 8);
 #pragma unroll
-            for (int p = 0; p < 2; ++p)
+            for (int p = 0; p < 2; ++p) {
+                const uint16_t *w = a.a + static_cast<int64_t>(which[p]) * a.rank * a.k + kk + g * 8;
 #pragma unroll
                 for (int b = 0; b < BLOCKS; ++b) {
                     u32x4 wv = {0, 0, 0, 0};
-                    if (in) wv = *reinterpret_cast<const u32x4 *>(w[p][b] + kk);
+                    if (in) wv = *reinterpret_cast<const u32x4 *>(w + (16 * b + col < a.rank ? 16 * b + col : 0) * a.k);
                     acc[p][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(xv), frag(wv), acc[p][b], 0, 0, 0);
                 }
+            }
         }
+        __syncthreads();                           // the sums lie where the waves turn their rows
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
             if (!same[p]) continue;
 #pragma unroll
-            for (int b = 0; b < BLOCKS; ++b) sums[wave][b][lane] = acc[p][b];
+            for (int b = 0; b < BLOCKS; ++b) lds.sums[wave][b][lane] = acc[p][b];
             __syncthreads();
             for (int b = wave; b < BLOCKS; b += WAVES) {
-                f32x4 v = sums[0][b][lane];
+                f32x4 v = lds.sums[0][b][lane];
 #pragma unroll
                 for (int q = 1; q < WAVES; ++q) {
-                    const f32x4 u = sums[q][b][lane];
+                    const f32x4 u = lds.sums[q][b][lane];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) v[i] += u[i];
                 }
@@ -273,7 +307,9 @@ template <int FMT, int STEPS, int PERIOD>
 __global__ __launch_bounds__(256) void expand_many_kernel(LoraArgs a) {
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
     const int64_t t0 = static_cast<int64_t>(blockIdx.y) * 16;
+    constexpr bool kTurned = PERIOD > 1 && PERIOD < STEPS;     // rows of B are PERIOD * 32 elements
     __shared__ u32x4 shared[STEPS][64];
+    __shared__ Turn<PERIOD * 4> turn[kTurned ? 4 : 1];
     constexpr int kWide = FMT == WSL_OUT_F32 ? 4 : 2, kSize = FMT == WSL_OUT_F32 ? 4 : 2;
     const bool there = t0 + col < a.m;
     const int64_t t = there ? t0 + col : a.m - 1, n0 = (static_cast<int64_t>(blockIdx.x) * 4 + wave) * (kTiles * 64);
@@ -328,11 +364,21 @@ __global__ __launch_bounds__(256) void expand_many_kernel(LoraArgs a) {
             todo &= ~static_cast<uint32_t>(__ballot(id == which));
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const int64_t row = n + output_of<FMT>(q, col);
-                const uint16_t *w = a.b + (which * a.n_out + (row < a.n_out ? row : a.n_out - 1)) * a.rank;
+                const auto row_of = [&](int i) {
+                    const int64_t row = n + output_of<FMT>(q, i);
+                    return a.b + (which * a.n_out + (row < a.n_out ? row : a.n_out - 1)) * a.rank;
+                };
                 u32x4 b[PERIOD];
+                if constexpr (kTurned) {
+                    using T = Turn<PERIOD * 4>;
 #pragma unroll
-                for (int s = 0; s < PERIOD; ++s) b[s] = *reinterpret_cast<const u32x4 *>(w + at[s]);
+                    for (int s = 0; s < PERIOD; ++s) b[s] = *reinterpret_cast<const u32x4 *>(row_of(T::row(s)) + T::element());
+                    turn[wave](b);
+                } else {
+                    const uint16_t *w = row_of(col);
+#pragma unroll
+                    for (int s = 0; s < PERIOD; ++s) b[s] = *reinterpret_cast<const u32x4 *>(w + at[s]);
+                }
                 f32x4 d = {0, 0, 0, 0};
 #pragma unroll
                 for (int s = 0; s < STEPS; ++s)
