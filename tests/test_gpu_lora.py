@@ -96,6 +96,21 @@ def test_an_adapter_has_no_part_in_other_rows(m):
     assert out[none].view(torch.int32).equal(base[none].view(torch.int32))
 
 
+@pytest.mark.parametrize("rank", [40, 64, 128])
+@pytest.mark.parametrize("n_out", [150, 1024])
+def test_high_ranks_of_many_tokens_apart(rank, n_out):
+    """Six adapters among every 16 tokens, two of them and some rows full of NaN: the others are as before."""
+    import torch
+    base, x, a, b, ids, scales = _case(rank, 260, 1160, n_out, rank, 6, "float32")
+    want = wsl.lora_add(base, x, a, b, ids, scales)
+    _check(base, x, a, b, ids, scales, want)
+    a[4], b[5] = float("nan"), float("nan")
+    x[ids == 3] = float("nan")
+    fine = (ids < 3).cpu()
+    got = wsl.lora_add(base, x, a, b, ids, scales)
+    assert got[fine].equal(want[fine]) and got[(ids > 2).cpu()].isnan().all()
+
+
 @pytest.mark.parametrize("m", [5, 90, 1100])
 def test_bad_ids_are_reported_and_left_out(m):
     import torch

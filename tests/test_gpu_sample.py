@@ -225,6 +225,26 @@ def test_many_rows_and_strides():
     assert one.item() == tokens[5].item()
 
 
+@pytest.mark.parametrize("n,vocab", [(300, 3900), (300, 8000), (200, 32001), (70, 100003)])
+def test_many_rows_at_once_are_as_few(n, vocab):
+    """So many rows that waves or parts are others: probabilities as of one row (both right to 2^-32, then rounded),
+    and tokens inside of them."""
+    import torch
+    z, u = _logits(vocab, n, vocab, "float32", peaks=2)
+    how = dict(top_k=400, top_p=0.93, temperature=0.8)
+    probs = torch.empty((n, vocab), device="cuda")
+    tokens = wsl.sample_logits(z, u, probs=probs, **how)
+    assert (probs.gather(1, tokens.long()[:, None]) > 0).all()
+    for r in (0, n // 2, n - 1):
+        one = torch.empty((1, vocab), device="cuda")
+        wsl.sample_logits(z[r:r + 1], u[r:r + 1], probs=one, **how)
+        assert (one[0] > 0).equal(probs[r] > 0)
+        assert ((one[0] - probs[r]).abs() <= 2.0 ** -23 * 1.001 * one[0]).all()
+    _check(z[:3], u[:3], **how)
+    for r in (0, n - 1):
+        _check(z[r:r + 1], u[r:r + 1], **how)
+
+
 def test_a_long_row():
     import torch
     z, u = _logits(8, 1, 1 << 22, "bfloat16")

@@ -6,13 +6,20 @@
 // sequence b lacks and off_b the sum of need over those before it, page i of b is
 // free[n_free - 1 - off_b - i]: one running sum over the sequences, after which every token finds its
 // own slot without looking at another.
+//
+// Bound: latency, of one workgroup's loads one after the other; the bytes (16 to 20 a token) are nothing.
+// Measured: grow 3 us for one sequence, 4.3 for 256 of 5 tokens; 4.3 and 4.6 in two launches for
+// 64 prompts of 166,500 tokens together; trim 4.3 and 6.9.
 #include "device_common.h"
 
 namespace wsl {
 namespace {
 
 constexpr int kMost = 1024;            // threads of the workgroup that goes over the sequences
-constexpr int64_t kOneLaunch = 4096;   // tokens that it sees to itself
+// Tokens that it sees to itself.  That and a second launch for them, grow and trim together, in us: 64 sequences, 64 tokens
+// 10.3 and 11.6, 1024 12.5 and 12.9, 4096 15.2 and 13.2, 16384 25 and 13; 1024 sequences, 1024 tokens 15.4 and 18.9, 4096 18.5 and
+// 19.1, 8192 22.8 and 18.9.  (Outside of graphs, a launch costs the host 2.7 us besides.)
+constexpr int64_t kOneLaunch = 4096;
 
 // What the tokens of a sequence need to know.
 struct Row {

@@ -21,6 +21,9 @@
 // The first two read the row, the second mostly from the caches.  A workgroup passes through most of this
 // code once, so what bounds it besides the loads is how fast instructions come in: loops over LDS are
 // kept rolled.
+//
+// Measured, top-k and top-p of each row's own: 64 rows of 151937 fp32 entries (38.9 MB, 7.6 us as a copy) 52 us: cells 17, border
+// 15, pick 20; one row of 32000, 25.5: 5.7, 11.4 and 11; 40 rows of 32000 with their probabilities 43: 7.0, 12.6, 14.5 and 7.9.
 #include "row_scan.h"
 
 namespace wsl {
@@ -610,8 +613,9 @@ __global__ __launch_bounds__(kWaves * 64) void sample_short_kernel(SampleArgs a)
 }
 
 // ------------------------------------------------------------------ long rows
-// Cells of one part: blockIdx (part, row), a wave SEGS segments of it.  Bound by the 64-bit arithmetic, about 16
-// instructions an entry (an exponential in 32 bits would take as many and leave 2^-22 of a weight).
+// Cells of one part: blockIdx (part, row), a wave SEGS segments of it.  Bound by the loads (10.5 us of 64 rows' 17) and
+// the 64-bit arithmetic and atomics in LDS behind them, about 16 instructions an entry (an exponential in 32 bits would
+// take as many and leave 2^-22 of a weight).
 template <int FMT, int SEGS>
 __global__ __launch_bounds__(kWaves * 64) void sample_cells_kernel(SampleArgs a) {
     __shared__ uint64_t cells[kCells];
