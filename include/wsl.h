@@ -601,8 +601,8 @@ typedef struct wsl_sampling {
  * d_u        device fp32 [n_rows]; may be NULL where d_tokens is.
  * d_tokens   device int32 [n_rows] or NULL.     d_probs  device fp32 [n_rows][ld_probs] or NULL; one of
  *            them is needed.  Entries of a row past vocab are not written.
- * d_ws       device workspace, 16-byte aligned, of sample_logits_workspace_bytes (none where that is 0).
- *            Its contents on entry do not matter.  Calls that share a workspace must not overlap.
+ * d_ws       device workspace, 16-byte aligned, of sample_logits_workspace_bytes (none where that is 0; more
+ *            rows never take less).  Its contents on entry do not matter.  Calls that share a workspace must not overlap.
  */
 size_t sample_logits_workspace_bytes(int64_t n_rows, int64_t vocab);
 int sample_logits(const void *d_logits, int zfmt, int64_t n_rows, int64_t vocab, int64_t ld,
@@ -625,8 +625,8 @@ int sample_logits(const void *d_logits, int zfmt, int64_t n_rows, int64_t vocab,
  * three bf16 numbers, 24 bits; there an infinity in B gives a NaN.)  The sum with base is rounded once to
  * fmt.  Rows without an adapter are copied.  An adapter has no part in other tokens' rows, whatever
  * it holds.  Deterministic.
- * d_ws      device workspace, 16-byte aligned, of lora_add_workspace_bytes (A x in parts of k).  Its
- *           contents on entry do not matter.  Calls that share a workspace must not overlap.
+ * d_ws      device workspace, 16-byte aligned, of lora_add_workspace_bytes (A x in parts of k; more tokens
+ *           never take less).  Its contents on entry do not matter.  Calls that share a workspace must not overlap.
  */
 size_t lora_add_workspace_bytes(int64_t m, int64_t rank, int64_t k);
 int lora_add(const void *d_a, const void *d_b, int64_t n_adapters, int64_t rank, int64_t n_out, int64_t k,

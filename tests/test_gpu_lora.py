@@ -96,6 +96,25 @@ def test_an_adapter_has_no_part_in_other_rows(m):
     assert out[none].view(torch.int32).equal(base[none].view(torch.int32))
 
 
+@pytest.mark.parametrize("m", [(1 << 19) + 17, 1 << 20])
+def test_the_most_tokens(m):
+    """Whole numbers, and a workspace with a guard behind it."""
+    import torch
+    say(f"lora m={m}")
+    gen = torch.Generator(device="cuda").manual_seed(m)
+    r = lambda *s: torch.randint(-8, 9, s, generator=gen, device="cuda")
+    x, a, b, base = r(m, 16), r(2, 8, 16), r(2, 24, 8), r(m, 24)
+    ids = torch.randint(-1, 2, (m,), generator=gen, device="cuda", dtype=torch.int32)
+    bf, need = torch.bfloat16, wsl.lora_add_workspace_bytes(m, 8, 16)
+    ws = torch.full((need + 64,), 77, dtype=torch.uint8, device="cuda")
+    out = wsl.lora_add(base.float(), x.to(bf), a.to(bf), b.to(bf), ids, workspace=ws[:need])
+    want = base.float()
+    for i in range(2):
+        y = (x.float() @ a[i].float().t().contiguous()) @ b[i].float().t().contiguous()
+        want = torch.where((ids == i)[:, None], want + y, want)
+    assert out.equal(want) and (ws[need:] == 77).all()
+
+
 @pytest.mark.parametrize("rank", [40, 64, 128])
 @pytest.mark.parametrize("n_out", [150, 1024])
 def test_high_ranks_of_many_tokens_apart(rank, n_out):

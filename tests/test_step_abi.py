@@ -208,3 +208,16 @@ def test_validation_under_sanitizers(tmp_path):
                     "-fno-sanitize-recover=all", *srcs, "-o", exe], check=True)
     r = subprocess.run([exe], capture_output=True, text=True)
     assert r.returncode == 0, r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("rank", [8, 16, 40, 64, 128])
+@pytest.mark.parametrize("k", [8, 1024, 5120, 16384, 1 << 20])
+def test_a_workspace_for_many_tokens_serves_fewer(rank, k):
+    sizes = [wsl.lora_add_workspace_bytes(m, rank, k) for m in [*range(1, 3000), 4096, 5000, 70000, 1 << 20]]
+    assert sizes == sorted(sizes) and sizes[0] >= 4 * rank
+
+
+@pytest.mark.parametrize("vocab", [8193, 32000, 65536, 131072, 131073, 151937])
+def test_a_workspace_for_many_rows_serves_fewer(vocab):
+    sizes = [wsl.sample_logits_workspace_bytes(n, vocab) for n in range(1, 300)]
+    assert sizes == sorted(sizes)

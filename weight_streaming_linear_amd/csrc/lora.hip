@@ -31,6 +31,7 @@ constexpr int64_t kMostParts = 16;
 // 14.9; 2048: 29.7, 28.6 and 30.3; 1024 of 14336, rank 64: 42, 37 and 40.
 constexpr int64_t kGroups = 256;
 constexpr int kXcds = 8;
+constexpr int64_t kMostTiles = 32768;      // of 16 tokens along a grid's y, which ends at 65535
 
 struct LoraArgs {
     const uint16_t *a, *b, *x;
@@ -311,7 +312,8 @@ __device__ __forceinline__ int output_of(int q, int i) {
 template <int FMT, int STEPS, int PERIOD>
 __global__ __launch_bounds__(256) void expand_many_kernel(LoraArgs a) {
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
-    const int64_t t0 = static_cast<int64_t>(blockIdx.y) * 16;
+    const int64_t t0 = (static_cast<int64_t>(blockIdx.z) * kMostTiles + blockIdx.y) * 16;
+    if (t0 >= a.m) return;
     constexpr bool kTurned = PERIOD > 1 && PERIOD < STEPS;     // rows of B are PERIOD * 32 elements
     __shared__ u32x4 shared[STEPS][64];
     __shared__ Turn<PERIOD * 4> turn[kTurned ? 4 : 1];
@@ -440,7 +442,9 @@ void go_expand(const LoraArgs &a, hipStream_t s) {
                            dim3(256), 0, s, a);
         return;
     }
-    const dim3 grid(static_cast<unsigned>((a.n_out + kTiles * 256 - 1) / (kTiles * 256)), static_cast<unsigned>((a.m + 15) / 16));
+    const int64_t tiles = (a.m + 15) / 16;
+    const dim3 grid(static_cast<unsigned>((a.n_out + kTiles * 256 - 1) / (kTiles * 256)), static_cast<unsigned>(tiles < kMostTiles ? tiles : kMostTiles),
+                    static_cast<unsigned>((tiles + kMostTiles - 1) / kMostTiles));
     const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, a); };
     const int rank = a.rank, steps = (3 * rank + 31) / 32;
     if (rank <= 8) go(expand_many_kernel<FMT, 1, 1>);
@@ -455,7 +459,15 @@ void go_expand(const LoraArgs &a, hipStream_t s) {
 }  // namespace
 
 size_t lora_ws_bytes(int64_t m, int64_t rank, int64_t k) {
-    return static_cast<size_t>(parts_of(m, rank, k)) * static_cast<size_t>(m) * static_cast<size_t>(rank) * sizeof(float);
+    // At least parts_of * m, and never less for more tokens: m times all parts of k while they go one by one; from there on parts_of is
+    // below kGroups * 16 / m + 1.
+    const int64_t parts = parts_of(1, rank, k), last = kFewRows / rank;
+    int64_t sums = m * parts;
+    if (!few(m, rank)) {
+        if (sums > m + kGroups * 16) sums = m + kGroups * 16;
+        if (sums < last * parts) sums = last * parts;
+    }
+    return static_cast<size_t>(sums) * static_cast<size_t>(rank) * sizeof(float);
 }
 
 int launch_lora(const void *d_a, const void *d_b, int64_t n_adapters, int64_t rank, int64_t n_out, int64_t k,

@@ -8,8 +8,8 @@
 // own slot without looking at another.
 //
 // Bound: latency, of one workgroup's loads one after the other; the bytes (16 to 20 a token) are nothing.
-// Measured: grow 3 us for one sequence, 4.3 for 256 of 5 tokens; 4.3 and 4.6 in two launches for
-// 64 prompts of 166,500 tokens together; trim 4.3 and 6.9.
+// Measured: grow 3 us for one sequence, 6.6 for 256 of 5 tokens; 4.3 and 4.6 in two launches for
+// 64 prompts of 166,500 tokens together; trim 4.3 to 6.9.
 #include "device_common.h"
 
 namespace wsl {

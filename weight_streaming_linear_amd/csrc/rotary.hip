@@ -9,7 +9,7 @@
 //
 // Bound: the heads' bytes in and out once.  One workgroup a token: its first waves make the rot_dim / 2
 // pairs of cos and sin once for all heads, in LDS.  Measured: 2.6 us for one token of 40 and 8 heads of 128 (the launch), 35.3 for
-// 8192 tokens of 48 and 8 (235 MB: 6.7 TB/s, some of it from the caches).
+// 8192 tokens of 48 and 8 (235 MB: 6.7 TB/s).
 #include "device_common.h"
 
 namespace wsl {

@@ -22,8 +22,8 @@
 // code once, so what bounds it besides the loads is how fast instructions come in: loops over LDS are
 // kept rolled.
 //
-// Measured, top-k and top-p of each row's own: 64 rows of 151937 fp32 entries (38.9 MB, 7.6 us as a copy) 52 us: cells 17, border
-// 15, pick 20; one row of 32000, 25.5: 5.7, 11.4 and 11; 40 rows of 32000 with their probabilities 43: 7.0, 12.6, 14.5 and 7.9.
+// Measured, top-k and top-p of each row's own: 64 rows of 151937 fp32 entries (38.9 MB, 7.6 us as a copy) 52 us: cells 16.5, border
+// 15.4, pick 20; one row of 32000, 25.5: 6.2, 8.9 and 11.4; 40 bf16 rows of 32000 with their probabilities 40: 6.9, 9.5, 16 and 7.7.
 #include "row_scan.h"
 
 namespace wsl {
