@@ -15,7 +15,7 @@
 // segment that passes u * total looked through.
 //
 // A row up to kChunk entries is one workgroup's, in LDS.  Longer ones are cut into parts, a workgroup
-// each, so that few rows fill the chip too, in up to four launches: cells of each segment
+// each, so that few rows fill the chip too, in up to four launches: cells of each part
 // (relative to its own greatest entry, shifted by whole cells when they are put together); the entries
 // of the border's cells as a list; the border and the token, one workgroup a row; the probabilities.
 // The first two read the row, the second mostly from the caches.  A workgroup passes through most of this
@@ -1148,7 +1148,8 @@ void go_long(const SampleArgs &a, unsigned rows, hipStream_t s) {
 template <int FMT>
 void go(const SampleArgs &a, int64_t n_rows, hipStream_t s) {
     const unsigned rows = static_cast<unsigned>(n_rows);
-    if (a.vocab <= kChunk) hipLaunchKernelGGL(sample_short_kernel<FMT>, dim3(rows), dim3(static_cast<unsigned>(a.vocab <= 4 * kSeg && n_rows > kManyRows ? 4 : kWaves) * 64), 0, s, a);
+    const unsigned waves = a.vocab <= 4 * kSeg && n_rows > kManyRows ? 4 : kWaves;
+    if (a.vocab <= kChunk) hipLaunchKernelGGL(sample_short_kernel<FMT>, dim3(rows), dim3(waves * 64), 0, s, a);
     else if (a.part == kWaves * kSeg) go_long<FMT, 1, true>(a, rows, s);
     else if (a.parts <= kFewParts) go_long<FMT, 2, true>(a, rows, s);
     else go_long<FMT, 2, false>(a, rows, s);
