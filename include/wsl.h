@@ -586,7 +586,7 @@ typedef struct wsl_sampling {
  *   K: the first top_k entries (all where top_k <= 0);
  *   w_j = exp((z_j - max z) / temperature);
  *   P: the entries of K before which less than top_p * (sum of w over K) lies (all where top_p >= 1);
- *   Q: those with w_j >= min_p (all where min_p <= 0).
+ *   Q: those with w_j >= min_p (all where min_p <= 0; none where it is above 1).
  * The entries in K, P and Q, always the first one, are kept; the token is the least j with
  *   sum of the kept w_0 .. w_j > u * (sum of all kept), or the last kept where none is (u >= 1 or NaN),
  * and probs_j = w_j / (sum of all kept), 0 for the rest.  Where temperature is not above 0 the first

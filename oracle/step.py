@@ -142,7 +142,7 @@ def sample_ref(z, u=None, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     if top_p < 1:
         keep &= np.concatenate(([0.0], np.cumsum(w)[:-1])) < top_p * math.fsum(w)
     if min_p > 0:
-        keep &= w >= min(min_p, 1.0)
+        keep &= w >= min_p
     keep[0] = True
     assert not (np.diff(keep.astype(int)) > 0).any()       # a beginning of the order
     kept = np.sort(order[keep])

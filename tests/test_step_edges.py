@@ -1,0 +1,18 @@
+"""References and refusals of the page, position, sampling and adapter calls, without a GPU."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle.step as ref
+import weight_streaming_linear_amd as wsl
+
+
+def test_min_p_above_every_weight():
+    """By hand: no weight is 7 or more, and the first entry is kept always."""
+    z = np.array([1.0, 3.0, 3.0, 0.0])
+    assert (ref.sample_ref(z, min_p=7.0)[1] == [0, 1, 0, 0]).all() and ref.sample_ref(z, 0.99, min_p=7.0)[0] == 1
+    assert (ref.sample_ref(z, min_p=1.0)[1] == [0, 0.5, 0.5, 0]).all()
+    assert (ref.sample_ref(z, min_p=float("inf"))[1] == [0, 1, 0, 0]).all()

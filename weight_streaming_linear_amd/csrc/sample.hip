@@ -106,7 +106,7 @@ struct SampleArgs {
 // A row's settings.
 struct How {
     double c8;                                 // y = c8 * z
-    double log_min_p;                          // 8 log2(min_p), or -infinity
+    double log_min_p;                          // 8 log2(min_p), or -infinity: off
     float top_p;                               // 1: off
     uint32_t k;                                // vocab: off
     bool greedy;
@@ -117,11 +117,11 @@ __device__ __forceinline__ How how_of(const SampleArgs &a, int64_t r) {
     const float min_p = a.how.d_min_p ? a.how.d_min_p[r] : a.how.min_p;
     const int32_t k = a.how.d_top_k ? a.how.d_top_k[r] : a.how.top_k;
     How h;
-    h.greedy = !(t > 0) || k == 1 || top_p <= 0;
+    h.greedy = !(t > 0) || k == 1 || top_p <= 0 || min_p > 1;                  // (the greatest weight is 1)
     h.c8 = 11.541560327111707 / static_cast<double>(t > 0 ? t : 1.f);          // 8 log2(e) / T
     h.top_p = top_p < 1 ? top_p : 1.f;
     h.k = k <= 0 || k > a.vocab ? static_cast<uint32_t>(a.vocab) : static_cast<uint32_t>(k);
-    h.log_min_p = min_p > 0 ? 8 * log2(static_cast<double>(min_p < 1 ? min_p : 1.f)) : -__builtin_huge_val();
+    h.log_min_p = min_p > 0 ? 8 * log2(static_cast<double>(min_p)) : -__builtin_huge_val();
     return h;
 }
 
