@@ -549,8 +549,8 @@ int kv_pages_trim(const wsl_kv_pages *h_pages, const int32_t *d_lens, uint32_t *
  * For the token at position p and pair i < rot_dim / 2, with the angle p * freqs[i]:
  *   (a, b) -> amplitude * (a cos - b sin, a sin + b cos),
  * a and b the elements i and i + rot_dim / 2 of the head (or, with WSL_ROTARY_INTERLEAVED, 2i and
- * 2i + 1); elements from rot_dim on are copied.  Angles are reduced in 64 bits: cos and sin are right
- * to 2^-24 where |p * freqs[i]| < 2^40, the products and sums are in fp32.
+ * 2i + 1); elements from rot_dim on are copied.  Angles are formed and reduced in two 64-bit numbers
+ * each: cos and sin are right to 2^-24 where |p * freqs[i]| < 2^48, the products and sums are in fp32.
  * d_q, d_k     device [count][ld] of xfmt (WSL_OUT_F32 or WSL_OUT_BF16): n_heads (n_kv) * head_dim elements a
  *              token; 16-byte aligned, ld a multiple of 16 bytes (views of a fused projection serve).
  *              d_k may be NULL (then d_k_out is ignored).

@@ -122,6 +122,38 @@ def rotary_bound(x, ref, parts, positions, freqs, interleaved, amplitude, bf16):
     return bound + (HALF_BF16 * (np.abs(ref) + bound) if bf16 else 0)
 
 
+def _two_pi(bits):
+    """2 pi * 2^bits, cut off: pi = 16 atan(1/5) - 4 atan(1/239) (Machin), in whole numbers."""
+    guard = 32
+
+    def atan_inverse(n):
+        term = (1 << (bits + guard)) // n
+        total, k, sign = term, 1, -1
+        while term:
+            term //= n * n
+            k += 2
+            total += sign * (term // k)
+            sign = -sign
+        return total
+
+    return 2 * (16 * atan_inverse(5) - 4 * atan_inverse(239)) >> guard
+
+
+def turn_ref(positions, freqs):
+    """(cos, sin) of position * frequency, [len(positions)][len(freqs)]: the product of the two as whole
+    numbers and the angle left of whole turns of it, so that nothing is lost at any size (to 2^-52)."""
+    bits = 320
+    turn = _two_pi(bits)
+    out = np.empty((2, len(positions), len(freqs)))
+    for i, p in enumerate(positions):
+        for j, f in enumerate(freqs):
+            num, den = float(f).as_integer_ratio()
+            angle = ((int(p) * num) << bits) // den % turn
+            angle = math.ldexp(angle - turn if 2 * angle > turn else angle, -bits)
+            out[:, i, j] = math.cos(angle), math.sin(angle)
+    return out[0], out[1]
+
+
 def sample_ref(z, u=None, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     """(token, probabilities) of one row of logits (float64 values of its type); settings are floats
     that fp32 holds."""

@@ -1,11 +1,11 @@
 // Rotary positions (rotary_embed) for gfx950.
 //
 // For the token at position p and pair i, the angle is p * f_i radians.  Far positions lose it in
-// binary32 (p = 10^6 leaves 2^-4 of a radian), so it is formed in 64 bits and brought to
-// turns with 1 / 2 pi as the sum of two doubles:
-//     t = p f,  r = frac(t / 2 pi) = (h - rint(h)) + l,   h + l = t * (C1 + C2),
-// then to the nearest quarter turn: |angle| <= pi / 4, sin and cos by their Taylor series (to x^11 and
-// x^12: below 2^-33), rounded once to binary32.
+// binary32 (p = 10^6 leaves 2^-4 of a radian) and, rounded, in 64 bits too (2^-24 at 2^29), so the product is kept as
+// the sum of two doubles, and brought to turns with 1 / 2 pi as two more:
+//     t + t' = p f,  r = frac((t + t') / 2 pi) = (h - rint(h)) + l,   h + l = t * (C1 + C2) + t' * C1,
+// (off by 2^-50 while |p f| < 2^52), then to the nearest quarter turn: |angle| <= pi / 4, sin and cos by their Taylor series
+// (to x^11 and x^12: below 2^-33), rounded once to binary32.
 //
 // Bound: the heads' bytes in and out once.  One workgroup a token: its first waves make the rot_dim / 2
 // pairs of cos and sin once for all heads, in LDS.  Measured: 2.6 us for one token of 40 and 8 heads of 128 (the launch), 35.3 for
@@ -29,11 +29,16 @@ struct RotaryArgs {
     uint32_t heads, kv_heads, head_dim, half;      // half: rot_dim / 2
 };
 
-__device__ __forceinline__ float2 cos_sin(double angle, double amplitude) {
+__device__ __forceinline__ float2 cos_sin(int64_t position, double freq, double amplitude) {
     constexpr double kTurns = 0.15915494309189535, kTurnsLow = -9.839338337591243e-18;   // 1 / 2 pi
     constexpr double kTau = 6.283185307179586;
+    // the position's halves are doubles; what their sum loses (from 2^53 on) is the rest
+    const double upper = static_cast<double>(static_cast<int32_t>(position >> 32)) * 4294967296.0;
+    const double lower = static_cast<double>(static_cast<uint32_t>(position));
+    const double p = upper + lower, rest = lower - (p - upper);
+    const double angle = p * freq, more = __builtin_fma(p, freq, -angle) + rest * freq;
     const double h = angle * kTurns;
-    const double l = __builtin_fma(angle, kTurns, -h) + angle * kTurnsLow;
+    const double l = __builtin_fma(angle, kTurns, -h) + (angle * kTurnsLow + more * kTurns);
     const double r = (h - __builtin_rint(h)) + l;      // about -0.5 .. 0.5 turns
     const double quarter = __builtin_rint(4 * r);
     const double x = (r - 0.25 * quarter) * kTau, y = x * x;
@@ -104,7 +109,7 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a) {
     const uint32_t rest = LAYOUT == kHalves ? (a.head_dim - 2 * a.half) / 8 : (LAYOUT == kPairs ? 0 : a.head_dim - 2 * a.half);
     const uint32_t tasks = turned + rest, n = (a.heads + a.kv_heads) * tasks;
     for (int64_t t = blockIdx.x; t < a.count; t += gridDim.x) {
-        if (tid < a.half) cs[tid] = cos_sin(static_cast<double>(a.positions[t]) * a.freqs[tid], a.amplitude);
+        if (tid < a.half) cs[tid] = cos_sin(a.positions[t], a.freqs[tid], a.amplitude);
         __syncthreads();
         for (uint32_t i = tid; i < n; i += kThreads) {
             const uint32_t h = i / tasks, e = i - h * tasks;
