@@ -44,3 +44,17 @@ def test_turns_of_positions_that_differ_by_one():
     cos, sin = ref.turn_ref(positions, freqs)
     for h in range(2):
         assert np.abs(y[:, h, :2] - cos).max() <= 2.0 ** -25 + 2.0 ** -32 and np.abs(y[:, h, 2:4] - sin).max() <= 2.0 ** -25 + 2.0 ** -32
+
+
+def test_positions_of_another_shape():
+    """Flat positions of [n_seq][q_len] tokens are theirs in order; transposed ones are refused, not misread."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    q, freqs = torch.randn((3, 5, 4, 64), generator=gen, device="cuda"), wsl.rotary_freqs(64)
+    at = torch.randint(0, 1000, (3, 5), generator=gen, device="cuda")
+    want = wsl.rotary_embed(q, at, freqs)
+    assert wsl.rotary_embed(q, at.view(-1), freqs).equal(want)
+    assert wsl.rotary_embed(q.flatten(0, 1), at, freqs).equal(want.flatten(0, 1))
+    for bad in (at.t().contiguous(), at[:2], at.view(-1)[:14], at[..., None], at.t(), at.int()):
+        with pytest.raises(ValueError, match="positions"):
+            wsl.rotary_embed(q, bad, freqs)

@@ -16,3 +16,14 @@ def test_min_p_above_every_weight():
     assert (ref.sample_ref(z, min_p=7.0)[1] == [0, 1, 0, 0]).all() and ref.sample_ref(z, 0.99, min_p=7.0)[0] == 1
     assert (ref.sample_ref(z, min_p=1.0)[1] == [0, 0.5, 0.5, 0]).all()
     assert (ref.sample_ref(z, min_p=float("inf"))[1] == [0, 1, 0, 0]).all()
+
+
+def test_positions_are_in_the_order_of_their_tokens():
+    """[n_seq][q_len] tokens take positions of that shape, or all in one row; as many in another order are refused."""
+    size = torch.Size
+    for shape, tokens in (((6,), (2, 3)), ((6,), (6,)), ((2, 3), (6,)), ((0,), (0, 3)), ((0, 4), (0,))):
+        wsl._one_each(size(shape), size(tokens), math.prod(tokens))
+    for shape, tokens in (((3, 2), (2, 3)), ((2, 3, 1), (2, 3)), ((1, 6), (2, 3)), ((5,), (2, 3)), ((7,), (6,)), ((2, 4), (6,)), ((), (6,)),
+                          ((1, 2, 3), (6,)), ((2, 2), (2, 3)), ((), (1,))):
+        with pytest.raises(ValueError, match="positions: shape"):
+            wsl._one_each(size(shape), size(tokens), math.prod(tokens))

@@ -960,13 +960,20 @@ def rotary_freqs(rot_dim, base=10000.0, scaling=None, factor=1.0, trained=8192, 
     return torch.tensor(freqs, dtype=torch.float64, device=device)
 
 
+def _one_each(shape, tokens, count):
+    """Check a shape of positions that is not the tokens' own: [count], or of tokens [count] also [n_seq][q_len]."""
+    if shape == (count,) or (len(tokens) == 1 and len(shape) == 2 and shape.numel() == count):
+        return
+    raise ValueError(f"positions: shape {tuple(shape)}, expected {tuple(tokens)}" + (f" or ({count},)" if len(tokens) > 1 else ""))
+
+
 def rotary_embed(q, positions, freqs, k=None, interleaved=False, amplitude=1.0, out=None, k_out=None, ofmt=None,
                  stream=None):
     """Turn pairs of elements of q (and k) by their token's position times freqs; returns out, or
     (out, k_out) with a k.
 
     q, k: [count][heads][head_dim] or [n_seq][q_len][heads][head_dim] (views of a fused projection
-    serve), fp32 or bf16; positions: int64 [count] or [n_seq][q_len]; freqs: float64 [rot_dim / 2]
+    serve), fp32 or bf16; positions: int64 [count] or [n_seq][q_len], in the order of the tokens; freqs: float64 [rot_dim / 2]
     (rotary_freqs), the rest of a head is copied; interleaved: pairs lie side by side instead of half
     a rotation apart; amplitude: a factor of the turned elements; out, k_out may be q and k."""
     if _torch is None:
@@ -980,10 +987,10 @@ def rotary_embed(q, positions, freqs, k=None, interleaved=False, amplitude=1.0, 
         raise ValueError(f"q: expected 3 or 4 dimensions, got shape {tuple(shape)}")
     xfmt = _format_of(q, "q")
     ld_q = heads * dim if q.is_contiguous() else _head_rows(q, "q", q.device, tuple(shape))
-    if positions.dtype is not _i64 or positions.get_device() != index or positions.numel() != count or \
-            not positions.is_contiguous():
+    if positions.dtype is not _i64 or positions.get_device() != index or not positions.is_contiguous():
         _require(positions, "positions", (_i64,), device=q.device, contiguous=True)
-        raise ValueError(f"positions: shape {tuple(positions.shape)}, {count} tokens")
+    if positions.shape != shape[:-2]:
+        _one_each(positions.shape, shape[:-2], count)
     if freqs.dtype is not _torch.float64 or freqs.get_device() != index or freqs.dim() != 1 or not freqs.is_contiguous():
         _require(freqs, "freqs", (_torch.float64,), device=q.device, contiguous=True, ndim=1)
     if ofmt is None:
