@@ -283,9 +283,10 @@ __global__ __launch_bounds__(WAVES * 64) void shrink_many_kernel(LoraArgs a) {
     }
 }
 
-// x = hi + mid + lo, each a bf16 number: part p of it.
+// x = hi + mid + lo, each a bf16 number: part p of it.  hi is cut off: rounded, the finite numbers next to the largest
+// would become infinite.  (A NaN is a quiet one here, its mark in the upper half.)
 __device__ __forceinline__ float third(float x, int p) {
-    const float hi = bf16_lo(pack_bf16x2(x, x));
+    const float hi = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, x) & 0xffff0000u);
     if (p == 0) return hi;
     if (!(__builtin_fabsf(hi) < __builtin_huge_valf())) return 0.f;        // infinite: hi alone
     const float rest = x - hi, mid = bf16_lo(pack_bf16x2(rest, rest));
