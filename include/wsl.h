@@ -591,7 +591,8 @@ typedef struct wsl_sampling {
  *   sum of the kept w_0 .. w_j > u * (sum of all kept), or the last kept where none is (u >= 1 or NaN),
  * and probs_j = w_j / (sum of all kept), 0 for the rest.  Where temperature is not above 0 the first
  * entry alone is kept.  A NaN in top_p or min_p counts as off.  Weights and their sums are right to 2^-32,
- * exact where all weights are equal; decisions are made in 64 bits.
+ * exact where all weights are equal; decisions are made in 64 bits.  The same call gives the same bits; with other
+ * rows beside it a long row may be cut elsewhere, and a decision as near to its border as 2^-32 fall the other way.
  * Entries of -infinity are out.  A row that holds a NaN or +infinity, or nothing but -infinity, gives
  * token -1, probabilities 0, and WSL_STATUS_NONFINITE.
  * d_logits   device [n_rows][ld] of zfmt (WSL_OUT_F32 or WSL_OUT_BF16), the first vocab of each row used;

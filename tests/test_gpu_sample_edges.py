@@ -1,4 +1,4 @@
-"""sample_logits where its definition is easily missed: thresholds above every weight."""
+"""sample_logits where its definition is easily missed: thresholds above every weight, rows cut in other ways."""
 
 import numpy as np
 import pytest
@@ -35,3 +35,28 @@ def test_min_p_above_one_keeps_the_first_alone(vocab, dtype):
     assert (probs > 0).sum(1).tolist() == [9, 1] * 4
     for i in range(n):
         assert (ref.sample_ref(f32_of(z[i]), min_p=float(mixed[i]))[1] > 0).tolist() == (probs[i] > 0).tolist()
+
+
+@pytest.mark.parametrize("n,vocab", [(300, 3900), (300, 8000), (200, 32001), (520, 9000), (300, 131072), (70, 100003)])
+def test_a_rows_token_does_not_depend_on_the_rows_beside_it(n, vocab):
+    """Among many rows parts are longer, or waves fewer; sums agree to 2^-32, and so a u in the middle of an entry's share
+    of 2^-20 or more (rounded to fp32: 2^-25) gives that entry, alone and among the others."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(vocab + n)
+    z = 2.5 * torch.randn((n, vocab), generator=gen, device="cuda")
+    how = dict(top_k=400, top_p=0.93, temperature=0.8)
+    rows = [0, 1, n // 3, n // 2, n - 1]
+    u = torch.rand(n, generator=gen, device="cuda")
+    want = {}
+    for r in rows:
+        probs = ref.sample_ref(f32_of(z[r]), **{x: float(np.float32(v)) if x != "top_k" else v for x, v in how.items()})[1]
+        up = np.cumsum(probs)
+        at = int(np.searchsorted(up, u[r].item(), side="right"))
+        if at >= vocab or probs[at] < 2.0 ** -20:
+            at = int(probs.argmax())
+        u[r], want[r] = float(up[at] - probs[at] / 2), at
+    tokens = wsl.sample_logits(z, u, **how)
+    for r in rows:
+        alone = wsl.sample_logits(z[r:r + 1], u[r:r + 1], **how)
+        assert alone.item() == tokens[r].item() == want[r]
+    assert wsl.sample_logits(z, u, **how).equal(tokens)
