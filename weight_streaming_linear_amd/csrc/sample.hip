@@ -738,18 +738,19 @@ template <bool FEW>
 struct PartCells;
 template <>
 struct PartCells<true> {
-    uint64_t raw[kFewParts];
+    static constexpr int kThreads = kWaves * 64, kMine = kFewParts * kCells / kThreads;
+    uint64_t raw[kMine];
     __device__ __forceinline__ void take(const uint64_t *from, int parts) {
 #pragma unroll
-        for (int i = 0; i < kFewParts; ++i) {
-            const uint32_t at = i * blockDim.x + threadIdx.x;
+        for (int i = 0; i < kMine; ++i) {
+            const uint32_t at = i * kThreads + threadIdx.x;
             raw[i] = at < static_cast<uint32_t>(parts) * kCells ? from[at] : 0;
         }
     }
     __device__ __forceinline__ void put(uint64_t *lds, int parts) const {
 #pragma unroll
-        for (int i = 0; i < kFewParts; ++i) {
-            const uint32_t at = i * blockDim.x + threadIdx.x;
+        for (int i = 0; i < kMine; ++i) {
+            const uint32_t at = i * kThreads + threadIdx.x;
             if (at < static_cast<uint32_t>(parts) * kCells) lds[at] = raw[i];
         }
     }
