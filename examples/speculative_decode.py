@@ -83,6 +83,7 @@ class Decoder:
         for layer, cache in zip(self.layers, self.caches):
             x = self.linear(layer["qkv"], self.norm(h), layer.get("qkv_lora"))
             q, k, v = (y.unflatten(-1, (-1, self.dim)) for y in x.split((q_heads, kv, kv), 1))
+            # (two calls, since k stays in fp32: the cache rounds it once, to its own type)
             q = wsl.rotary_embed(q, at, self.freqs, ofmt=wsl.WSL_OUT_BF16)
             k = wsl.rotary_embed(k, at, self.freqs, out=k)
             wsl.kv_cache_write(cache, k, v, slots)

@@ -8,29 +8,33 @@
 // tokens share theirs).  There h goes in as three bf16 numbers (hi + mid + lo, 24 bits): its
 // rounding to one would be the largest error of the result.
 //
-// Bound: base and out once each, x, and A and B of the adapters in use.  Measured, launches behind one another: one token,
-// 5120 to 5120, rank 16, 6.2 us (3 and 3; half of it is the launches); 48 tokens of 7168 to 5120, 24 adapters, 7.7;
-// 4224 tokens of 6144 to 5120, 21 adapters, 49 (225 MB of x, base and out: 4.6 TB/s): 14.5 for h and 34.6 for out (173 MB: 5.0 TB/s); rank 64, 75.
+// Bound: base and out once each, x, and A and B of the adapters in use.  Measured, launches behind one another in a graph (as all
+// figures here, fp32 and on inputs that the caches may hold): one token, 5120 to 5120, rank 16, 6.1 us (3 and 3; half of it is the
+// launches); 48 tokens of 7168 to 5120, 24 adapters, 7.5; 4224 tokens of 6144 to 5120, 21 adapters, 50.2 (225 MB of x, base and
+// out: 4.5 TB/s); rank 64, 78.5.  Rows of base and out that are not 16-byte aligned go an element at a time: 4224 tokens
+// of 6144, 12 adapters, to 6144 outputs 52.5, to 6145 148; in bf16 37.5 and 157.
 #include "device_common.h"
 
 namespace wsl {
 namespace {
 
-// Tokens one by one up to here.  That costs the same whatever their adapters; tiles of 16 cost by the adapters among
-// them.  5120 to 5120, one against the other, in us: tokens with adapters of their own, rank 16: 9 and 44 for 128, 21 and
-// 46 for 512, 36 and 62 for 1024; requests of 200 tokens: 9 and 10, 19.5 and 13.6, 35 and 20.  Rank 64: 24 and 91 for 128, 38 and
-// 90 for 256; requests: 23 and 14, 36 and 15.
+// Tokens one by one up to here.  That costs by the tokens, and adapters that caches do not hold; tiles of 16 cost by the adapters among
+// them, which the host does not know.  5120 to 5120, one against the other, in us: tokens with an adapter each, rank 16: 14 and
+// 44 for 128, 34 and 51 for 512, 85 and 107 for 1024; requests of 200 tokens: 8.8 and 10.2, 20.3 and 14.1, 36 and 20.  Rank 64: 41.5
+// and 94.5 for 128, 82 and 148 for 256; requests: 23.4 and 14.3, 38.5 and 17.7.  So next to the border either side loses up to twice for
+// some ids.
 constexpr int64_t kFewRows = 8192;         // m * rank
 bool few(int64_t m, int64_t rank) { return m * rank <= kFewRows; }
-// Least elements of k in a part; more only add partial sums to write and read.  512 against 1024, in us: 48 tokens, 7168 to
-// 5120, rank 16: 9.0 and 7.6; 128 tokens of 5120: 15.1 and 13.5; 256 tokens, rank 64: 37.7 and 33.0.
+// Least elements of k in a part; more only add partial sums to write and read.  512 against 1024, in us: one token of 5120, rank 16:
+// 6.4 and 6.1; 48 tokens of 7168: 8.9 and 7.5; 128 of 5120: 15.3 and 14.0; 1024 in requests: 20.1 and 20.1; but 256 with 128 adapters,
+// rank 64: 91 and 97.
 constexpr int kPart = 1024;
-// Parts at most: 8, 16 and 32 are as good (one token, 14336 to 5120, rank 64: 13.3, 12.6 and 14.4).
+// Parts at most.  8, 16 and 32, 14336 to 5120, rank 64: one token 13.0, 12.7 and 12.7; 8 tokens 11.9, 10.5 and 10.5.
 constexpr int64_t kMostParts = 16;
-// Workgroups of 16 tokens that keep the chip busy: one a CU.  128, 256 and 512: 600 tokens, 5120 to 5120, rank 16: 15.4, 14.9 and
-// 14.9; 2048: 29.7, 28.6 and 30.3; 1024 of 14336, rank 64: 42, 37 and 40.
+// Workgroups of 16 tokens that keep the chip busy: one a CU.  128, 256 and 512: 600 tokens, 5120 to 5120, rank 16: 15.3, 14.8 and
+// 14.9; 2048: 30.0, 29.1 and 30.3; 1024 of 14336, rank 64: 42.9, 37.4 and 40.5.
 constexpr int64_t kGroups = 256;
-constexpr int kXcds = 8;
+constexpr int kXcds = 8;                   // (another number costs locality alone)
 constexpr int64_t kMostTiles = 32768;      // of 16 tokens along a grid's y, which ends at 65535
 
 struct LoraArgs {
@@ -171,8 +175,8 @@ struct Turn {
     }
 };
 
-// A workgroup: 16 tokens and a part of k, those of an XCD in turn so that its L2 holds what they have of A (61.8 -> 60.0 us, the
-// whole, 4224 tokens of 6144, rank 16).  The tokens
+// A workgroup: 16 tokens and a part of k, those of an XCD in turn so that its L2 holds what they have of A (4224 tokens of 6144, 21
+// adapters, rank 16, 55.3 -> 50.2 us, the whole; rank 64, 96 -> 78.5).  The tokens
 // are the rows, 16 rows of A the columns; the waves take 128 elements of k in turn, all of their loads made
 // before the first product, and are added up in LDS, so that one part is enough where tokens are many.
 template <int BLOCKS, int WAVES>
@@ -294,13 +298,14 @@ __device__ __forceinline__ float third(float x, int p) {
 }
 
 // blockIdx: (outputs, 16 tokens): what runs together covers whole rows of base and out, and the parts of h are made
-// once for the four waves (a wave 16 tokens of its own: 1024 tokens, 5120 outputs, rank 64, 31.4 -> 21.7 us).  The products run over
+// once for the four waves (before, a wave had 16 tokens of its own: 1024 tokens, 5120 outputs, rank 64, 31.4 -> 21.7 us).  The products run over
 // (part of h, rank), 32 at a time.  Rows: 16 outputs, columns: a wave's 16 tokens; the outputs of four products are
 // shuffled so that a lane ends up with 16 successive bytes of its token's row for each access, the four lanes of a token
 // with 64.  A wave has kTiles * 64 outputs, whose base it asks for before it knows its adapters: waiting for those, and
 // for h, would otherwise take as long as the rest.  (B asked for as early takes registers for it, and half the
-// waves.)  kTiles 1, 2 and 4, the whole call: 1024 tokens, 5120 to 5120, rank 16: 20.6, 21.9 and 24.9 us; 4224 of 6144: 59.6, 58.3
-// and 60.9, rank 64: 112, 109 and 114.  The rows
+// waves.)  kTiles 1, 2 and 4, the whole call, to 5120, rank 16: 1024 tokens of 5120: 18.8, 20.0 and 23.3 us, 2048: 29.1, 29.2 and
+// 28.6, 8192: 98.4, 95.5 and 99.6; 4224 of 6144: 51.4, 50.2 and 52.9; rank 64: 31.6, 29.8 and 34.4 for 1024, 78.2, 78.5 and 86.9 for
+// 4224.  The rows
 // of B that go with the three parts of h are the same: PERIOD of them are different (STEPS where the rank neither divides
 // 32 nor is a multiple of it).
 constexpr int kTiles = 2;

@@ -8,8 +8,8 @@
 // own slot without looking at another.
 //
 // Bound: latency, of one workgroup's loads one after the other; the bytes (16 to 20 a token) are nothing.
-// Measured: grow 3 us for one sequence, 6.6 for 256 of 5 tokens; 4.3 and 4.6 in two launches for
-// 64 prompts of 166,500 tokens together; trim 4.3 to 6.9.
+// Measured: grow 3.2 us for one sequence, 6.8 for 256 of 5 tokens; 4.6 and 4.5 in two launches for
+// 64 prompts of 166,500 tokens together; trim of the same 4.7, 5.3 and 11.7.
 #include "device_common.h"
 
 namespace wsl {

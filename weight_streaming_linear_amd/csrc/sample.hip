@@ -22,8 +22,11 @@
 // code once, so what bounds it besides the loads is how fast instructions come in: loops over LDS are
 // kept rolled.
 //
-// Measured, top-k and top-p of each row's own: 64 rows of 151937 fp32 entries (38.9 MB, 7.6 us as a copy) 52 us: cells 16.5, border
-// 15.4, pick 20; one row of 32000, 25.5: 6.2, 8.9 and 11.4; 40 bf16 rows of 32000 with their probabilities 40: 6.9, 9.5, 16 and 7.7.
+// Measured, top-k and top-p of each row's own: 64 rows of 151937 fp32 entries (38.9 MB, 7.6 us as a copy) 51 us: cells 16.1, border
+// 15.1, pick 19.8; one row of 32000, 25: 6.4, 8.4 and 10.8; 40 bf16 rows of 32000 with their probabilities 41: 7.2, 9.5, 16.4 and 8.
+// Rows so flat that a border's cells hold more than kHeld entries have no list: one workgroup goes through the row in memory for each
+// step, and time grows with the row.  Top-p 0.9 of 64 rows of 151937 normal logits of spread 0.5: 530 us, of 2.5: 64; of equal ones 980;
+// one row of 2^22 of spread 2.5: 14 ms.
 #include "row_scan.h"
 
 namespace wsl {
@@ -33,15 +36,15 @@ constexpr int kCells = 256, kList = 256;
 constexpr int kWaves = 8, kPartSegs = 16;      // waves of a workgroup, and segments of a part, at most
 constexpr int kMostParts = 256, kFewParts = 16;
 constexpr int kHeld = 8192;                    // orders that a workgroup holds: a short row, or a long one's list
-// Entries of a short row, at most.  Against long rows' launches, in us (top-k 50 and top-p 0.9, as all figures here): 8192
-// entries, 1, 64 and 512 rows: 20, 22 and 44, the others 24, 26 and 51.
+// Entries of a short row, at most.  Against long rows' launches, in us (top-k 50 and top-p 0.9 in a graph, as all figures here): 8192
+// entries, 1, 64 and 512 rows: 18, 18.4 and 35, the others 24, 26 and 43.5.
 constexpr int kChunk = kHeld;
-// Short rows of up to 4096 entries beyond which four waves take one instead of eight, so that all have room.  Eight and four,
-// 4000 entries: 15 and 18 for 1 row, 16.6 and 19.2 for 256, 31 and 22 for 512, 58 and 42 for 1024.
+// Short rows of up to 4096 entries beyond which four waves take one, with a segment each, instead of eight.  (LDS has room for two rows
+// a CU either way.)  Eight and four, 4000 entries: 14.5 and 17.3 for 1 row, 15.5 and 18.5 for 256, 28 and 20 for 512, 55 and 39 for 1024.
 constexpr int64_t kManyRows = 256;
 // Parts of all rows up to which a part is 8 segments and not 16.  8 and 16: 32000 entries, 1, 64, 128 and 256 rows (1024 parts):
-// 25.5 and 30.6, 28 and 33, 32.6 and 35.4, 49 and 45; 65536, 64 rows (512) and 128: 33.5 and 34.7, 50 and 44; 131072, 1, 32
-// (512) and 64: 28 and 31, 35.9 and 36.5, 54 and 45.7.
+// 24.7 and 29.6, 27 and 32, 31.3 and 33.7, 46.3 and 43.7; 65536, 64 rows (512) and 128: 31.5 and 33.8, 46 and 41; 131072, 1, 32
+// (512) and 64: 27 and 30.3, 34.7 and 35.5, 49 and 43.8.
 constexpr int64_t kFill = 512;
 constexpr double kPartUnit = 4294967296.0;     // 2^32: whole numbers to a cell's unit; 2^14 entries of it fit 48 bits
 constexpr float kInf = __builtin_huge_valf();
