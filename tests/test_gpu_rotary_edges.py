@@ -55,6 +55,7 @@ def test_positions_of_another_shape():
     want = wsl.rotary_embed(q, at, freqs)
     assert wsl.rotary_embed(q, at.view(-1), freqs).equal(want)
     assert wsl.rotary_embed(q.flatten(0, 1), at, freqs).equal(want.flatten(0, 1))
-    for bad in (at.t().contiguous(), at[:2], at.view(-1)[:14], at[..., None], at.t(), at.int()):
+    assert wsl.rotary_embed(q, at[..., None], freqs).equal(want)
+    for bad in (at.t().contiguous(), at[:2], at.view(-1)[:14], at.t(), at.int()):
         with pytest.raises(ValueError, match="positions"):
             wsl.rotary_embed(q, bad, freqs)

@@ -19,11 +19,13 @@ def test_min_p_above_every_weight():
 
 
 def test_positions_are_in_the_order_of_their_tokens():
-    """[n_seq][q_len] tokens take positions of that shape, or all in one row; as many in another order are refused."""
+    """[n_seq][q_len] tokens take positions of that shape, or all in one row; as many in another order are refused.
+    Dimensions of one change no order."""
     size = torch.Size
-    for shape, tokens in (((6,), (2, 3)), ((6,), (6,)), ((2, 3), (6,)), ((0,), (0, 3)), ((0, 4), (0,))):
+    for shape, tokens in (((6,), (2, 3)), ((6,), (6,)), ((2, 3), (6,)), ((0,), (0, 3)), ((0, 4), (0,)), ((1, 6), (2, 3)), ((2, 3, 1), (2, 3)),
+                          ((), (1,)), ((6, 1), (1, 6)), ((1, 2, 3), (6,)), ((3, 0), (0, 3))):
         wsl._one_each(size(shape), size(tokens), math.prod(tokens))
-    for shape, tokens in (((3, 2), (2, 3)), ((2, 3, 1), (2, 3)), ((1, 6), (2, 3)), ((5,), (2, 3)), ((7,), (6,)), ((2, 4), (6,)), ((), (6,)),
-                          ((1, 2, 3), (6,)), ((2, 2), (2, 3)), ((), (1,))):
+    for shape, tokens in (((3, 2), (2, 3)), ((3, 1, 2), (2, 3)), ((6, 2), (3, 4)), ((5,), (2, 3)), ((7,), (6,)), ((2, 4), (6,)), ((), (6,)),
+                          ((2, 2), (2, 3)), ((2, 3), (1, 5))):
         with pytest.raises(ValueError, match="positions: shape"):
             wsl._one_each(size(shape), size(tokens), math.prod(tokens))

@@ -961,10 +961,11 @@ def rotary_freqs(rot_dim, base=10000.0, scaling=None, factor=1.0, trained=8192, 
 
 
 def _one_each(shape, tokens, count):
-    """Check a shape of positions that is not the tokens' own: [count], or of tokens [count] also [n_seq][q_len]."""
-    if shape == (count,) or (len(tokens) == 1 and len(shape) == 2 and shape.numel() == count):
-        return
-    raise ValueError(f"positions: shape {tuple(shape)}, expected {tuple(tokens)}" + (f" or ({count},)" if len(tokens) > 1 else ""))
+    """Check a shape of positions that is not the tokens' own: as many, and, of tokens [n_seq][q_len], in one row or in that
+    shape (but for dimensions of one), so that they are in the tokens' order."""
+    apart = tuple(n for n in shape if n != 1)
+    if shape.numel() != count or (count and len(tokens) > 1 and len(apart) > 1 and apart != tuple(n for n in tokens if n != 1)):
+        raise ValueError(f"positions: shape {tuple(shape)}, expected {tuple(tokens)}" + (f" or ({count},)" if len(tokens) > 1 else ""))
 
 
 def rotary_embed(q, positions, freqs, k=None, interleaved=False, amplitude=1.0, out=None, k_out=None, ofmt=None,
